@@ -34,3 +34,12 @@ from .qref import (  # noqa: F401
     prefill_attention_f16_inputs_f64,
     prefill_layer_f64,
 )
+from .kv8ref import (  # noqa: F401
+    kv8_append,
+    kv8_attention,
+    kv8_codes,
+    kv8_evict,
+    kv8_read,
+    kv8_scale,
+    kv8_values,
+)

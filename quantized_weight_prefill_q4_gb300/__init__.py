@@ -3,8 +3,9 @@
 ``Y = X . dequant(W)^T (+ R)``, ``silu(X . Wg^T) * (X . Wu^T)`` and the small-T
 GEMV, computed by the hand-written CUDA kernels of ``libapr_qgemm.so``
 (C ABI: ``include/apr_qgemm.h``). The names below come from the binding
-module :mod:`quantized_weight_prefill_q4_gb300.capi`, loaded on first use so
-that :mod:`quantized_weight_prefill_q4_gb300.build` can run before the library
+modules :mod:`quantized_weight_prefill_q4_gb300.capi` and, for the 8-bit KV
+cache of the decode steps (``include/apr_kv8.h``),
+:mod:`quantized_weight_prefill_q4_gb300.kv8`, loaded on first use so that :mod:`quantized_weight_prefill_q4_gb300.build` can run before the library
 exists; using any of them without the built library raises ``ImportError``.
 """
 
@@ -15,8 +16,8 @@ import importlib
 def __getattr__(name):
     if name.startswith("__"):
         raise AttributeError(name)
-    capi = importlib.import_module(__name__ + ".capi")
+    module = ".kv8" if name.startswith(("apr_kv8_", "Kv8", "KV8_", "APR_T_")) else ".capi"
     try:
-        return getattr(capi, name)
+        return getattr(importlib.import_module(__name__ + module), name)
     except AttributeError:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}") from None

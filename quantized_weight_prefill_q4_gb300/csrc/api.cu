@@ -18,6 +18,7 @@
 
 #include "apr_qgemm.h"
 #include "apr_internal.h"
+#include "dev_common.cuh"
 
 using namespace apr;
 
@@ -99,7 +100,8 @@ enum ScratchUse {
   kScratchNorm = 3,
   kScratchAttn = 4,
   kScratchLayer = 5,
-  kScratchExact = 6
+  kScratchExact = 6,
+  kScratchKv8 = 7
 };
 struct StreamScratch {
   int dev;
@@ -578,6 +580,19 @@ int check_gemm_args(int qtype, const void* W, int n, int k, const float* X, int 
   return check(Problem{qtype, APR_LEG_F16, APR_PATH_GEMM, W, nullptr, n, k, T, X, R, const_cast<float*>(Y), nullptr});
 }
 
+int device_status_word(unsigned** status) {
+  DeviceState* st = nullptr;
+  const int rc = device_state(&st);
+  if (rc == APR_OK) *status = st->status;
+  return rc;
+}
+
+int kv8_scratch(cudaStream_t s, size_t bytes, void** out) {
+  DeviceState* st = nullptr;
+  const int rc = device_state(&st);
+  return rc == APR_OK ? stream_scratch(st->dev, s, kScratchKv8, bytes, out) : rc;
+}
+
 unsigned* status_word_address() {
   void* p = nullptr;
   if (cudaGetSymbolAddress(&p, g_status) != cudaSuccess) {
@@ -765,7 +780,10 @@ int apr_stream_status(apr_stream_t stream) {
   if (v) {
     const unsigned zero = 0;
     cudaMemcpy(st->status, &zero, sizeof zero, cudaMemcpyHostToDevice);
-    scratch_mark_dirty(st->dev);
+    if (v & kStatusTimeout) scratch_mark_dirty(st->dev);
+    if (!(v & kStatusTimeout))
+      return fail(APR_E_INVAL, "a page id, a length or a row range of an 8-bit cache call was out of range (status 0x%x)",
+                  v);
     return fail(APR_E_TIMEOUT, "a kernel's bounded wait gave up (status 0x%x)", v);
   }
   return APR_OK;

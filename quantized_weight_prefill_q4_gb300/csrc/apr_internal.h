@@ -177,4 +177,34 @@ int set_error(int code, const char* msg);
 int check_gemm_args(int qtype, const void* W, int n, int k, const float* X, int T, const float* Y, const float* R);
 unsigned* status_word_address();
 
+// Shared with the 8-bit cache's entry points (kv8_api.cu): checks the current
+// device and gives its status word; the stream's scratch buffer of those
+// calls (both set this thread's error message where they fail).
+int device_status_word(unsigned** status);
+int kv8_scratch(cudaStream_t s, size_t bytes, void** out);
+
+// The 8-bit paged KV cache (kv8_append.cu, kv8_attention.cu, kv8_evict.cu):
+// include/apr_kv8.h says what each computes; kv8_api.cu has checked the
+// arguments. All are launched programmatically and wait for the work ahead
+// before they touch memory. The attention's scratch: kv8_attention_scratch.
+struct Kv8View;
+cudaError_t launch_kv8_append(const Kv8View& v, int type, const void* k, const void* vv, long long ld, cudaStream_t s);
+cudaError_t launch_kv8_read(const Kv8View& v, int type, void* k, void* vv, long long ld, cudaStream_t s);
+struct Kv8Attention {
+  int type;
+  const void* q;
+  void* out;
+  long long ldq, ldo;
+  int heads;
+  float scale;
+  float* weights;  // nullptr: not wanted
+  long long weights_ld;
+  int accumulate;
+};
+size_t kv8_attention_scratch(const Kv8View& v, const Kv8Attention& a);
+cudaError_t launch_kv8_attention(const Kv8View& v, const Kv8Attention& a, void* scratch, cudaStream_t s);
+cudaError_t launch_kv8_evict(const Kv8View& v, const float* weights, long long weights_ld, int budget, int recent,
+                             const int* fresh, int* table_out, int* lens_out, float* weights_out,
+                             long long weights_out_ld, int* kept, cudaStream_t s);
+
 }  // namespace apr

@@ -9,6 +9,7 @@ namespace apr {
 
 // Bits of the per-device status word.
 constexpr unsigned kStatusTimeout = 1u;   // a bounded wait gave up
+constexpr unsigned kStatusBadIndex = 2u;  // a page id, length or row range of the 8-bit cache was out of range
 
 // A bounded wait gives up after this many nanoseconds of %globaltimer.
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s

@@ -1,0 +1,219 @@
+"""ctypes binding of the 8-bit paged KV cache (include/apr_kv8.h), same names.
+
+Like :mod:`.capi` it only marshals: tensors become device pointers, sizes are
+checked against the tensors so that no call can address past an allocation,
+and a nonzero status raises :class:`~.capi.AprError`.
+"""
+
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+
+import torch
+
+from . import capi
+
+APR_T_F32 = 0
+APR_T_F16 = 1
+APR_T_BF16 = 30
+
+# Every symbol include/apr_kv8.h declares.
+KV8_EXPORTS = ("apr_kv8_append", "apr_kv8_read", "apr_kv8_attention", "apr_kv8_evict")
+
+_TYPES = {torch.float32: APR_T_F32, torch.float16: APR_T_F16, torch.bfloat16: APR_T_BF16}
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [
+        ("K", ctypes.c_void_p),
+        ("V", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int),
+        ("num_kv_heads", ctypes.c_int),
+        ("page_tokens", ctypes.c_int),
+        ("head_dim", ctypes.c_int),
+    ]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [
+        ("page_table", ctypes.c_void_p),
+        ("table_ld", ctypes.c_int),
+        ("lens", ctypes.c_void_p),
+        ("row_start", ctypes.c_void_p),
+        ("num_seqs", ctypes.c_int),
+        ("num_rows", ctypes.c_int),
+        ("max_rows", ctypes.c_int),
+        ("max_len", ctypes.c_int),
+    ]
+
+
+def _bind():
+    lib = capi.library()
+    vp, ci, ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
+    cache, rows = ctypes.POINTER(_Cache), ctypes.POINTER(_Rows)
+    sig = {
+        "apr_kv8_append": [cache, rows, ci, vp, vp, ll, vp],
+        "apr_kv8_read": [cache, rows, ci, vp, vp, ll, vp],
+        "apr_kv8_attention": [cache, rows, ci, vp, ll, vp, ll, ci, ctypes.c_float, vp, ll, ci, vp],
+        "apr_kv8_evict": [cache, rows, vp, ll, ci, ci, vp, vp, vp, vp, ll, vp, vp],
+    }
+    for name, args in sig.items():
+        f = getattr(lib, name)
+        f.argtypes = args
+        f.restype = ctypes.c_int
+    return lib
+
+
+_lib = _bind()
+
+
+def _array(x, name, dtype, dims):
+    """A contiguous CUDA tensor of the type and number of dimensions, checked."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name}: expected a CUDA tensor, got {type(x).__name__}")
+    if not x.is_cuda:
+        raise ValueError(f"{name}: tensor is on {x.device}, the library takes device memory")
+    if x.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {x.dtype}")
+    if x.dim() != dims or not x.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor of {dims} dimensions, got shape {tuple(x.shape)}")
+    return x
+
+
+@dataclass
+class Kv8Cache:
+    """The cache's arrays: codes K and V int8 [pages][kv_heads][page_tokens][head_dim],
+    scales k_scale and v_scale float32 [pages][kv_heads], all contiguous."""
+
+    K: torch.Tensor
+    V: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+    def __post_init__(self):
+        K = _array(self.K, "K", torch.int8, 4)
+        _array(self.V, "V", torch.int8, 4)
+        _array(self.k_scale, "k_scale", torch.float32, 2)
+        _array(self.v_scale, "v_scale", torch.float32, 2)
+        if self.V.shape != K.shape or self.k_scale.shape != K.shape[:2] or self.v_scale.shape != K.shape[:2]:
+            raise ValueError("Kv8Cache: V, k_scale and v_scale must match K's pages, heads, tokens and head_dim")
+        pages, heads, tokens, dim = K.shape
+        self._c = _Cache(K.data_ptr(), self.V.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(), pages,
+                         heads, tokens, dim)
+
+    @classmethod
+    def allocate(cls, num_pages, num_kv_heads, head_dim, page_tokens=64, device="cuda"):
+        """A cache of num_pages pages (zeros)."""
+        codes = (num_pages, num_kv_heads, page_tokens, head_dim)
+        return cls(torch.zeros(codes, dtype=torch.int8, device=device),
+                   torch.zeros(codes, dtype=torch.int8, device=device),
+                   torch.zeros(codes[:2], dtype=torch.float32, device=device),
+                   torch.zeros(codes[:2], dtype=torch.float32, device=device))
+
+
+def _rows(page_table, lens, row_start, num_rows, max_rows, max_len):
+    table = _array(page_table, "page_table", torch.int32, 2)
+    n = _array(lens, "lens", torch.int32, 1).numel()
+    if table.shape[0] != n:
+        raise ValueError(f"page_table has {table.shape[0]} rows, lens {n} entries")
+    start = None
+    if row_start is not None:
+        if _array(row_start, "row_start", torch.int32, 1).numel() != n + 1:
+            raise ValueError(f"row_start: expected {n + 1} entries, got {row_start.numel()}")
+        start = row_start.data_ptr()
+    return _Rows(table.data_ptr(), table.shape[1], lens.data_ptr(), start, n, num_rows, max_rows, max_len)
+
+
+def _matrix(x, name, width, like=None):
+    """(pointer, rows, elements from row to row) of rows of `width` elements: a
+    2-D tensor, or a 3-D one of [rows][heads][head_dim], whose rows are dense."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype not in _TYPES:
+        raise ValueError(f"{name}: expected a float32, float16 or bfloat16 CUDA tensor")
+    shape, stride = x.shape, x.stride()
+    dense = (x.dim() == 2 and shape[1] == width and (width == 1 or stride[1] == 1)) or (
+        x.dim() == 3 and shape[1] * shape[2] == width and stride[2] == 1 and (shape[1] == 1 or stride[1] == shape[2]))
+    if not dense:
+        raise ValueError(f"{name}: expected rows of {width} consecutive elements, got shape {tuple(shape)}, "
+                         f"strides {tuple(stride)}")
+    if like is not None and (x.dtype != like.dtype or shape[0] != like.shape[0]):
+        raise ValueError(f"{name}: expected {like.shape[0]} rows of {like.dtype}, got {shape[0]} of {x.dtype}")
+    rows = shape[0]
+    ld = stride[0] if rows > 1 else width
+    return x.data_ptr(), rows, ld
+
+
+def _k_and_v(cache, k, v):
+    width = cache.K.shape[1] * cache.K.shape[3]
+    kp, rows, ld = _matrix(k, "k", width)
+    vp, _, vld = _matrix(v, "v", width, like=k)
+    if vld != ld and rows > 1:
+        raise ValueError(f"k and v must have the same row stride, got {ld} and {vld}")
+    return kp, vp, rows, ld
+
+
+def apr_kv8_append(cache, page_table, lens, k, v, *, row_start=None, max_rows=0, stream=None) -> int:
+    """Quantises the packed rows k and v ([rows][kv_heads * head_dim], strided
+    rows allowed) into the cache, as the last positions of their sequences:
+    lens counts them already. row_start None: one row a sequence."""
+    kp, vp, n, ld = _k_and_v(cache, k, v)
+    rows = _rows(page_table, lens, row_start, n, max_rows, 0)
+    return capi._check(_lib.apr_kv8_append(cache._c, rows, _TYPES[k.dtype], kp, vp, ld, capi._stream(stream)))
+
+
+def apr_kv8_read(cache, page_table, lens, k, v, *, row_start=None, max_rows=0, stream=None) -> int:
+    """Writes the values of each sequence's last rows to k and v (their types
+    and strides as for the append)."""
+    kp, vp, n, ld = _k_and_v(cache, k, v)
+    rows = _rows(page_table, lens, row_start, n, max_rows, 0)
+    return capi._check(_lib.apr_kv8_read(cache._c, rows, _TYPES[k.dtype], kp, vp, ld, capi._stream(stream)))
+
+
+def apr_kv8_attention(cache, page_table, lens, q, out, num_heads, *, row_start=None, max_rows=0, max_len=0, scale=0.0,
+                      weights=None, accumulate=False, stream=None) -> int:
+    """out[row][head] = the causal attention of each sequence's last rows q
+    over its cache, which holds their own k and v; out has q's type. weights
+    ([sequences][kv_heads][>= max_len] float32) receives, or with accumulate
+    adds, the weight of each position. max_len bounds lens (0: the table)."""
+    width = num_heads * cache.K.shape[3]
+    qp, n, ldq = _matrix(q, "q", width)
+    op, _, ldo = _matrix(out, "out", width, like=q)
+    rows = _rows(page_table, lens, row_start, n, max_rows, max_len)
+    wp, wld = None, 0
+    if weights is not None:
+        _array(weights, "weights", torch.float32, 3)
+        if weights.shape[0] != lens.numel() or weights.shape[1] != cache.K.shape[1]:
+            raise ValueError(f"weights: expected [{lens.numel()}][{cache.K.shape[1]}][...], got {tuple(weights.shape)}")
+        wp, wld = weights.data_ptr(), weights.shape[2]
+    return capi._check(_lib.apr_kv8_attention(cache._c, rows, _TYPES[q.dtype], qp, ldq, op, ldo, num_heads, scale, wp,
+                                              wld, int(accumulate), capi._stream(stream)))
+
+
+def apr_kv8_evict(cache, page_table, lens, weights, budget, recent, fresh_pages, table_out, lens_out, weights_out, kept,
+                  *, max_len=0, stream=None) -> int:
+    """Cuts every sequence of more than `budget` positions to its `recent` last
+    and the others of the largest weights, moved into fresh_pages
+    ([sequences][ceil(budget / page_tokens)]); table_out, lens_out, weights_out
+    ([sequences][kv_heads][>= budget]) and kept ([sequences][kv_heads][budget])
+    say what the sequences are afterwards."""
+    heads, tokens = cache.K.shape[1], cache.K.shape[2]
+    rows = _rows(page_table, lens, None, 0, 0, max_len)
+    n = lens.numel()
+    want = {
+        "weights": (weights, torch.float32, (n, heads, None)),
+        "fresh_pages": (fresh_pages, torch.int32, (n, -(-budget // tokens))),
+        "table_out": (table_out, torch.int32, tuple(page_table.shape)),
+        "lens_out": (lens_out, torch.int32, (n,)),
+        "weights_out": (weights_out, torch.float32, (n, heads, None)),
+        "kept": (kept, torch.int32, (n, heads, budget)),
+    }
+    for name, (x, dtype, shape) in want.items():
+        _array(x, name, dtype, len(shape))
+        if any(w is not None and w != h for w, h in zip(shape, x.shape)):
+            raise ValueError(f"{name}: expected shape {shape}, got {tuple(x.shape)}")
+    return capi._check(_lib.apr_kv8_evict(cache._c, rows, weights.data_ptr(), weights.shape[2], budget, recent,
+                                          fresh_pages.data_ptr(), table_out.data_ptr(), lens_out.data_ptr(),
+                                          weights_out.data_ptr(), weights_out.shape[2], kept.data_ptr(),
+                                          capi._stream(stream)))
