@@ -306,7 +306,7 @@ def _run_own(s):
     B, kv, budget, i32 = lens.numel(), s["kv"], s["budget"], torch.int32
     kept, weights = empty(B, kv, budget, dtype=i32), empty(B, kv, budget, dtype=torch.float32)
     table_out, lens_out = torch.empty_like(table), torch.empty_like(lens)
-    q.apr_kv8_evict(cache, table, lens, s["acc"], budget, s["recent"], s["fresh"], table_out, lens_out, weights, kept)
+    q.apr_kv8_evict(cache, table, lens, s["acc"], budget, s["recent"], s["fresh"], table_out, lens_out, weights, kept, max_len=s["max_len"])
     k, v = empty(s["back_rows"], wide), empty(s["back_rows"], wide)
     q.apr_kv8_read(cache, table_out, lens_out, k, v, row_start=s["back_start"], max_rows=s["back_max"])
     return {"kept": kept, "weights": weights, "table": table_out, "lens": lens_out, "k": k, "v": v}
