@@ -49,6 +49,8 @@ int view_of(const apr_kv8_cache* c, const apr_kv8_rows* r, bool with_rows, Kv8Vi
     return failf(APR_E_INVAL, "page_tokens must be 32, 64, 128 or 256 (got %lld)", c->page_tokens);
   if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
     return failf(APR_E_INVAL, "head_dim must be 64, 128 or 256 (got %lld)", c->head_dim);
+  if ((long long)c->num_pages * c->num_kv_heads * c->page_tokens > (1LL << 36))
+    return set_error(APR_E_INVAL, "a cache of more than 2^36 tokens and heads");
   if (r->num_seqs < 0 || r->num_seqs > 16384 || r->num_rows < 0 || r->num_rows > (1 << 24))
     return failf(APR_E_INVAL, "bad sizes: num_seqs=%lld num_rows=%lld", r->num_seqs, r->num_rows);
   if (with_rows && !r->row_start && r->num_rows != r->num_seqs)

@@ -2,18 +2,53 @@
 // (include/apr_kv8.h):
 //   p_j = softmax_j(scale q . (c_j s)),  out = sum_j p_j (c'_j s'),  w_j = sum of p_j
 //
-// Work. The (row, head) pairs of a sequence that read the same KV head are
-// taken PAIRS at a time; one such group of pairs over all the sequence's
-// positions is a segment, and its positions go in units of UNIT. The units of
-// all segments are numbered through, and each CTA takes an equal, contiguous
-// share of them, so that sequences of any lengths in one batch keep every SM
-// equally busy. A segment within one CTA's share is finished there; otherwise
-// each CTA that has a piece of it writes the piece's unnormalised sums with
-// their reference maximum and total, and a second kernel combines the pieces in
-// order. A third kernel, where the weights are wanted, turns the scores that
-// the first one kept into them once the totals are known.
+// Bound. One byte of K or V enters 2 operations for each (row, head) pair that
+// reads it, 8 pairs in a decode step of usual grouping: 16 operations a byte,
+// far below the tensor cores' ratio, far above the CUDA cores' (float32 FMAs at
+// the HBM rate: 6.7 TB/s x 16 = 107 TFLOP/s). So the products go to the tensor
+// cores as m16n8k16 steps with 8 pairs as the M side, and what has to be kept
+// below the HBM time is the rest: two byte permutes, an exclusive or and two
+// subtractions for each four codes turned into fp16, which holds them exactly.
+//
+// Precision for free. The M side has 16 rows and 8 pairs, so each pair's
+// float32 query (scaled by a power of two) goes in as two fp16 rows, q = hi +
+// lo to 22 bits, and each softmax weight likewise: the two rows' results are
+// added in float32. The sums over positions restart every TILE positions and
+// are added up in float32 with the page's V scale, so the tensor cores never
+// accumulate over a long sequence. A weight is kept times 2^10 against a
+// reference that trails the running maximum by at most 4 (base 2), so weights
+// down to 2^-34 of the largest keep a bit.
+//
+// Work. The pairs of a sequence that read the same KV head are taken PAIRS =
+// 8 MT at a time; one such group of pairs over all the sequence's positions is
+// a segment, and its positions go in units of UNIT. The units of all segments
+// are numbered through, and each CTA takes an equal, contiguous share of them,
+// so that sequences of any lengths in one batch keep every SM equally busy. A
+// segment within one CTA's share is finished there; otherwise each CTA that has
+// a piece of it writes the piece's unnormalised sums with their reference
+// maximum and total, and a second kernel combines the pieces in order. A third
+// kernel, where the weights are wanted, turns the scores that the first one
+// kept into them once the totals are known.
+//
+// A CTA. Its 8 warps form 8 / MT key groups; a group takes every (8 / MT)-th
+// tile of TILE positions, and each of its MT warps 8 of the pairs. The group
+// streams its tiles through a ring of its own in shared memory by asynchronous
+// 16-byte copies (a tile's K, its V, the next tile's K, ...), so that warps do
+// not wait for one another. A row's 16-byte chunks are stored exclusive-or'ed
+// with bits of the row so that both products' reads are free of bank
+// conflicts: for K a quarter warp reads 4 chunks of 2 neighbouring rows, for V
+// 2 chunks of every other row of 8.
+// Lane (r, c) = (lane / 4, lane % 4) reads K's row 8 t + r, dims 16 c .. + 15 of
+// each 64: word w holds its 4 dims of k-step w, an order of the dims that the
+// query's fragments share. For V it reads dims 16 r .. + 15 of each 128 of the
+// four rows 16 j + 2 c + {0, 1, 8, 9} that its weights belong to, and word w's
+// byte t of them is its part of the product's columns 4 w + t.
 //
 // The softmax works in base 2.
+//
+// Measured (GB300; the CUDA-core form that came first): 48 sequences of 130 to
+// 9000 tokens, 32 heads over 8 of 128: 82 us (690); 3 of 100000 to 131000, 16
+// over 4 of 256: 133 us, 5.2 TB/s (1829).
 
 #include "apr_internal.h"
 #include "host_common.h"
@@ -23,8 +58,11 @@ namespace apr {
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int UNIT = 64;   // positions of a unit of work
-constexpr int PAIRS = 8;   // (row, head) pairs of a segment
+constexpr int WARPS = THREADS / 32;
+constexpr int UNIT = 64;      // positions of a unit of work
+constexpr int TILE = 32;      // positions of a tile, within one page
+constexpr float HEADROOM = 10.f;  // weights are kept times 2^10
+constexpr float MOVE_ABOVE = 4.f;  // the reference moves when the maximum is more than this above it
 
 struct AttnArgs {
   Kv8View v;
@@ -32,23 +70,20 @@ struct AttnArgs {
   void* out;
   long long ldq, ldo;
   int type, heads, group;
+  int pairs;         // (row, head) pairs of a segment
   float scale_log2;  // softmax scale times log2(e)
   int ctas;          // of the grid; no more than there are units share them
   int* prefix;       // [num_seqs + 1] first unit of each sequence (written by CTA 0)
-  float2* part_ml;   // [2 ctas][PAIRS] reference maximum and total of a piece
-  float* part_o;     // [2 ctas][PAIRS][dim]
+  float2* part_ml;   // [2 ctas][pairs] reference maximum and total of a piece
+  float* part_o;     // [2 ctas][pairs][dim]
   float2* final_ml;  // [rows][heads] maximum and 1 / total, or nullptr
-  float* scores;     // [rows][heads][max_len] scores in base 2, or nullptr
+  float* scores;     // [rows][heads][scores_ld] scores in base 2, or nullptr
+  int scores_ld;     // max_len rounded up to whole tiles
   float* weights;
   long long weights_ld;
   int accumulate;
 };
 
-__device__ __forceinline__ float load_any(const void* p, int type, size_t i) {
-  if (type == APR_T_F32) return static_cast<const float*>(p)[i];
-  if (type == APR_T_F16) return __half2float(static_cast<const __half*>(p)[i]);
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
 __device__ __forceinline__ void store_any(void* p, int type, size_t i, float x) {
   if (type == APR_T_F32)
     static_cast<float*>(p)[i] = x;
@@ -61,7 +96,7 @@ __device__ __forceinline__ void store_any(void* p, int type, size_t i, float x) 
 // Units of one segment of a sequence, and its segments.
 __device__ __forceinline__ int segment_units(int len) { return max(1, (len + UNIT - 1) / UNIT); }
 __device__ __forceinline__ int segment_count(const AttnArgs& a, int n) {
-  return (n * a.group + PAIRS - 1) / PAIRS * a.v.kv_heads;
+  return (n * a.group + a.pairs - 1) / a.pairs * a.v.kv_heads;
 }
 __device__ __forceinline__ int sequence_units(const AttnArgs& a, int b) {
   const int n = kv8_rows(a.v, b).n;
@@ -77,24 +112,106 @@ __device__ __forceinline__ int cta_of(int u, int ctas, int total) {
   return (int)((((long long)u + 1) * ctas - 1) / total);
 }
 
+// ---------------------------------------------------------------- the tiles
+// Where 16-byte chunk x of a tile (row x / (D / 16)) lies in its slot.
 template <int D>
-__global__ void __launch_bounds__(THREADS) kv8_attention_kernel(const AttnArgs a) {
+__device__ __forceinline__ int swizzled(int x) {
+  const int row = x / (D / 16);
+  const int bits = D >= 128 ? (((row ^ (row >> 1)) & 1) << 2) | (((row >> 2) & 1) << 1)
+                            : (((row >> 1) & 1) << 2) | (((row >> 2) & 1) << 1);
+  return x ^ bits;
+}
+
+__device__ __forceinline__ void copy_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// D += A . B, m16n8k16, fp16 in, float32 sums.
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+// Two codes, plus 128, from the bytes that `sel` picks: 0x64uu is the fp16
+// number 1024 + uu.
+__device__ __forceinline__ uint32_t half2_of_codes(uint32_t biased, uint32_t sel) {
+  const uint32_t h = __byte_perm(biased, 0x64646464u, sel);
+  const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&h), __half2half2(__ushort_as_half(0x6480)));
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 half2_values(uint32_t u) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 4 consecutive elements of a row.
+__device__ __forceinline__ float4 load4_any(const void* p, int type, size_t i) {
+  if (type == APR_T_F32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+  const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+  if (type == APR_T_F16) {
+    const float2 a = half2_values(w.x), b = half2_values(w.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xffff0000u));
+}
+
+template <int D, int MT>
+struct Shape {
+  static constexpr int PAIRS = 8 * MT;
+  static constexpr int GROUPS = WARPS / MT;          // key groups
+  static constexpr int SLOT = TILE * D;              // bytes of a tile's K or V
+  static constexpr int SLOTS = MT == 1 ? 3 : 4;      // of a group's ring
+  static constexpr int CHUNKS = SLOT / 16 / (32 * MT);  // 16-byte copies a lane and slot
+  static constexpr int STEPS = D / 16;               // k-steps of a score
+  static constexpr int RING = GROUPS * SLOTS * SLOT;
+  static constexpr int MERGE = WARPS * 8 * D * 4;    // the warps' sums, in the ring's place
+  static constexpr int OFF_Q = RING > MERGE ? RING : MERGE;
+  static constexpr int BYTES = OFF_Q + MT * STEPS * 512;
+  // two CTAs on an SM where registers and shared memory allow
+  static constexpr int CTAS = D <= 128 ? 2 : 1;
+};
+
+template <int D, int MT>
+__global__ void __launch_bounds__(THREADS, Shape<D, MT>::CTAS) kv8_attention_kernel(const __grid_constant__ AttnArgs a) {
+  using S = Shape<D, MT>;
   grid_launch_dependents();
   grid_dependency_wait();
-  constexpr int TILE = 32;
-  __shared__ float sq[PAIRS][D];
-  __shared__ float sk[TILE][D + 1];
-  __shared__ float sp[PAIRS][TILE];
-  __shared__ int s_scan[THREADS / 32];
-  __shared__ int s_find[3];
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ int s_scan[WARPS];
+  __shared__ int s_find[2];
+  __shared__ float s_factor[S::PAIRS];          // score of a pair = factor * (K scale) * sum of products
+  __shared__ float2 s_ml[WARPS][8];
   const Kv8View& v = a.v;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
+  const int mt = warp % MT, kg = warp / MT;
+  uint8_t* ring = smem + kg * S::SLOTS * S::SLOT;
+  const uint32_t ring_u32 = smem_u32(ring);
+  const uint4* sq = reinterpret_cast<const uint4*>(smem + S::OFF_Q) + mt * S::STEPS * 32 + lane;
 
   // ---- the units of the sequences, and where this CTA's share begins
-  int total = 0;
+  int total = 0, ctas = 0;
   for (int pass = 0; pass < 2; ++pass) {
     int base = 0;
-    const int u0 = pass ? first_unit(blockIdx.x, min(a.ctas, total), total) : 0;
+    const int u0 = pass ? first_unit(blockIdx.x, ctas, total) : 0;
     for (int b0 = 0; b0 < v.num_seqs; b0 += THREADS) {
       const int b = b0 + (int)threadIdx.x;
       const int n = b < v.num_seqs ? sequence_units(a, b) : 0;
@@ -109,7 +226,7 @@ __global__ void __launch_bounds__(THREADS) kv8_attention_kernel(const AttnArgs a
       __syncthreads();
       int before = base, all = 0;
 #pragma unroll
-      for (int w = 0; w < THREADS / 32; ++w) {
+      for (int w = 0; w < WARPS; ++w) {
         if (w < warp) before += s_scan[w];
         all += s_scan[w];
       }
@@ -122,11 +239,12 @@ __global__ void __launch_bounds__(THREADS) kv8_attention_kernel(const AttnArgs a
       base += all;
     }
     total = base;
+    ctas = min(a.ctas, total);
+    if (pass == 0 && (int)blockIdx.x >= max(ctas, 1)) return;
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) a.prefix[v.num_seqs] = total;
+  if (total == 0) return;
   __syncthreads();
-  const int ctas = min(a.ctas, total);
-  if ((int)blockIdx.x >= ctas) return;
   int u = first_unit(blockIdx.x, ctas, total);
   const int u_begin = u, u_end = first_unit(blockIdx.x + 1, ctas, total);
   int b = s_find[0], seq_u0 = s_find[1];
@@ -141,80 +259,302 @@ __global__ void __launch_bounds__(THREADS) kv8_attention_kernel(const AttnArgs a
       continue;
     }
     const int seg = (u - seq_u0) / su, seg_u0 = seq_u0 + seg * su;
-    const int g = seg % v.kv_heads, p0 = seg / v.kv_heads * PAIRS, np = min(PAIRS, span.n * a.group - p0);
+    const int g = seg % v.kv_heads, p0 = seg / v.kv_heads * S::PAIRS, np = min(S::PAIRS, span.n * a.group - p0);
     const int ue = min(u_end, seg_u0 + su);
     const int k0 = (u - seg_u0) * UNIT, k1 = min(len, (ue - seg_u0) * UNIT);
-    // ---- the pairs' query rows
-    __syncthreads();
-    for (int i = threadIdx.x; i < PAIRS * D; i += THREADS) {
-      const int p = i / D, c = i % D, pair = p0 + p;
-      const int row = span.r0 + pair / a.group, head = g * a.group + pair % a.group;
-      sq[p][c] = p < np ? load_any(a.q, a.type, (size_t)row * a.ldq + (size_t)head * D + c) : 0.f;
+    // this group's tiles: kg, kg + GROUPS, ... of the piece's
+    const int tiles = k1 > k0 ? (k1 - k0 + TILE - 1) / TILE : 0;
+    const int mine = tiles > kg ? (tiles - kg + S::GROUPS - 1) / S::GROUPS : 0;
+
+    // a tile's place in the cache, in tiles: lane i has that of this group's
+    // tile 32 n + i (page ids out of range read page 0, and are flagged)
+    const int in_page = (1 << v.page_shift) / TILE - 1;
+    auto tile_of = [&](int i, size_t* scale_at) {
+      const int k = k0 + (kg + min(i, mine - 1) * S::GROUPS) * TILE;
+      const int page = max(kv8_page(v, b, k >> v.page_shift), 0);
+      *scale_at = kv8_scale_at(v, page, g);
+      return (uint32_t)(*scale_at << (v.page_shift - 5)) + (uint32_t)((k / TILE) & in_page);
+    };
+    uint32_t at_next = 0;
+    float ks_all = 0.f, vs_all = 0.f;
+    if (mine > 0) {
+      size_t scale_at;
+      at_next = tile_of(lane, &scale_at);
+      ks_all = __ldg(v.k_scale + scale_at);
+      vs_all = __ldg(v.v_scale + scale_at);
     }
-    const int pair = p0 + warp;  // this warp's pair
-    const bool live = warp < np;
-    const int row = span.r0 + pair / a.group, head = g * a.group + pair % a.group;
-    const int limit = len - span.n + pair / a.group + 1;  // positions the pair sees
-    float m = -INFINITY, l = 0.f, o[D / 32];
+    // sends chunk n of the group (tile n / 2; its K, then its V) into the ring
+    auto send = [&](int n) {
+      if (n < 2 * mine) {
+        const int i = n >> 1;
+        if ((n & 63) == 0 && n) {
+          size_t scale_at;
+          at_next = tile_of(i + lane, &scale_at);
+        }
+        const uint32_t at = __shfl_sync(0xffffffffu, at_next, i & 31);
+        const int8_t* src = (n & 1 ? v.V : v.K) + (size_t)at * S::SLOT;
+        const uint32_t dst = ring_u32 + (n % S::SLOTS) * S::SLOT;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-    for (int k = k0; k < k1; k += TILE) {
-      const int page = kv8_page(v, b, k >> v.page_shift);
-      const size_t at = page < 0 ? 0 : kv8_codes_at(v, page, g) + (size_t)(k & ((1 << v.page_shift) - 1)) * D;
-      const float ks = page < 0 ? 0.f : v.k_scale[kv8_scale_at(v, page, g)];
-      const float vs = page < 0 ? 0.f : v.v_scale[kv8_scale_at(v, page, g)];
-      __syncthreads();
-      for (int i = threadIdx.x; i < TILE * D / 4; i += THREADS) {
-        const uint32_t w = page < 0 ? 0 : reinterpret_cast<const uint32_t*>(v.K + at)[i];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) sk[4 * i / D][4 * i % D + t] = (float)kv8_byte(w, t);
+        for (int j = 0; j < S::CHUNKS; ++j) {
+          const int x = (j * MT + mt) * 32 + lane;
+          copy_async_16(dst + swizzled<D>(x) * 16, src + x * 16);
+        }
       }
-      __syncthreads();
-      float s = -INFINITY;
-      if (live && k + lane < min(limit, len) && page >= 0) {
-        s = 0.f;
-        for (int c = 0; c < D; ++c) s = fmaf(sq[warp][c], sk[lane][c], s);
-        s *= ks * a.scale_log2;
-      }
-      if (live && a.scores && k + lane < len) a.scores[((size_t)row * a.heads + head) * v.max_len + k + lane] = s;
-      float top = s;
+      copy_commit();
+    };
 #pragma unroll
-      for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-      const float m_new = fmaxf(m, top), ref = m_new == -INFINITY ? 0.f : m_new;
-      const float f = exp2f(m - ref), p = exp2f(s - ref);
-      m = m_new;
-      l = l * f + p;  // per lane
-      sp[warp][lane] = p * vs;
-      __syncthreads();
-      for (int i = threadIdx.x; i < TILE * D / 4; i += THREADS) {
-        const uint32_t w = page < 0 ? 0 : reinterpret_cast<const uint32_t*>(v.V + at)[i];
+    for (int n = 0; n < S::SLOTS - 1; ++n) send(n);
+
+    // ---- the pairs' query rows as fragments: row r of an M tile its fp16 hi, row r + 8 its lo
+    for (int p = warp; p < S::PAIRS; p += WARPS) {
+      const int pair = p0 + p;
+      const size_t row = span.r0 + pair / a.group, head = g * a.group + pair % a.group;
+      float4 x[(D + 127) / 128];
+      float top = 0.f;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) sk[4 * i / D][4 * i % D + t] = (float)kv8_byte(w, t);
+      for (int j = 0; j < (D + 127) / 128; ++j) {
+        const int d = 128 * j + 4 * lane;
+        x[j] = p < np && d < D ? load4_any(a.q, a.type, row * a.ldq + head * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+        top = fmaxf(top, fmaxf(fmaxf(fabsf(x[j].x), fabsf(x[j].y)), fmaxf(fabsf(x[j].z), fabsf(x[j].w))));
       }
-      __syncthreads();
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // the power of two that brings the largest magnitude into [1, 2)
+      const int e = top > 0.f && top <= FLT_MAX ? ilogbf(top) : 0;
+      if (lane == 0) s_factor[p] = scalbnf(a.scale_log2, e);
+#pragma unroll
+      for (int j = 0; j < (D + 127) / 128; ++j) {
+        const int d = 128 * j + 4 * lane;
+        if (d < D) {
+          const float4 y = make_float4(scalbnf(x[j].x, -e), scalbnf(x[j].y, -e), scalbnf(x[j].z, -e), scalbnf(x[j].w, -e));
+          const uint32_t h0 = half2_bits(y.x, y.y), h1 = half2_bits(y.z, y.w);
+          const float2 f0 = half2_values(h0), f1 = half2_values(h1);
+          const int step = d / 64 * 4 + d % 16 / 4, col = d % 64 / 16;
+          reinterpret_cast<uint4*>(smem + S::OFF_Q)[((p / 8) * S::STEPS + step) * 32 + (p % 8) * 4 + col] =
+              make_uint4(h0, half2_bits(y.x - f0.x, y.y - f0.y), h1, half2_bits(y.z - f1.x, y.w - f1.y));
+        }
+      }
+    }
+    __syncthreads();
+
+    // this lane's pair: row r of its M tile
+    const int pair = p0 + 8 * mt + r;
+    const bool live = 8 * mt + r < np;
+    const int limit = live ? min(len, len - span.n + pair / a.group + 1) : 0;  // positions the pair sees
+    const int least = len - span.n + (p0 + 8 * mt) / a.group + 1;              // the fewest of this M tile's
+    const float factor = s_factor[8 * mt + r];
+    float* score_row = nullptr;
+    if (a.scores && live)
+      score_row = a.scores +
+                  ((size_t)(span.r0 + pair / a.group) * a.heads + g * a.group + pair % a.group) * a.scores_ld + 2 * c;
+
+    float ref = -INFINITY, l = 0.f;
+    float sum[D / 8][2];  // [column 4 w + t of each 128 dims]: dims 32 c + (4 w + t) and + 16 (D = 64: 16 c and + 8)
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) sum[i][0] = sum[i][1] = 0.f;
+
+    auto group_sync = [&] {
+      if (MT == 1)
+        __syncwarp();
+      else
+        named_sync(1 + kg, 32 * MT);
+    };
+
+#pragma unroll 1
+    for (int i = 0; i < mine; ++i) {
+      if ((i & 31) == 0 && i) {
+        size_t scale_at;
+        tile_of(i + lane, &scale_at);
+        ks_all = __ldg(v.k_scale + scale_at);
+        vs_all = __ldg(v.v_scale + scale_at);
+      }
+      const float ks = __shfl_sync(0xffffffffu, ks_all, i & 31), vs = __shfl_sync(0xffffffffu, vs_all, i & 31);
+      const int k = k0 + (kg + i * S::GROUPS) * TILE;
+
+      // ---- scores of the tile's 32 positions: 4 columns of 8
+      copy_wait<S::SLOTS - 2>();
+      group_sync();
+      send(2 * i + S::SLOTS - 1);
+      const uint8_t* kt = ring + (2 * i) % S::SLOTS * S::SLOT;
+      float s[4][4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+#pragma unroll
+      for (int d64 = 0; d64 < D / 64; ++d64) {
+        uint4 kw[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          kw[t] = *reinterpret_cast<const uint4*>(kt + swizzled<D>((8 * t + r) * (D / 16) + 4 * d64 + c) * 16);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint4 qa = sq[(4 * d64 + w) * 32];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint32_t x = (w == 0 ? kw[t].x : w == 1 ? kw[t].y : w == 2 ? kw[t].z : kw[t].w) ^ 0x80808080u;
+            mma16816(s[t], qa, half2_of_codes(x, 0x4140), half2_of_codes(x, 0x4342));
+          }
+        }
+      }
+
+      // ---- the softmax weights
+      const float kf = ks * factor;
+      float top = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        s[t][0] = (s[t][0] + s[t][2]) * kf;
+        s[t][1] = (s[t][1] + s[t][3]) * kf;
+      }
+      if (k + TILE > least) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int j = k + 8 * t + 2 * c;
+          if (j >= limit) s[t][0] = -INFINITY;
+          if (j + 1 >= limit) s[t][1] = -INFINITY;
+        }
+      }
+      if (score_row) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) *reinterpret_cast<float2*>(score_row + k + 8 * t) = make_float2(s[t][0], s[t][1]);
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) top = fmaxf(top, fmaxf(s[t][0], s[t][1]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      if (__any_sync(0xffffffffu, top > ref + MOVE_ABOVE)) {
+        const float now = fmaxf(ref, top);
+        const float f = ref == -INFINITY ? 0.f : exp2_fast(ref - now);
+        l *= f;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+          sum[j][0] *= f;
+          sum[j][1] *= f;
+        }
+        ref = now;
+      }
+      const float shift = ref == -INFINITY ? 0.f : ref - HEADROOM;
+      uint4 pa[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float x = exp2_fast(s[2 * j + h][0] - shift), y = exp2_fast(s[2 * j + h][1] - shift);
+          l += x + y;
+          hi[h] = half2_bits(x, y);
+          const float2 f = half2_values(hi[h]);
+          lo[h] = half2_bits(x - f.x, y - f.y);
+        }
+        pa[j] = make_uint4(hi[0], lo[0], hi[1], lo[1]);
+      }
+
+      // ---- their product with the tile's V
+      copy_wait<S::SLOTS - 2>();
+      group_sync();
+      send(2 * i + S::SLOTS);
+      const uint8_t* vt = ring + (2 * i + 1) % S::SLOTS * S::SLOT;
+      constexpr int COLS = D >= 128 ? 16 : 8;  // columns a lane's bytes of a row give
+#pragma unroll
+      for (int dc = 0; dc < (D + 127) / 128; ++dc) {
+        uint32_t vw[2][4][COLS / 4];  // [k-step][row 2 c + {0, 1, 8, 9}][words]
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const int row = 16 * j + 2 * c + (h & 1) + 8 * (h >> 1);
+            if (D >= 128) {
+              *reinterpret_cast<uint4*>(vw[j][h]) =
+                  *reinterpret_cast<const uint4*>(vt + swizzled<D>(row * (D / 16) + 8 * dc + r) * 16);
+            } else {
+              *reinterpret_cast<uint2*>(vw[j][h]) =
+                  *reinterpret_cast<const uint2*>(vt + swizzled<D>(row * (D / 16) + r / 2) * 16 + (r & 1) * 8);
+            }
+          }
+#pragma unroll
+        for (int w = 0; w < COLS / 4; ++w) {
+          float o[4][4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            uint32_t x[2][2];  // [rows 2 c, 2 c + 1 or + 8][columns 0, 1 or 2, 3]: the two rows' bytes side by side
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              x[h][0] = __byte_perm(vw[j][2 * h][w], vw[j][2 * h + 1][w], 0x5140) ^ 0x80808080u;
+              x[h][1] = __byte_perm(vw[j][2 * h][w], vw[j][2 * h + 1][w], 0x7362) ^ 0x80808080u;
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const uint32_t sel = t & 1 ? 0x4342 : 0x4140;
+              mma16816(o[t], pa[j], half2_of_codes(x[0][t / 2], sel), half2_of_codes(x[1][t / 2], sel));
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            float* to = sum[COLS * dc + 4 * w + t];
+            to[0] = fmaf(vs, o[t][0] + o[t][2], to[0]);
+            to[1] = fmaf(vs, o[t][1] + o[t][3], to[1]);
+          }
+        }
+      }
+    }
+    copy_wait<0>();
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+
+    // ---- the warps' sums together, in order, through the ring's memory
+    __syncthreads();
+    float* merge = reinterpret_cast<float*>(smem);  // [warp][8][D]
+    const float m_own = ref == -INFINITY ? -INFINITY : ref - HEADROOM;
+    if (c == 0) s_ml[warp][r] = make_float2(m_own, l);
+    {
+      float* to = merge + ((size_t)warp * 8 + r) * D;
+      constexpr int COLS = D >= 128 ? 16 : 8;
+#pragma unroll
+      for (int dc = 0; dc < (D + 127) / 128; ++dc)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < COLS; i += 4)
+            *reinterpret_cast<float4*>(to + 128 * dc + (2 * c + h) * COLS + i) =
+                make_float4(sum[COLS * dc + i][h], sum[COLS * dc + i + 1][h], sum[COLS * dc + i + 2][h],
+                            sum[COLS * dc + i + 3][h]);
+    }
+    __syncthreads();
+    const bool whole = u == seg_u0 && ue == seg_u0 + su;
+    const size_t slot = (size_t)(2 * blockIdx.x + (u_begin > seg_u0 ? 0 : 1)) * S::PAIRS;
+    for (int p = warp; p < np; p += WARPS) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < S::GROUPS; ++w) m = fmaxf(m, s_ml[w * MT + p / 8][p % 8].x);
+      if (m == -INFINITY) m = 0.f;
+      float total_l = 0.f, f[S::GROUPS];
+#pragma unroll
+      for (int w = 0; w < S::GROUPS; ++w) {
+        const float2 ml = s_ml[w * MT + p / 8][p % 8];
+        f[w] = ml.y > 0.f || ml.y != ml.y ? exp2f(ml.x == -INFINITY ? 0.f : ml.x - m) : 0.f;
+        total_l = fmaf(f[w], ml.y, total_l);
+      }
+      const float inv = total_l > 0.f || total_l != total_l ? 1.f / total_l : 0.f;
+      const size_t row = span.r0 + (p0 + p) / a.group, head = g * a.group + (p0 + p) % a.group;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        float acc = o[i] * f;
-        for (int j = 0; j < TILE; ++j) acc = fmaf(sp[warp][j], sk[j][32 * i + lane], acc);
-        o[i] = acc;
+        const int d = 32 * i + lane;
+        float o = 0.f;
+#pragma unroll
+        for (int w = 0; w < S::GROUPS; ++w) o = fmaf(f[w], merge[((size_t)(w * MT + p / 8) * 8 + p % 8) * D + d], o);
+        if (whole)
+          store_any(a.out, a.type, row * a.ldo + head * D + d, o * inv);
+        else
+          a.part_o[(slot + p) * D + d] = o;
+      }
+      if (lane == 0) {
+        if (!whole)
+          a.part_ml[slot + p] = make_float2(m, total_l);
+        else if (a.final_ml)
+          a.final_ml[row * a.heads + head] = make_float2(m, inv);
       }
     }
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-    if (m == -INFINITY) m = 0.f;
-    const bool whole = u == seg_u0 && ue == seg_u0 + su;
-    if (live && whole) {
-      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i)
-        store_any(a.out, a.type, (size_t)row * a.ldo + (size_t)head * D + 32 * i + lane, o[i] * inv);
-      if (a.final_ml && lane == 0) a.final_ml[(size_t)row * a.heads + head] = make_float2(m, inv);
-    } else if (live) {
-      const size_t slot = (size_t)(2 * blockIdx.x + (u_begin > seg_u0 ? 0 : 1)) * PAIRS + warp;
-      if (lane == 0) a.part_ml[slot] = make_float2(m, l);
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) a.part_o[slot * D + 32 * i + lane] = o[i];
-    }
+    __syncthreads();
     u = ue;
   }
 }
@@ -232,11 +572,11 @@ __global__ void __launch_bounds__(256) kv8_combine_kernel(const AttnArgs a) {
   const int g = id % v.kv_heads, pair = id / v.kv_heads;
   if (pair >= span.n * a.group) return;
   const int total = a.prefix[v.num_seqs], ctas = min(a.ctas, total), su = segment_units(kv8_len(v, b));
-  const int u0 = a.prefix[b] + (pair / PAIRS * v.kv_heads + g) * su;
+  const int u0 = a.prefix[b] + (pair / a.pairs * v.kv_heads + g) * su;
   const int c0 = cta_of(u0, ctas, total), c1 = cta_of(u0 + su - 1, ctas, total);
   if (c0 == c1) return;
   // the first CTA wrote it as the segment it began, the others as the one they continued
-  auto slot = [&](int c) { return (size_t)(c == c0 ? 2 * c + 1 : 2 * c) * PAIRS + pair % PAIRS; };
+  auto slot = [&](int c) { return (size_t)(c == c0 ? 2 * c + 1 : 2 * c) * a.pairs + pair % a.pairs; };
   float m = -INFINITY;
   for (int c = c0 + lane; c <= c1; c += 32) {
     const float2 ml = a.part_ml[slot(c)];
@@ -283,7 +623,7 @@ __global__ void __launch_bounds__(256) kv8_weights_kernel(const AttnArgs a) {
       for (int h = 0; h < a.group; ++h) {
         const size_t at = (size_t)(span.r0 + i) * a.heads + g * a.group + h;
         const float2 ml = a.final_ml[at];
-        sum += exp2f(a.scores[at * v.max_len + j] - ml.x) * ml.y;
+        sum += exp2f(a.scores[at * a.scores_ld + j] - ml.x) * ml.y;
       }
     if (a.accumulate && j < len - span.n) sum += *w;
   }
@@ -291,16 +631,29 @@ __global__ void __launch_bounds__(256) kv8_weights_kernel(const AttnArgs a) {
 }
 
 struct Layout {
-  int ctas;
+  int mt, ctas;
   size_t prefix, part_ml, part_o, final_ml, scores, bytes;
 };
 
+// M tiles of 8 pairs that share a key tile's loads: as many as the longest
+// row group of a sequence fills, at most 4.
+int m_tiles(const Kv8View& v, const Kv8Attention& a) {
+  const long long pairs = (long long)v.max_rows * (a.heads / v.kv_heads);
+  return pairs <= 8 ? 1 : (pairs <= 16 ? 2 : 4);
+}
+
+// CTAs that run at once: one or two an SM (Shape::CTAS).
+int resident_ctas(int dim) { return (dim <= 128 ? 2 : 1) * num_sms(); }
+
+int scores_ld(const Kv8View& v) { return (int)(((long long)v.max_len + TILE - 1) / TILE * TILE); }
+
 Layout layout_of(const Kv8View& v, const Kv8Attention& a) {
   Layout l;
-  const int group = a.heads / v.kv_heads;
-  const long long segs = ((long long)v.num_rows * group / PAIRS + v.num_seqs) * v.kv_heads;  // at most
+  l.mt = m_tiles(v, a);
+  const int group = a.heads / v.kv_heads, pairs = 8 * l.mt, most_ctas = resident_ctas(v.dim);
+  const long long segs = ((long long)v.num_rows * group / pairs + v.num_seqs) * v.kv_heads;  // at most
   const long long most = segs * (v.max_len / UNIT + 1);
-  l.ctas = (int)(most < 2 * num_sms() ? (most < 1 ? 1 : most) : 2 * num_sms());
+  l.ctas = (int)(most < most_ctas ? most : most_ctas);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -308,32 +661,50 @@ Layout layout_of(const Kv8View& v, const Kv8Attention& a) {
     return here;
   };
   l.prefix = take(((size_t)v.num_seqs + 1) * 4);
-  l.part_ml = take((size_t)2 * l.ctas * PAIRS * 8);
-  l.part_o = take((size_t)2 * l.ctas * PAIRS * v.dim * 4);
+  l.part_ml = take((size_t)2 * l.ctas * pairs * 8);
+  l.part_o = take((size_t)2 * l.ctas * pairs * v.dim * 4);
   l.final_ml = take(a.weights ? (size_t)v.num_rows * a.heads * 8 : 0);
-  l.scores = take(a.weights ? (size_t)v.num_rows * a.heads * v.max_len * 4 : 0);
+  l.scores = take(a.weights ? (size_t)v.num_rows * a.heads * scores_ld(v) * 4 : 0);
   l.bytes = at;
   return l;
 }
 
-template <int D>
-cudaError_t launch_dim(const AttnArgs& a, cudaStream_t s) {
+template <int D, int MT>
+cudaError_t launch_shape(const AttnArgs& a, cudaStream_t s) {
+  using S = Shape<D, MT>;
+  static bool ready[64] = {};  // the attribute is set once for each device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !ready[dev]) {
+    e = cudaFuncSetAttribute(kv8_attention_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) ready[dev] = true;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.ctas);
   cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = S::BYTES;
   cfg.stream = s;
   cudaLaunchAttribute attr[1] = {pdl_attr()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_attention_kernel<D>, a);
+  e = cudaLaunchKernelEx(&cfg, kv8_attention_kernel<D, MT>, a);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)(((long long)a.v.max_rows * a.heads + 7) / 8), (unsigned)a.v.num_seqs);
   cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, kv8_combine_kernel<D>, a);
   if (e != cudaSuccess || !a.weights) return e;
   const long long span = a.accumulate ? a.v.max_len : a.weights_ld;
+  if (span == 0) return cudaSuccess;
   cfg.gridDim = dim3((unsigned)((span + 255) / 256), (unsigned)a.v.kv_heads, (unsigned)a.v.num_seqs);
   return cudaLaunchKernelEx(&cfg, kv8_weights_kernel, a);
+}
+
+template <int D>
+cudaError_t launch_dim(const AttnArgs& a, int mt, cudaStream_t s) {
+  return mt == 1 ? launch_shape<D, 1>(a, s) : (mt == 2 ? launch_shape<D, 2>(a, s) : launch_shape<D, 4>(a, s));
 }
 
 }  // namespace
@@ -352,6 +723,7 @@ cudaError_t launch_kv8_attention(const Kv8View& v, const Kv8Attention& in, void*
   a.type = in.type;
   a.heads = in.heads;
   a.group = in.heads / v.kv_heads;
+  a.pairs = 8 * l.mt;
   a.scale_log2 = in.scale * 1.4426950408889634f;
   a.ctas = l.ctas;
   a.prefix = reinterpret_cast<int*>(base + l.prefix);
@@ -360,13 +732,14 @@ cudaError_t launch_kv8_attention(const Kv8View& v, const Kv8Attention& in, void*
   if (in.weights) {
     a.final_ml = reinterpret_cast<float2*>(base + l.final_ml);
     a.scores = reinterpret_cast<float*>(base + l.scores);
+    a.scores_ld = scores_ld(v);
     a.weights = in.weights;
     a.weights_ld = in.weights_ld;
     a.accumulate = in.accumulate;
   }
-  if (v.dim == 64) return launch_dim<64>(a, s);
-  if (v.dim == 128) return launch_dim<128>(a, s);
-  return launch_dim<256>(a, s);
+  if (v.dim == 64) return launch_dim<64>(a, l.mt, s);
+  if (v.dim == 128) return launch_dim<128>(a, l.mt, s);
+  return launch_dim<256>(a, l.mt, s);
 }
 
 }  // namespace apr
