@@ -18,6 +18,8 @@ def __getattr__(name):
         raise AttributeError(name)
     module = ".kv8" if name.startswith(("apr_kv8_", "Kv8", "KV8_", "APR_T_")) else ".capi"
     try:
-        return getattr(importlib.import_module(__name__ + module), name)
+        value = getattr(importlib.import_module(__name__ + module), name)
     except AttributeError:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}") from None
+    globals()[name] = value  # found at once from now on
+    return value

@@ -40,8 +40,6 @@ __device__ __forceinline__ uint2 codes_of(const Elems<T, 8>& e, float s, float i
 template <typename T>
 __global__ void __launch_bounds__(A_THREADS) kv8_append_kernel(Kv8View v, const T* __restrict__ k,
                                                                const T* __restrict__ vv, long long ld) {
-  grid_launch_dependents();
-  grid_dependency_wait();
   __shared__ float s_max[A_THREADS / 32];
   const int b = blockIdx.z, g = (int)(blockIdx.x % v.kv_heads), slot = (int)(blockIdx.x / v.kv_heads);
   const bool is_v = blockIdx.y != 0;
@@ -53,6 +51,8 @@ __global__ void __launch_bounds__(A_THREADS) kv8_append_kernel(Kv8View v, const 
   if (index > (len - 1) >> v.page_shift) return;
   const int page = kv8_page(v, b, index);
   if (page < 0) return;
+  kv8_ready();
+  grid_launch_dependents();
   const int page0 = index << v.page_shift;
   const int lo = max(max(first, 0), page0), hi = min(len, page0 + (1 << v.page_shift));
   const int held = lo - page0;
@@ -126,8 +126,6 @@ __host__ __device__ inline int read_run_shift(int page_shift) { return page_shif
 template <typename T>
 __global__ void __launch_bounds__(R_THREADS) kv8_read_kernel(Kv8View v, T* __restrict__ k, T* __restrict__ vv,
                                                              long long ld) {
-  grid_launch_dependents();
-  grid_dependency_wait();
   constexpr int N = 16 / sizeof(T);  // values of a 16-byte store
   const int b = blockIdx.z, g = (int)(blockIdx.x % v.kv_heads), run = (int)(blockIdx.x / v.kv_heads);
   const bool is_v = blockIdx.y != 0;
@@ -139,6 +137,8 @@ __global__ void __launch_bounds__(R_THREADS) kv8_read_kernel(Kv8View v, T* __res
   const int vshift = 31 - __clz(v.dim / N), cmask = (1 << vshift) - 1;
   T* out = (is_v ? vv : k) + (long long)span.r0 * ld + (size_t)g * v.dim;
   const int index = (max(first, 0) >> rshift) + run;
+  kv8_ready();
+  grid_launch_dependents();
   if (run == 0 && first < 0) {  // rows before the sequence's start
     Elems<T, N> zero;
 #pragma unroll

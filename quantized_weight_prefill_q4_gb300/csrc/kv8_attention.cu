@@ -26,12 +26,14 @@
 // so that sequences of any lengths in one batch keep every SM equally busy. A
 // segment within one CTA's share is finished there; otherwise each CTA that has
 // a piece of it writes the piece's unnormalised sums with their reference
-// maximum and total, and a second kernel combines the pieces in order. A third
-// kernel, where the weights are wanted, turns the scores that the first one
-// kept into them once the totals are known.
+// maximum and total, and a second kernel combines the pieces in order, a CTA for
+// each pair. (Having the last CTA of a segment combine them instead took 3 to 9
+// us more at the end of the measured cases: a fence behind every piece, and one
+// CTA's loads instead of all SMs'.) A third kernel, where the weights are wanted,
+// turns the scores that the first one kept into them once the totals are known.
 //
-// A CTA. Its 8 warps form 8 / MT key groups; a group takes every (8 / MT)-th
-// tile of TILE positions, and each of its MT warps 8 of the pairs. The group
+// A CTA. Its WARPS warps form WARPS / MT key groups; the groups take the tiles
+// of TILE positions in turn, and each of a group's MT warps 8 of the pairs. A group
 // streams its tiles through a ring of its own in shared memory by asynchronous
 // 16-byte copies (a tile's K, its V, the next tile's K, ...), so that warps do
 // not wait for one another. A row's 16-byte chunks are stored exclusive-or'ed
@@ -46,9 +48,12 @@
 //
 // The softmax works in base 2.
 //
-// Measured (GB300; the CUDA-core form that came first): 48 sequences of 130 to
-// 9000 tokens, 32 heads over 8 of 128: 82 us (690); 3 of 100000 to 131000, 16
-// over 4 of 256: 133 us, 5.2 TB/s (1829).
+// Measured (GB300, back to back in a graph): 48 sequences of 130 to 9000 tokens,
+// 32 heads over 8 of 128: 43.5 us, 207 MB (0.71 of the HBM rate); 3 of 100000 to
+// 131000, 16 over 4 of 256: 116 us (0.90); one of 700: 8.9 us. Of the 43.5 us the
+// tiles stream at 6.3 TB/s for 33; the rest is the way to the first codes
+// (length, table, codes: 3 us), CTAs of equal shares that end up to 5 us apart,
+// and the combination (3 us).
 
 #include "apr_internal.h"
 #include "host_common.h"
@@ -57,9 +62,13 @@
 namespace apr {
 namespace {
 
-constexpr int THREADS = 256;
-constexpr int WARPS = THREADS / 32;
 constexpr int UNIT = 64;      // positions of a unit of work
+constexpr int MIN_SHARE = 2;  // units of a CTA's share, where there are not enough for every CTA
+// Units that a segment counts for besides its positions: what its start (the
+// way from the length over the page table to the codes, the query rows) and
+// its end (the warps' sums) take, in units of 128 D bytes. (48 ragged
+// sequences: 49 us with half as much, 44 with this or twice as much.)
+__host__ __device__ constexpr int overhead_units(int dim) { return 512 / dim; }
 constexpr int TILE = 32;      // positions of a tile, within one page
 constexpr float HEADROOM = 10.f;  // weights are kept times 2^10
 constexpr float MOVE_ABOVE = 4.f;  // the reference moves when the maximum is more than this above it
@@ -73,7 +82,7 @@ struct AttnArgs {
   int pairs;         // (row, head) pairs of a segment
   float scale_log2;  // softmax scale times log2(e)
   int ctas;          // of the grid; no more than there are units share them
-  int* prefix;       // [num_seqs + 1] first unit of each sequence (written by CTA 0)
+  int* prefix;       // [num_seqs + 1] first unit of each sequence, all units (written by CTA 0)
   float2* part_ml;   // [2 ctas][pairs] reference maximum and total of a piece
   float* part_o;     // [2 ctas][pairs][dim]
   float2* final_ml;  // [rows][heads] maximum and 1 / total, or nullptr
@@ -84,26 +93,24 @@ struct AttnArgs {
   int accumulate;
 };
 
-__device__ __forceinline__ void store_any(void* p, int type, size_t i, float x) {
-  if (type == APR_T_F32)
-    static_cast<float*>(p)[i] = x;
-  else if (type == APR_T_F16)
-    static_cast<__half*>(p)[i] = __float2half_rn(x);
-  else
-    static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
+// Units of one segment of a sequence (the overhead's first), and its segments.
+__device__ __forceinline__ int segment_units(const AttnArgs& a, int len) {
+  return overhead_units(a.v.dim) + max(1, (len + UNIT - 1) / UNIT);
 }
-
-// Units of one segment of a sequence, and its segments.
-__device__ __forceinline__ int segment_units(int len) { return max(1, (len + UNIT - 1) / UNIT); }
 __device__ __forceinline__ int segment_count(const AttnArgs& a, int n) {
   return (n * a.group + a.pairs - 1) / a.pairs * a.v.kv_heads;
 }
 __device__ __forceinline__ int sequence_units(const AttnArgs& a, int b) {
   const int n = kv8_rows(a.v, b).n;
-  return n == 0 ? 0 : segment_count(a, n) * segment_units(kv8_len(a.v, b));
+  return n == 0 ? 0 : segment_count(a, n) * segment_units(a, kv8_len(a.v, b));
 }
 
-// The `ctas` CTAs that share `total` units: each has one at least. CTA c has the units first_unit(c) .. first_unit(c + 1) - 1 of `total`; the
+// CTAs that share `total` units, MIN_SHARE at least each (fewer share nothing).
+__device__ __forceinline__ int sharing_ctas(const AttnArgs& a, int total) {
+  return min(a.ctas, (total + MIN_SHARE - 1) / MIN_SHARE);
+}
+
+// Of `ctas` CTAs that share `total` units, CTA c has the units first_unit(c) .. first_unit(c + 1) - 1 of `total`; the
 // CTA that has unit u.
 __device__ __forceinline__ int first_unit(int c, int ctas, int total) {
   return (int)((long long)c * total / ctas);
@@ -174,27 +181,67 @@ __device__ __forceinline__ float4 load4_any(const void* p, int type, size_t i) {
                      __uint_as_float(w.y & 0xffff0000u));
 }
 
+__device__ __forceinline__ void store4_any(void* p, int type, size_t i, const float4& x) {
+  if (type == APR_T_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = x;
+  } else if (type == APR_T_F16) {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = make_uint2(half2_bits(x.x, x.y), half2_bits(x.z, x.w));
+  } else {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  }
+}
+
+// What a piece's sums and total are to be multiplied by under the reference m.
+__device__ __forceinline__ float piece_factor(float2 ml, float m) {
+  return ml.y > 0.f ? exp2f(ml.x - m) : (ml.y != ml.y ? 1.f : 0.f);
+}
+// Four dims from d of a (row, head)'s output, from its unnormalised sums and total.
+__device__ __forceinline__ void finish4(const AttnArgs& a, size_t row, size_t head, int dim, int d, const float4& o,
+                                        float m, float total) {
+  const float inv = total > 0.f || total != total ? 1.f / total : 0.f;  // no position seen: zeros
+  store4_any(a.out, a.type, row * a.ldo + head * dim + d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+  if (a.final_ml && d == 0) a.final_ml[row * a.heads + head] = make_float2(m, inv);
+}
+
+// CTAs on an SM: 12 warps, 8 at 256 dims, as registers (168 a thread, 255) and
+// shared memory allow. (At 128 dims 16 warps of 128 registers took 96 us for 4
+// sequences of 60000 where 12 take 83.)
+__host__ __device__ constexpr int ctas_per_sm(int dim, int mt) {
+  return dim <= 128 ? (mt == 1 ? 3 : 2) : (mt == 1 ? 2 : 1);
+}
+
 template <int D, int MT>
 struct Shape {
   static constexpr int PAIRS = 8 * MT;
+  // small CTAs, several on an SM, so that one's start and end overlap the
+  // others' streams; more warps where the pairs take several for each tile
+  static constexpr int WARPS = MT == 1 ? 4 : 8;
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int CTAS = ctas_per_sm(D, MT);
   static constexpr int GROUPS = WARPS / MT;          // key groups
   static constexpr int SLOT = TILE * D;              // bytes of a tile's K or V
   static constexpr int SLOTS = MT == 1 ? 3 : 4;      // of a group's ring
   static constexpr int CHUNKS = SLOT / 16 / (32 * MT);  // 16-byte copies a lane and slot
   static constexpr int STEPS = D / 16;               // k-steps of a score
   static constexpr int RING = GROUPS * SLOTS * SLOT;
-  static constexpr int MERGE = WARPS * 8 * D * 4;    // the warps' sums, in the ring's place
-  static constexpr int OFF_Q = RING > MERGE ? RING : MERGE;
-  static constexpr int BYTES = OFF_Q + MT * STEPS * 512;
-  // two CTAs on an SM where registers and shared memory allow
-  static constexpr int CTAS = D <= 128 ? 2 : 1;
+  static constexpr int OFF_Q = RING;
+  // the warps' sums, 8 rows each: with one M tile in the last slot of the
+  // warp's own ring (of the same size), which the next piece's first chunks do not use
+  static constexpr int OFF_M = MT == 1 ? (SLOTS - 1) * SLOT : OFF_Q + MT * STEPS * 512;
+  static constexpr int M_STEP = MT == 1 ? SLOTS * SLOT : 8 * D * 4;
+  static constexpr int BYTES = OFF_Q + MT * STEPS * 512 + (MT == 1 ? 0 : WARPS * 8 * D * 4);
+  static_assert(8 * D * 4 == SLOT && CHUNKS >= 1, "a warp's sums fill a slot");
 };
 
 template <int D, int MT>
-__global__ void __launch_bounds__(THREADS, Shape<D, MT>::CTAS) kv8_attention_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(Shape<D, MT>::THREADS, Shape<D, MT>::CTAS) kv8_attention_kernel(const __grid_constant__ AttnArgs a) {
   using S = Shape<D, MT>;
-  grid_launch_dependents();
-  grid_dependency_wait();
+  constexpr int WARPS = S::WARPS, THREADS = S::THREADS;
+  // no early launch of the next kernel: its CTAs would take the places of this
+  // grid's as they free up, and those of the next call's grid would find some
+  // SMs full (48 ragged sequences: 50 us so, 64 us with it)
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int s_scan[WARPS];
   __shared__ int s_find[2];
@@ -207,126 +254,160 @@ __global__ void __launch_bounds__(THREADS, Shape<D, MT>::CTAS) kv8_attention_ker
   const uint32_t ring_u32 = smem_u32(ring);
   const uint4* sq = reinterpret_cast<const uint4*>(smem + S::OFF_Q) + mt * S::STEPS * 32 + lane;
 
-  // ---- the units of the sequences, and where this CTA's share begins
-  int total = 0, ctas = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    int base = 0;
-    const int u0 = pass ? first_unit(blockIdx.x, ctas, total) : 0;
-    for (int b0 = 0; b0 < v.num_seqs; b0 += THREADS) {
-      const int b = b0 + (int)threadIdx.x;
-      const int n = b < v.num_seqs ? sequence_units(a, b) : 0;
-      int inc = n;
+  // ---- the units of the sequences, and where this CTA's share begins: a
+  // thread counts the units of `run` neighbouring sequences
+  const int run = (v.num_seqs + THREADS - 1) / THREADS;
+  const int my_b0 = min((int)threadIdx.x * run, v.num_seqs), my_b1 = min(my_b0 + run, v.num_seqs);
+  int my_units = 0;
+  for (int b = my_b0; b < my_b1; ++b) my_units += sequence_units(a, b);
+  int inc = my_units;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-      }
-      __syncthreads();
-      if (lane == 31) s_scan[warp] = inc;
-      __syncthreads();
-      int before = base, all = 0;
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        if (w < warp) before += s_scan[w];
-        all += s_scan[w];
-      }
-      const int at = before + inc - n;
-      if (pass && n > 0 && at <= u0 && u0 < at + n) {
-        s_find[0] = b;
-        s_find[1] = at;
-      }
-      if (pass && blockIdx.x == 0 && b < v.num_seqs) a.prefix[b] = at;
-      base += all;
-    }
-    total = base;
-    ctas = min(a.ctas, total);
-    if (pass == 0 && (int)blockIdx.x >= max(ctas, 1)) return;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.prefix[v.num_seqs] = total;
-  if (total == 0) return;
+  if (lane == 31) s_scan[warp] = inc;
   __syncthreads();
+  int my_u0 = inc - my_units, total = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) my_u0 += s_scan[w];
+    total += s_scan[w];
+  }
+  const int ctas = sharing_ctas(a, total);
+  if ((int)blockIdx.x >= ctas) return;
   int u = first_unit(blockIdx.x, ctas, total);
   const int u_begin = u, u_end = first_unit(blockIdx.x + 1, ctas, total);
+  if (my_u0 <= u && u < my_u0 + my_units) {
+    int b = my_b0, at = my_u0;
+    for (int n; at + (n = sequence_units(a, b)) <= u; ++b) at += n;
+    s_find[0] = b;
+    s_find[1] = at;
+  }
+  __syncthreads();
   int b = s_find[0], seq_u0 = s_find[1];
 
-  while (u < u_end) {
-    const int len = kv8_len(v, b);
-    const Kv8Span span = kv8_rows(v, b);
-    const int su = segment_units(len), nseg = span.n ? segment_count(a, span.n) : 0;
-    if (u >= seq_u0 + nseg * su) {  // the next sequence that has rows
-      seq_u0 += nseg * su;
-      ++b;
-      continue;
+  // ---- the piece of work at hand
+  int len, g, p0, np, first, seg_end, ue, k0, mine;
+  Kv8Span span;
+  uint32_t at_next = 0;           // lane i: the place in the cache, in tiles, of the group's tile 32 n + i
+  float ks_all = 0.f, vs_all = 0.f;  // and its scales
+  constexpr int QP = S::PAIRS / WARPS, QV = (D + 127) / 128;
+  float4 x[QP][QV];               // the pairs' query rows, on their way
+
+  const int in_page = (1 << v.page_shift) / TILE - 1;
+  // (page ids out of range read page 0, and are flagged)
+  auto tile_of = [&](int i, size_t* scale_at) {
+    const int k = k0 + (kg + min(i, mine - 1) * S::GROUPS) * TILE;
+    const int page = max(kv8_page(v, b, k >> v.page_shift), 0);
+    *scale_at = kv8_scale_at(v, page, g);
+    return (uint32_t)(*scale_at << (v.page_shift - 5)) + (uint32_t)((k / TILE) & in_page);
+  };
+  // sends chunk n of the group (tile n / 2; its K, then its V) into the ring
+  auto send = [&](int n) {
+    if (n < 2 * mine) {
+      const int i = n >> 1;
+      if ((n & 63) == 0 && n) {
+        size_t scale_at;
+        at_next = tile_of(i + lane, &scale_at);
+      }
+      const uint32_t at = __shfl_sync(0xffffffffu, at_next, i & 31);
+      const int8_t* src = (n & 1 ? v.V : v.K) + (size_t)at * S::SLOT;
+      const uint32_t dst = ring_u32 + (n % S::SLOTS) * S::SLOT;
+#pragma unroll
+      for (int j = 0; j < S::CHUNKS; ++j) {
+        const int y = (j * MT + mt) * 32 + lane;
+        copy_async_16(dst + swizzled<D>(y) * 16, src + y * 16);
+      }
     }
-    const int seg = (u - seq_u0) / su, seg_u0 = seq_u0 + seg * su;
-    const int g = seg % v.kv_heads, p0 = seg / v.kv_heads * S::PAIRS, np = min(S::PAIRS, span.n * a.group - p0);
-    const int ue = min(u_end, seg_u0 + su);
-    const int k0 = (u - seg_u0) * UNIT, k1 = min(len, (ue - seg_u0) * UNIT);
+    copy_commit();
+  };
+  auto group_sync = [&] {
+    if (MT == 1)
+      __syncwarp();
+    else
+      named_sync(1 + kg, 32 * MT);
+  };
+  // the next piece of this CTA's share, if there is one: its first tiles and its query rows under way
+  auto begin = [&]() -> bool {
+    for (;;) {
+      if (u >= u_end) return false;
+      len = kv8_len(v, b);
+      span = kv8_rows(v, b);
+      const int su = segment_units(a, len), nseg = span.n ? segment_count(a, span.n) : 0;
+      if (u >= seq_u0 + nseg * su) {  // the next sequence that has rows
+        seq_u0 += nseg * su;
+        ++b;
+        continue;
+      }
+      const int seg = (u - seq_u0) / su, seg_u0 = seq_u0 + seg * su;
+      g = seg % v.kv_heads;
+      p0 = seg / v.kv_heads * S::PAIRS;
+      np = min(S::PAIRS, span.n * a.group - p0);
+      first = seg_u0 + overhead_units(D);  // the segment's first unit of positions
+      seg_end = seg_u0 + su;
+      ue = min(u_end, seg_end);
+      if (ue > first) break;
+      u = ue;  // nothing but overhead: the next CTA begins the segment
+    }
+    k0 = max(u - first, 0) * UNIT;
+    const int k1 = min(len, (ue - first) * UNIT);
     // this group's tiles: kg, kg + GROUPS, ... of the piece's
     const int tiles = k1 > k0 ? (k1 - k0 + TILE - 1) / TILE : 0;
-    const int mine = tiles > kg ? (tiles - kg + S::GROUPS - 1) / S::GROUPS : 0;
-
-    // a tile's place in the cache, in tiles: lane i has that of this group's
-    // tile 32 n + i (page ids out of range read page 0, and are flagged)
-    const int in_page = (1 << v.page_shift) / TILE - 1;
-    auto tile_of = [&](int i, size_t* scale_at) {
-      const int k = k0 + (kg + min(i, mine - 1) * S::GROUPS) * TILE;
-      const int page = max(kv8_page(v, b, k >> v.page_shift), 0);
-      *scale_at = kv8_scale_at(v, page, g);
-      return (uint32_t)(*scale_at << (v.page_shift - 5)) + (uint32_t)((k / TILE) & in_page);
-    };
-    uint32_t at_next = 0;
-    float ks_all = 0.f, vs_all = 0.f;
+    mine = tiles > kg ? (tiles - kg + S::GROUPS - 1) / S::GROUPS : 0;
     if (mine > 0) {
       size_t scale_at;
       at_next = tile_of(lane, &scale_at);
-      ks_all = __ldg(v.k_scale + scale_at);
-      vs_all = __ldg(v.v_scale + scale_at);
+      kv8_ready();
+      ks_all = v.k_scale[scale_at];
+      vs_all = v.v_scale[scale_at];
     }
-    // sends chunk n of the group (tile n / 2; its K, then its V) into the ring
-    auto send = [&](int n) {
-      if (n < 2 * mine) {
-        const int i = n >> 1;
-        if ((n & 63) == 0 && n) {
-          size_t scale_at;
-          at_next = tile_of(i + lane, &scale_at);
-        }
-        const uint32_t at = __shfl_sync(0xffffffffu, at_next, i & 31);
-        const int8_t* src = (n & 1 ? v.V : v.K) + (size_t)at * S::SLOT;
-        const uint32_t dst = ring_u32 + (n % S::SLOTS) * S::SLOT;
+    kv8_ready();
 #pragma unroll
-        for (int j = 0; j < S::CHUNKS; ++j) {
-          const int x = (j * MT + mt) * 32 + lane;
-          copy_async_16(dst + swizzled<D>(x) * 16, src + x * 16);
-        }
+    for (int i = 0; i < QP; ++i) {
+      const int p = warp + i * WARPS, pair = p0 + p;
+      const size_t row = span.r0 + pair / a.group, head = g * a.group + pair % a.group;
+#pragma unroll
+      for (int j = 0; j < QV; ++j) {
+        const int d = 128 * j + 4 * lane;
+        x[i][j] = p < np && d < D ? load4_any(a.q, a.type, row * a.ldq + head * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      copy_commit();
-    };
+    }
 #pragma unroll
     for (int n = 0; n < S::SLOTS - 1; ++n) send(n);
+    return true;
+  };
 
-    // ---- the pairs' query rows as fragments: row r of an M tile its fp16 hi, row r + 8 its lo
-    for (int p = warp; p < S::PAIRS; p += WARPS) {
-      const int pair = p0 + p;
-      const size_t row = span.r0 + pair / a.group, head = g * a.group + pair % a.group;
-      float4 x[(D + 127) / 128];
+  bool more = begin();
+  if (blockIdx.x == 0) {
+    int at = my_u0;
+    for (int b = my_b0; b < my_b1; ++b) {
+      a.prefix[b] = at;
+      at += sequence_units(a, b);
+    }
+    if (threadIdx.x == 0) a.prefix[v.num_seqs] = total;
+  }
+  while (more) {
+    // ---- the rows as fragments: row r of an M tile its fp16 hi, row r + 8 its lo
+#pragma unroll
+    for (int i = 0; i < QP; ++i) {
+      const int p = warp + i * WARPS;
       float top = 0.f;
 #pragma unroll
-      for (int j = 0; j < (D + 127) / 128; ++j) {
-        const int d = 128 * j + 4 * lane;
-        x[j] = p < np && d < D ? load4_any(a.q, a.type, row * a.ldq + head * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
-        top = fmaxf(top, fmaxf(fmaxf(fabsf(x[j].x), fabsf(x[j].y)), fmaxf(fabsf(x[j].z), fabsf(x[j].w))));
-      }
+      for (int j = 0; j < QV; ++j)
+        top = fmaxf(top, fmaxf(fmaxf(fabsf(x[i][j].x), fabsf(x[i][j].y)), fmaxf(fabsf(x[i][j].z), fabsf(x[i][j].w))));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // the power of two that brings the largest magnitude into [1, 2)
-      const int e = top > 0.f && top <= FLT_MAX ? ilogbf(top) : 0;
-      if (lane == 0) s_factor[p] = scalbnf(a.scale_log2, e);
+      // the power of two that brings the largest magnitude into [1, 2) (kept
+      // to 2^+-120: beyond, the row enters scaled less, its products still in range)
+      const int e = top <= FLT_MAX ? min(max((int)(__float_as_uint(top) >> 23) - 127, -120), 120) : 0;
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+      if (lane == 0) s_factor[p] = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
-      for (int j = 0; j < (D + 127) / 128; ++j) {
+      for (int j = 0; j < QV; ++j) {
         const int d = 128 * j + 4 * lane;
         if (d < D) {
-          const float4 y = make_float4(scalbnf(x[j].x, -e), scalbnf(x[j].y, -e), scalbnf(x[j].z, -e), scalbnf(x[j].w, -e));
+          const float4 y = make_float4(x[i][j].x * down, x[i][j].y * down, x[i][j].z * down, x[i][j].w * down);
           const uint32_t h0 = half2_bits(y.x, y.y), h1 = half2_bits(y.z, y.w);
           const float2 f0 = half2_values(h0), f1 = half2_values(h1);
           const int step = d / 64 * 4 + d % 16 / 4, col = d % 64 / 16;
@@ -353,20 +434,13 @@ __global__ void __launch_bounds__(THREADS, Shape<D, MT>::CTAS) kv8_attention_ker
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) sum[i][0] = sum[i][1] = 0.f;
 
-    auto group_sync = [&] {
-      if (MT == 1)
-        __syncwarp();
-      else
-        named_sync(1 + kg, 32 * MT);
-    };
-
 #pragma unroll 1
     for (int i = 0; i < mine; ++i) {
       if ((i & 31) == 0 && i) {
         size_t scale_at;
         tile_of(i + lane, &scale_at);
-        ks_all = __ldg(v.k_scale + scale_at);
-        vs_all = __ldg(v.v_scale + scale_at);
+        ks_all = v.k_scale[scale_at];
+        vs_all = v.v_scale[scale_at];
       }
       const float ks = __shfl_sync(0xffffffffu, ks_all, i & 31), vs = __shfl_sync(0xffffffffu, vs_all, i & 31);
       const int k = k0 + (kg + i * S::GROUPS) * TILE;
@@ -375,6 +449,12 @@ __global__ void __launch_bounds__(THREADS, Shape<D, MT>::CTAS) kv8_attention_ker
       copy_wait<S::SLOTS - 2>();
       group_sync();
       send(2 * i + S::SLOTS - 1);
+      if (MT > 1 && 8 * mt >= np) {  // no pair of this warp's M tile: it only copies
+        copy_wait<S::SLOTS - 2>();
+        group_sync();
+        send(2 * i + S::SLOTS);
+        continue;
+      }
       const uint8_t* kt = ring + (2 * i) % S::SLOTS * S::SLOT;
       float s[4][4];
 #pragma unroll
@@ -497,17 +577,20 @@ __global__ void __launch_bounds__(THREADS, Shape<D, MT>::CTAS) kv8_attention_ker
         }
       }
     }
-    copy_wait<0>();
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
+    group_sync();  // every warp of the group is done with the ring
 
-    // ---- the warps' sums together, in order, through the ring's memory
-    __syncthreads();
-    float* merge = reinterpret_cast<float*>(smem);  // [warp][8][D]
-    const float m_own = ref == -INFINITY ? -INFINITY : ref - HEADROOM;
-    if (c == 0) s_ml[warp][r] = make_float2(m_own, l);
+    // ---- the next piece begins while the warps' sums of this one are added up, in order
+    const bool whole = u <= first && ue == seg_end;
+    const int done_np = np, done_g = g, done_p0 = p0, done_r0 = span.r0;
+    const size_t slot = (size_t)(2 * blockIdx.x + (u_begin > first ? 0 : 1)) * S::PAIRS;
+    u = ue;
+    more = begin();
+    auto merge = [&](int w) { return reinterpret_cast<float*>(smem + S::OFF_M + w * S::M_STEP); };  // warp w's [8][D]
+    if (c == 0) s_ml[warp][r] = make_float2(ref == -INFINITY ? -INFINITY : ref - HEADROOM, l);
     {
-      float* to = merge + ((size_t)warp * 8 + r) * D;
+      float* to = merge(warp) + r * D;
       constexpr int COLS = D >= 128 ? 16 : 8;
 #pragma unroll
       for (int dc = 0; dc < (D + 127) / 128; ++dc)
@@ -520,114 +603,110 @@ __global__ void __launch_bounds__(THREADS, Shape<D, MT>::CTAS) kv8_attention_ker
                             sum[COLS * dc + i + 3][h]);
     }
     __syncthreads();
-    const bool whole = u == seg_u0 && ue == seg_u0 + su;
-    const size_t slot = (size_t)(2 * blockIdx.x + (u_begin > seg_u0 ? 0 : 1)) * S::PAIRS;
-    for (int p = warp; p < np; p += WARPS) {
-      float m = -INFINITY;
+    for (int i = threadIdx.x; i < done_np * (D / 4); i += THREADS) {
+      const int p = i / (D / 4), d = 4 * (i % (D / 4));
+      float m = -INFINITY, all = 0.f;
 #pragma unroll
       for (int w = 0; w < S::GROUPS; ++w) m = fmaxf(m, s_ml[w * MT + p / 8][p % 8].x);
       if (m == -INFINITY) m = 0.f;
-      float total_l = 0.f, f[S::GROUPS];
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < S::GROUPS; ++w) {
         const float2 ml = s_ml[w * MT + p / 8][p % 8];
-        f[w] = ml.y > 0.f || ml.y != ml.y ? exp2f(ml.x == -INFINITY ? 0.f : ml.x - m) : 0.f;
-        total_l = fmaf(f[w], ml.y, total_l);
+        const float f = piece_factor(ml, m);
+        const float4 y = *reinterpret_cast<const float4*>(merge(w * MT + p / 8) + (p % 8) * D + d);
+        all = fmaf(f, ml.y, all);
+        o = make_float4(fmaf(f, y.x, o.x), fmaf(f, y.y, o.y), fmaf(f, y.z, o.z), fmaf(f, y.w, o.w));
       }
-      const float inv = total_l > 0.f || total_l != total_l ? 1.f / total_l : 0.f;
-      const size_t row = span.r0 + (p0 + p) / a.group, head = g * a.group + (p0 + p) % a.group;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const int d = 32 * i + lane;
-        float o = 0.f;
-#pragma unroll
-        for (int w = 0; w < S::GROUPS; ++w) o = fmaf(f[w], merge[((size_t)(w * MT + p / 8) * 8 + p % 8) * D + d], o);
-        if (whole)
-          store_any(a.out, a.type, row * a.ldo + head * D + d, o * inv);
-        else
-          a.part_o[(slot + p) * D + d] = o;
-      }
-      if (lane == 0) {
-        if (!whole)
-          a.part_ml[slot + p] = make_float2(m, total_l);
-        else if (a.final_ml)
-          a.final_ml[row * a.heads + head] = make_float2(m, inv);
+      if (whole) {
+        finish4(a, done_r0 + (done_p0 + p) / a.group, done_g * a.group + (done_p0 + p) % a.group, D, d, o, m, all);
+      } else {
+        if (d == 0) a.part_ml[slot + p] = make_float2(m, all);
+        *reinterpret_cast<float4*>(a.part_o + (slot + p) * D + d) = o;
       }
     }
-    __syncthreads();
-    u = ue;
+    // (the fragments are written, and synchronised on, before the last slots are sent into again)
   }
 }
 
-// The pieces of each segment that more than one CTA had: a warp for each
-// (row, head), pieces in order.
-template <int D>
-__global__ void __launch_bounds__(256) kv8_combine_kernel(const AttnArgs a) {
-  grid_launch_dependents();
-  grid_dependency_wait();
+// The pieces of the segments that more than one CTA had. A CTA for each (row,
+// head): D / 4 threads take four dims each of every GROUPS-th piece, so that
+// the loads are under way at once, then add up.
+template <int D, int GROUPS>
+__global__ void __launch_bounds__(D / 4 * GROUPS) kv8_combine_kernel(const __grid_constant__ AttnArgs a) {
+  constexpr int LANES = D / 4;
+  __shared__ float4 s_o[GROUPS][LANES];
+  __shared__ float2 s_ml[GROUPS];
   const Kv8View& v = a.v;
-  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  const int b = blockIdx.y, g = (int)(blockIdx.x % v.kv_heads), pair = (int)(blockIdx.x / v.kv_heads);
+  const int su = segment_units(a, kv8_len(v, b));
   const Kv8Span span = kv8_rows(v, b);
-  const int id = (int)blockIdx.x * 8 + ((int)threadIdx.x >> 5);  // pair * kv_heads + g
-  const int g = id % v.kv_heads, pair = id / v.kv_heads;
+  kv8_ready();
+  grid_launch_dependents();
+  const int total = a.prefix[v.num_seqs], seq_u0 = a.prefix[b];
   if (pair >= span.n * a.group) return;
-  const int total = a.prefix[v.num_seqs], ctas = min(a.ctas, total), su = segment_units(kv8_len(v, b));
-  const int u0 = a.prefix[b] + (pair / a.pairs * v.kv_heads + g) * su;
-  const int c0 = cta_of(u0, ctas, total), c1 = cta_of(u0 + su - 1, ctas, total);
-  if (c0 == c1) return;
-  // the first CTA wrote it as the segment it began, the others as the one they continued
-  auto slot = [&](int c) { return (size_t)(c == c0 ? 2 * c + 1 : 2 * c) * a.pairs + pair % a.pairs; };
-  float m = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) {
-    const float2 ml = a.part_ml[slot(c)];
-    if (ml.y > 0.f) m = fmaxf(m, ml.x);
+  const int u0 = seq_u0 + (pair / a.pairs * v.kv_heads + g) * su, ctas = sharing_ctas(a, total);
+  const int c0 = cta_of(u0 + overhead_units(D), ctas, total), n = cta_of(u0 + su - 1, ctas, total) - c0 + 1;
+  if (n == 1) return;
+  const int group = threadIdx.x / LANES, d = 4 * (threadIdx.x % LANES);
+  float m = -INFINITY, all = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto take = [&](float2 ml, const float4& x) {  // the reference follows the largest so far
+    const float now = ml.y > 0.f ? fmaxf(m, ml.x) : m;
+    const float keep = m == now ? 1.f : exp2f(m - now), f = piece_factor(ml, now);
+    m = now;
+    all = fmaf(f, ml.y, all * keep);
+    o = make_float4(fmaf(f, x.x, o.x * keep), fmaf(f, x.y, o.y * keep), fmaf(f, x.z, o.z * keep),
+                    fmaf(f, x.w, o.w * keep));
+  };
+#pragma unroll 8
+  for (int i = group; i < n; i += GROUPS) {
+    // the first CTA wrote it as the segment that it began, the others as the one that they continued
+    const size_t slot = (size_t)(2 * (c0 + i) + (i == 0)) * a.pairs + pair % a.pairs;
+    take(a.part_ml[slot], *reinterpret_cast<const float4*>(a.part_o + slot * D + d));
   }
+  s_o[group][threadIdx.x % LANES] = o;
+  if (threadIdx.x % LANES == 0) s_ml[group] = make_float2(m, all);
+  __syncthreads();
+  if (group != 0) return;
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-  if (m == -INFINITY) m = 0.f;
-  float l = 0.f, o[D / 32];
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const float2 ml = a.part_ml[slot(c)];
-    const float f = ml.y > 0.f || ml.y != ml.y ? exp2f(ml.x - m) : 0.f;
-    l = fmaf(f, ml.y, l);
-    const float* po = a.part_o + slot(c) * D;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] = fmaf(f, po[32 * i + lane], o[i]);
-  }
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-  const int row = span.r0 + pair / a.group, head = g * a.group + pair % a.group;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i)
-    store_any(a.out, a.type, (size_t)row * a.ldo + (size_t)head * D + 32 * i + lane, o[i] * inv);
-  if (a.final_ml && lane == 0) a.final_ml[(size_t)row * a.heads + head] = make_float2(m, inv);
+  for (int i = 1; i < GROUPS; ++i) take(s_ml[i], s_o[i][threadIdx.x]);
+  finish4(a, span.r0 + pair / a.group, g * a.group + pair % a.group, D, d, o, m == -INFINITY ? 0.f : m, all);
 }
 
-// w_j: a thread for each position of a sequence and KV head, its pairs in order.
-__global__ void __launch_bounds__(256) kv8_weights_kernel(const AttnArgs a) {
-  grid_launch_dependents();
-  grid_dependency_wait();
+// w_j: a thread for each four positions of a sequence and KV head, its pairs in order.
+__global__ void __launch_bounds__(128) kv8_weights_kernel(const __grid_constant__ AttnArgs a) {
   const Kv8View& v = a.v;
   const int g = blockIdx.y, b = blockIdx.z;
-  const long long j = (long long)blockIdx.x * 256 + threadIdx.x;
   const int len = kv8_len(v, b);
   const Kv8Span span = kv8_rows(v, b);
+  kv8_ready();
+  grid_launch_dependents();
+  const long long j = ((long long)blockIdx.x * 128 + threadIdx.x) * 4;
   if (j >= a.weights_ld || (a.accumulate && j >= len)) return;
-  float* w = a.weights + ((size_t)b * v.kv_heads + g) * a.weights_ld + j;
-  float sum = 0.f;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
   if (j < len) {
-    for (int i = 0; i < span.n; ++i)
-#pragma unroll 4
+    for (int i = 0; i < span.n; ++i) {
+      const size_t at = (size_t)(span.r0 + i) * a.heads + g * a.group;
+#pragma unroll 8
       for (int h = 0; h < a.group; ++h) {
-        const size_t at = (size_t)(span.r0 + i) * a.heads + g * a.group + h;
-        const float2 ml = a.final_ml[at];
-        sum += exp2f(a.scores[at * a.scores_ld + j] - ml.x) * ml.y;
+        const float2 ml = a.final_ml[at + h];
+        const float4 s = __ldcg(reinterpret_cast<const float4*>(a.scores + (at + h) * a.scores_ld + j));
+        sum[0] = fmaf(exp2_fast(s.x - ml.x), ml.y, sum[0]);
+        sum[1] = fmaf(exp2_fast(s.y - ml.x), ml.y, sum[1]);
+        sum[2] = fmaf(exp2_fast(s.z - ml.x), ml.y, sum[2]);
+        sum[3] = fmaf(exp2_fast(s.w - ml.x), ml.y, sum[3]);
       }
-    if (a.accumulate && j < len - span.n) sum += *w;
+    }
   }
-  *w = sum;
+  float* w = a.weights + ((size_t)b * v.kv_heads + g) * a.weights_ld + j;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    if (j + t >= a.weights_ld || (a.accumulate && j + t >= len)) break;
+    float x = j + t < len ? sum[t] : 0.f;
+    if (a.accumulate && j + t < len - span.n) x += w[t];
+    w[t] = x;
+  }
 }
 
 struct Layout {
@@ -642,17 +721,16 @@ int m_tiles(const Kv8View& v, const Kv8Attention& a) {
   return pairs <= 8 ? 1 : (pairs <= 16 ? 2 : 4);
 }
 
-// CTAs that run at once: one or two an SM (Shape::CTAS).
-int resident_ctas(int dim) { return (dim <= 128 ? 2 : 1) * num_sms(); }
+int resident_ctas(int dim, int mt) { return ctas_per_sm(dim, mt) * num_sms(); }
 
 int scores_ld(const Kv8View& v) { return (int)(((long long)v.max_len + TILE - 1) / TILE * TILE); }
 
 Layout layout_of(const Kv8View& v, const Kv8Attention& a) {
   Layout l;
   l.mt = m_tiles(v, a);
-  const int group = a.heads / v.kv_heads, pairs = 8 * l.mt, most_ctas = resident_ctas(v.dim);
+  const int group = a.heads / v.kv_heads, pairs = 8 * l.mt, most_ctas = resident_ctas(v.dim, l.mt);
   const long long segs = ((long long)v.num_rows * group / pairs + v.num_seqs) * v.kv_heads;  // at most
-  const long long most = segs * (v.max_len / UNIT + 1);
+  const long long most = segs * (v.max_len / UNIT + 1 + overhead_units(v.dim));
   l.ctas = (int)(most < most_ctas ? most : most_ctas);
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -683,7 +761,7 @@ cudaError_t launch_shape(const AttnArgs& a, cudaStream_t s) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.ctas);
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(S::THREADS);
   cfg.dynamicSmemBytes = S::BYTES;
   cfg.stream = s;
   cudaLaunchAttribute attr[1] = {pdl_attr()};
@@ -691,14 +769,21 @@ cudaError_t launch_shape(const AttnArgs& a, cudaStream_t s) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kv8_attention_kernel<D, MT>, a);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)(((long long)a.v.max_rows * a.heads + 7) / 8), (unsigned)a.v.num_seqs);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3((unsigned)((long long)a.v.max_rows * a.heads), (unsigned)a.v.num_seqs);
   cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, kv8_combine_kernel<D>, a);
+  // few (row, head) pairs have many pieces each; of many pairs most are whole or in two pieces
+  if ((long long)a.v.num_rows * a.heads <= 4 * num_sms()) {
+    cfg.blockDim = dim3(D / 4 * 8);
+    e = cudaLaunchKernelEx(&cfg, kv8_combine_kernel<D, 8>, a);
+  } else {
+    cfg.blockDim = dim3(D / 4 * 2);
+    e = cudaLaunchKernelEx(&cfg, kv8_combine_kernel<D, 2>, a);
+  }
   if (e != cudaSuccess || !a.weights) return e;
   const long long span = a.accumulate ? a.v.max_len : a.weights_ld;
   if (span == 0) return cudaSuccess;
-  cfg.gridDim = dim3((unsigned)((span + 255) / 256), (unsigned)a.v.kv_heads, (unsigned)a.v.num_seqs);
+  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3((unsigned)((span + 511) / 512), (unsigned)a.v.kv_heads, (unsigned)a.v.num_seqs);
   return cudaLaunchKernelEx(&cfg, kv8_weights_kernel, a);
 }
 

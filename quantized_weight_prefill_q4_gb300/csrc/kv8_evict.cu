@@ -79,8 +79,8 @@ struct EvictArgs {
 };
 
 __global__ void __launch_bounds__(S_THREADS) kv8_select_kernel(Kv8View v, EvictArgs a) {
-  grid_launch_dependents();
-  grid_dependency_wait();
+  kv8_ready();
+  grid_launch_dependents();  // of the move, which waits for this grid's end and lets nothing start before its own
   __shared__ uint32_t hist[S_BINS];
   __shared__ uint32_t chosen[2];  // the round's bin, and how many of it are kept
   __shared__ uint32_t counts[2];  // this CTA's keys above the border, and equal to it
@@ -227,8 +227,7 @@ constexpr int M_THREADS = 256;
 constexpr int M_PAGE = 256;  // most tokens of a page
 
 __global__ void __launch_bounds__(M_THREADS) kv8_move_kernel(Kv8View v, EvictArgs a) {
-  grid_launch_dependents();
-  grid_dependency_wait();
+  kv8_ready();
   __shared__ const int8_t* row_codes[M_PAGE];
   __shared__ float row_scale[M_PAGE];
   __shared__ float s_max[M_THREADS / 32];

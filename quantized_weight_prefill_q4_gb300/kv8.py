@@ -8,7 +8,6 @@ and a nonzero status raises :class:`~.capi.AprError`.
 from __future__ import annotations
 
 import ctypes
-from dataclasses import dataclass
 
 import torch
 
@@ -72,42 +71,48 @@ _lib = _bind()
 
 def _array(x, name, dtype, dims):
     """A contiguous CUDA tensor of the type and number of dimensions, checked."""
+    if isinstance(x, torch.Tensor) and x.is_cuda and x.dtype is dtype and x.dim() == dims and x.is_contiguous():
+        return x
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name}: expected a CUDA tensor, got {type(x).__name__}")
     if not x.is_cuda:
         raise ValueError(f"{name}: tensor is on {x.device}, the library takes device memory")
     if x.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype}, got {x.dtype}")
-    if x.dim() != dims or not x.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor of {dims} dimensions, got shape {tuple(x.shape)}")
-    return x
+    raise ValueError(f"{name}: expected a contiguous tensor of {dims} dimensions, got shape {tuple(x.shape)}")
 
 
-@dataclass
+def _stream(stream, device_index):
+    """The raw stream: the given one, or torch's current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device_index)
+    return capi._stream(stream)
+
+
 class Kv8Cache:
     """The cache's arrays: codes K and V int8 [pages][kv_heads][page_tokens][head_dim],
     scales k_scale and v_scale float32 [pages][kv_heads], all contiguous."""
 
-    K: torch.Tensor
-    V: torch.Tensor
-    k_scale: torch.Tensor
-    v_scale: torch.Tensor
+    __slots__ = ("K", "V", "k_scale", "v_scale", "kv_heads", "page_tokens", "head_dim", "device_index", "_c")
 
-    def __post_init__(self):
-        K = _array(self.K, "K", torch.int8, 4)
-        _array(self.V, "V", torch.int8, 4)
-        _array(self.k_scale, "k_scale", torch.float32, 2)
-        _array(self.v_scale, "v_scale", torch.float32, 2)
-        if self.V.shape != K.shape or self.k_scale.shape != K.shape[:2] or self.v_scale.shape != K.shape[:2]:
+    def __init__(self, K, V, k_scale, v_scale):
+        shape = _array(K, "K", torch.int8, 4).shape
+        if (_array(V, "V", torch.int8, 4).shape != shape
+                or _array(k_scale, "k_scale", torch.float32, 2).shape != shape[:2]
+                or _array(v_scale, "v_scale", torch.float32, 2).shape != shape[:2]):
             raise ValueError("Kv8Cache: V, k_scale and v_scale must match K's pages, heads, tokens and head_dim")
-        pages, heads, tokens, dim = K.shape
-        self._c = _Cache(K.data_ptr(), self.V.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(), pages,
-                         heads, tokens, dim)
+        self.K, self.V, self.k_scale, self.v_scale = K, V, k_scale, v_scale
+        pages, self.kv_heads, self.page_tokens, self.head_dim = shape
+        self.device_index = K.get_device()
+        self._c = _Cache(K.data_ptr(), V.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, self.kv_heads,
+                         self.page_tokens, self.head_dim)
 
     @classmethod
     def allocate(cls, num_pages, num_kv_heads, head_dim, page_tokens=64, device="cuda"):
         """A cache of num_pages pages (zeros)."""
         codes = (num_pages, num_kv_heads, page_tokens, head_dim)
+        if torch.device(device).type != "cuda":
+            raise ValueError(f"Kv8Cache: the library takes device memory, got {device}")
         return cls(torch.zeros(codes, dtype=torch.int8, device=device),
                    torch.zeros(codes, dtype=torch.int8, device=device),
                    torch.zeros(codes[:2], dtype=torch.float32, device=device),
@@ -133,20 +138,19 @@ def _matrix(x, name, width, like=None):
     if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype not in _TYPES:
         raise ValueError(f"{name}: expected a float32, float16 or bfloat16 CUDA tensor")
     shape, stride = x.shape, x.stride()
-    dense = (x.dim() == 2 and shape[1] == width and (width == 1 or stride[1] == 1)) or (
-        x.dim() == 3 and shape[1] * shape[2] == width and stride[2] == 1 and (shape[1] == 1 or stride[1] == shape[2]))
+    rows = shape[0] if shape else 0
+    dense = (len(shape) == 2 and shape[1] == width and stride[1] == 1) or (
+        len(shape) == 3 and shape[1] * shape[2] == width and stride[2] == 1 and (shape[1] == 1 or stride[1] == shape[2]))
     if not dense:
         raise ValueError(f"{name}: expected rows of {width} consecutive elements, got shape {tuple(shape)}, "
                          f"strides {tuple(stride)}")
-    if like is not None and (x.dtype != like.dtype or shape[0] != like.shape[0]):
-        raise ValueError(f"{name}: expected {like.shape[0]} rows of {like.dtype}, got {shape[0]} of {x.dtype}")
-    rows = shape[0]
-    ld = stride[0] if rows > 1 else width
-    return x.data_ptr(), rows, ld
+    if like is not None and (x.dtype is not like.dtype or rows != like.shape[0]):
+        raise ValueError(f"{name}: expected {like.shape[0]} rows of {like.dtype}, got {rows} of {x.dtype}")
+    return x.data_ptr(), rows, stride[0] if rows > 1 else width
 
 
 def _k_and_v(cache, k, v):
-    width = cache.K.shape[1] * cache.K.shape[3]
+    width = cache.kv_heads * cache.head_dim
     kp, rows, ld = _matrix(k, "k", width)
     vp, _, vld = _matrix(v, "v", width, like=k)
     if vld != ld and rows > 1:
@@ -160,7 +164,7 @@ def apr_kv8_append(cache, page_table, lens, k, v, *, row_start=None, max_rows=0,
     lens counts them already. row_start None: one row a sequence."""
     kp, vp, n, ld = _k_and_v(cache, k, v)
     rows = _rows(page_table, lens, row_start, n, max_rows, 0)
-    return capi._check(_lib.apr_kv8_append(cache._c, rows, _TYPES[k.dtype], kp, vp, ld, capi._stream(stream)))
+    return capi._check(_lib.apr_kv8_append(cache._c, rows, _TYPES[k.dtype], kp, vp, ld, _stream(stream, cache.device_index)))
 
 
 def apr_kv8_read(cache, page_table, lens, k, v, *, row_start=None, max_rows=0, stream=None) -> int:
@@ -168,7 +172,7 @@ def apr_kv8_read(cache, page_table, lens, k, v, *, row_start=None, max_rows=0, s
     and strides as for the append)."""
     kp, vp, n, ld = _k_and_v(cache, k, v)
     rows = _rows(page_table, lens, row_start, n, max_rows, 0)
-    return capi._check(_lib.apr_kv8_read(cache._c, rows, _TYPES[k.dtype], kp, vp, ld, capi._stream(stream)))
+    return capi._check(_lib.apr_kv8_read(cache._c, rows, _TYPES[k.dtype], kp, vp, ld, _stream(stream, cache.device_index)))
 
 
 def apr_kv8_attention(cache, page_table, lens, q, out, num_heads, *, row_start=None, max_rows=0, max_len=0, scale=0.0,
@@ -177,18 +181,18 @@ def apr_kv8_attention(cache, page_table, lens, q, out, num_heads, *, row_start=N
     over its cache, which holds their own k and v; out has q's type. weights
     ([sequences][kv_heads][>= max_len] float32) receives, or with accumulate
     adds, the weight of each position. max_len bounds lens (0: the table)."""
-    width = num_heads * cache.K.shape[3]
+    width = num_heads * cache.head_dim
     qp, n, ldq = _matrix(q, "q", width)
     op, _, ldo = _matrix(out, "out", width, like=q)
     rows = _rows(page_table, lens, row_start, n, max_rows, max_len)
     wp, wld = None, 0
     if weights is not None:
         _array(weights, "weights", torch.float32, 3)
-        if weights.shape[0] != lens.numel() or weights.shape[1] != cache.K.shape[1]:
-            raise ValueError(f"weights: expected [{lens.numel()}][{cache.K.shape[1]}][...], got {tuple(weights.shape)}")
+        if weights.shape[0] != lens.numel() or weights.shape[1] != cache.kv_heads:
+            raise ValueError(f"weights: expected [{lens.numel()}][{cache.kv_heads}][...], got {tuple(weights.shape)}")
         wp, wld = weights.data_ptr(), weights.shape[2]
     return capi._check(_lib.apr_kv8_attention(cache._c, rows, _TYPES[q.dtype], qp, ldq, op, ldo, num_heads, scale, wp,
-                                              wld, int(accumulate), capi._stream(stream)))
+                                              wld, int(accumulate), _stream(stream, cache.device_index)))
 
 
 def apr_kv8_evict(cache, page_table, lens, weights, budget, recent, fresh_pages, table_out, lens_out, weights_out, kept,
@@ -198,7 +202,7 @@ def apr_kv8_evict(cache, page_table, lens, weights, budget, recent, fresh_pages,
     ([sequences][ceil(budget / page_tokens)]); table_out, lens_out, weights_out
     ([sequences][kv_heads][>= budget]) and kept ([sequences][kv_heads][budget])
     say what the sequences are afterwards."""
-    heads, tokens = cache.K.shape[1], cache.K.shape[2]
+    heads, tokens = cache.kv_heads, cache.page_tokens
     rows = _rows(page_table, lens, None, 0, 0, max_len)
     n = lens.numel()
     want = {
@@ -216,4 +220,4 @@ def apr_kv8_evict(cache, page_table, lens, weights, budget, recent, fresh_pages,
     return capi._check(_lib.apr_kv8_evict(cache._c, rows, weights.data_ptr(), weights.shape[2], budget, recent,
                                           fresh_pages.data_ptr(), table_out.data_ptr(), lens_out.data_ptr(),
                                           weights_out.data_ptr(), weights_out.shape[2], kept.data_ptr(),
-                                          capi._stream(stream)))
+                                          _stream(stream, cache.device_index)))
