@@ -28,10 +28,11 @@ struct Kv8View {
 
 // Every kernel of the cache is launched before the work ahead of it is done
 // and waits here for it. What it reads before are the index arrays alone (lens,
-// row_start, page_table): no kernel of the library writes those but the
+// row_start, page_table, fresh_pages): no kernel of the library writes those but the
 // eviction's, which let nothing start before they have ended, and a kernel
 // that lets the next one start early does so after its own wait, so that all
-// work but its own is done by then.
+// work but its own is done by then. Every grid waits somewhere, whatever it
+// finds to do: what is launched behind it relies on that.
 __device__ __forceinline__ void kv8_ready() { grid_dependency_wait(); }
 
 __device__ __forceinline__ void kv8_flag(const Kv8View& v) { atomicOr(v.status, kStatusBadIndex); }
@@ -75,29 +76,62 @@ __device__ __forceinline__ size_t kv8_codes_at(const Kv8View& v, int page, int g
 }
 
 // ---------------------------------------------------------------- elements
+// Eight consecutive elements of a row, on a 16-byte boundary.
 template <typename T>
-__device__ __forceinline__ float to_f32(T x);
+struct Vec8;
 template <>
-__device__ __forceinline__ float to_f32<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_f32<__half>(__half x) { return __half2float(x); }
-template <>
-__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-
-template <typename T>
-__device__ __forceinline__ T from_f32(float x);
-template <>
-__device__ __forceinline__ float from_f32<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-
-// N consecutive elements on a 16-byte boundary (N * sizeof(T) a multiple of 16)
-template <typename T, int N>
-struct alignas(16) Elems {
-  T x[N];
+struct Vec8<float> {
+  float4 a, b;
 };
+template <>
+struct Vec8<__half> {
+  uint4 a;
+};
+template <>
+struct Vec8<__nv_bfloat16> {
+  uint4 a;
+};
+__device__ __forceinline__ Vec8<float> load8(const float* p) {
+  const float4* q = reinterpret_cast<const float4*>(p);
+  return Vec8<float>{q[0], q[1]};
+}
+__device__ __forceinline__ Vec8<__half> load8(const __half* p) {
+  return Vec8<__half>{*reinterpret_cast<const uint4*>(p)};
+}
+__device__ __forceinline__ Vec8<__nv_bfloat16> load8(const __nv_bfloat16* p) {
+  return Vec8<__nv_bfloat16>{*reinterpret_cast<const uint4*>(p)};
+}
+__device__ __forceinline__ void values8(const Vec8<float>& e, float (&x)[8]) {
+  x[0] = e.a.x, x[1] = e.a.y, x[2] = e.a.z, x[3] = e.a.w;
+  x[4] = e.b.x, x[5] = e.b.y, x[6] = e.b.z, x[7] = e.b.w;
+}
+__device__ __forceinline__ void values8(const Vec8<__half>& e, float (&x)[8]) {
+  const uint32_t w[4] = {e.a.x, e.a.y, e.a.z, e.a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    x[2 * i] = f.x, x[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void values8(const Vec8<__nv_bfloat16>& e, float (&x)[8]) {
+  const uint32_t w[4] = {e.a.x, e.a.y, e.a.z, e.a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+}
+
+// Two float32 values as two 16-bit ones.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
 
 // ---------------------------------------------------------------- codes
 // The scale of a page and head whose largest finite magnitude is amax: the
@@ -110,30 +144,94 @@ __device__ __forceinline__ float finite_abs(float x) {
   return a <= FLT_MAX ? a : 0.f;
 }
 
-// x / s decided in 64 bits. A quotient of two float32 values that is not a
-// half itself is further from one than 64-bit division rounds by.
-static __device__ __noinline__ float kv8_round_exact(float x, float s) {
-  return (float)fmin(fmax(rint((double)x / (double)s), -127.0), 127.0);
+// rint(x / s) clamped to +-127; NaN 0, infinities +-127, 0 under s = 0. The
+// quotient is taken in 64 bits: one of two float32 values that is not a half
+// itself is further from one than 64-bit division rounds by.
+static __device__ __noinline__ uint32_t kv8_code(float x, float s) {
+  if (!(s > 0.f) || x != x) return 0;
+  return (uint32_t)(int)fmin(fmax(rint((double)x / (double)s), -127.0), 127.0);
 }
 
-// rint(x / s) clamped to +-127, inv = 1 / s. The float32 product x * inv is
-// within 3e-5 of the quotient; only where that leaves the rounding open (one
-// value in about 5000) is the quotient taken in 64 bits.
-__device__ __forceinline__ int kv8_code(float x, float s, float inv) {
-  if (!(s > 0.f)) return 0;
-  const float f = x * inv;
-  if (!(fabsf(f) < 128.f) || s < 1e-37f)  // infinities, NaN, scales whose reciprocal is not a normal number
-    return x != x ? 0 : (fabsf(x) <= FLT_MAX ? (int)kv8_round_exact(x, s) : (x > 0.f ? 127 : -127));
-  float r = rintf(f);
-  if (fabsf(f - r) > 0.4999f) r = kv8_round_exact(x, s);
-  return (int)fminf(fmaxf(r, -127.f), 127.f);
+// Bytes i and i + 1 of a word, exclusive-or'ed with 0x80808080, as float32
+// values: 2^23 + (code + 128) less what was added.
+__device__ __forceinline__ float2 kv8_bytes_f32(uint32_t biased, int i) {
+  return __fadd2_rn(make_float2(__uint_as_float(__byte_perm(biased, 0x4b000000u, 0x7540u + i)),
+                                __uint_as_float(__byte_perm(biased, 0x4b000000u, 0x7541u + i))),
+                    make_float2(-8388736.f, -8388736.f));
 }
 
-// Four codes as one word, the first in the lowest byte.
-__device__ __forceinline__ uint32_t kv8_pack4(int a, int b, int c, int d) {
-  return (uint32_t)(a & 255) | ((uint32_t)(b & 255) << 8) | ((uint32_t)(c & 255) << 16) | ((uint32_t)d << 24);
+// A scale with what rounding under it takes. (Halves and reciprocals of the
+// smallest numbers are not exact, or not numbers: half = -1 leaves all to kv8_code.)
+struct Kv8Scale {
+  float s, inv, half;
+};
+__device__ __forceinline__ Kv8Scale kv8_rounding_to(float s) {
+  return Kv8Scale{s, __fdiv_rn(1.0f, s), s >= 1e-37f ? 0.5f * s : -1.f};
 }
-// Byte i of a word of codes, as a signed number.
-__device__ __forceinline__ int kv8_byte(uint32_t w, int i) { return (int)(int8_t)(w >> (8 * i)); }
+
+// The fast way to rint(x / s), two values at a time: x * (1 / s) added to
+// 1.5 * 2^23 rounds to a whole number w, and the sum's low byte is the code.
+// Where w is nearest to the exact quotient, x - w s is less than s / 2, and one
+// fma gives it exactly (it is a multiple of half the scale's last bit, below
+// 2^24 of them). `open` says where it is not less, or not a number: a tie, or a
+// product that rounded across one (one float32 value in 10^5, but one bf16 value
+// in 200, whose quotients by the largest of them often lie next to a half).
+__device__ __forceinline__ uint2 kv8_round_sums(float2 x, const Kv8Scale& k, bool& open) {
+  const float2 sum = __ffma2_rn(x, make_float2(k.inv, k.inv), make_float2(12582912.f, 12582912.f));
+  const float2 w = __fadd2_rn(sum, make_float2(-12582912.f, -12582912.f));
+  const float2 r = __ffma2_rn(w, make_float2(-k.s, -k.s), x);
+  open |= !(fabsf(r.x) < k.half) || !(fabsf(r.y) < k.half);
+  return make_uint2(__float_as_uint(sum.x), __float_as_uint(sum.y));
+}
+// The same settled: one more or less where x - w s is over s / 2, or at it and w odd.
+__device__ __forceinline__ uint32_t kv8_round_settled(uint32_t sum, float x, const Kv8Scale& k) {
+  if (!(k.half > 0.f && fabsf(x) <= FLT_MAX)) return kv8_code(x, k.s);
+  const float r = fmaf(-(__uint_as_float(sum) - 12582912.f), k.s, x), a = fabsf(r);
+  return a > k.half || (a == k.half && (sum & 1)) ? (r > 0.f ? sum + 1 : sum - 1) : sum;
+}
+// The low bytes of four words as one.
+__device__ __forceinline__ uint32_t kv8_low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+// Codes of eight values of magnitude up to 127 s (1 + 2^-23).
+__device__ __forceinline__ uint2 kv8_codes8(const float (&x)[8], const Kv8Scale& k) {
+  bool open = false;
+  uint2 r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = kv8_round_sums(make_float2(x[2 * i], x[2 * i + 1]), k, open);
+  if (open) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      r[i] = make_uint2(kv8_round_settled(r[i].x, x[2 * i], k), kv8_round_settled(r[i].y, x[2 * i + 1], k));
+  }
+  return make_uint2(kv8_low_bytes(r[0].x, r[0].y, r[1].x, r[1].y), kv8_low_bytes(r[2].x, r[2].y, r[3].x, r[3].y));
+}
+
+// Four codes under the scale `from` as codes under k.s, of values of magnitude
+// up to 127 s (1 + 2^-23): rint(float32(code * from) / s).
+static __device__ __noinline__ uint32_t kv8_requantise4_settled(uint32_t biased, float from, Kv8Scale k) {
+  bool open = false;
+  uint2 r[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 x = __fmul2_rn(kv8_bytes_f32(biased, 2 * i), make_float2(from, from));
+    r[i] = kv8_round_sums(x, k, open);
+    r[i] = make_uint2(kv8_round_settled(r[i].x, x.x, k), kv8_round_settled(r[i].y, x.y, k));
+  }
+  return kv8_low_bytes(r[0].x, r[0].y, r[1].x, r[1].y);
+}
+__device__ __forceinline__ uint32_t kv8_requantise4(uint32_t w, float from, const Kv8Scale& k) {
+  const uint32_t biased = w ^ 0x80808080u;
+  const float2 f = make_float2(from, from);
+  bool open = false;
+  const uint2 a = kv8_round_sums(__fmul2_rn(kv8_bytes_f32(biased, 0), f), k, open);
+  const uint2 b = kv8_round_sums(__fmul2_rn(kv8_bytes_f32(biased, 2), f), k, open);
+  return open ? kv8_requantise4_settled(biased, from, k) : kv8_low_bytes(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ uint4 kv8_requantise16(const uint4& w, float from, const Kv8Scale& k) {
+  return make_uint4(kv8_requantise4(w.x, from, k), kv8_requantise4(w.y, from, k), kv8_requantise4(w.z, from, k),
+                    kv8_requantise4(w.w, from, k));
+}
 
 }  // namespace apr

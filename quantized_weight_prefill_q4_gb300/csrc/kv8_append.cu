@@ -1,16 +1,22 @@
 // Rows into and out of the 8-bit paged KV cache (include/apr_kv8.h).
 //
-// Append. One CTA per (page that gets rows, KV head, K or V): it finds the
-// largest magnitude of the page's new rows, raises the page's scale if that
-// asks for more, re-rounds what the page held if it was raised, and writes the
-// new codes. The block of a scale is one CTA's whole work, so no two CTAs
-// share a scale and the result does not depend on their order. Bound by
-// memory: a row is read once (its first 32 values a thread stay in registers
-// between the two passes, longer pages come from L1 the second time) and one
-// byte a value written.
+// Append. The block of a scale, a page of one head, is one CTA's work at a
+// time, so no two CTAs share a scale and the result does not depend on their
+// order: it finds the largest magnitude of the page's new rows, raises the
+// page's scale if that asks for more, re-rounds what the page held if it was
+// raised, and writes the new codes. A CTA takes several heads of the page one
+// after the other, K or V: the way from the lengths over the table to the page
+// is gone once, and the next head's rows are under way while one is rounded.
+// The pages that a call touches are numbered through (each CTA adds up the
+// sequences before its own), so that prompts of different lengths leave no CTA
+// without work.
+// Bound by memory: a row is read once (up to 32 registers a thread hold it
+// between the two passes; what a larger page has more comes from L1 the second
+// time) and one byte a value written; the rounding is five instructions and a
+// byte permute a value (kv8_codes8).
 //
-// Read. One CTA per (run of at most 128 tokens within a page, KV head, K or
-// V); a thread's 16-byte stores cover neighbouring elements of a row.
+// Read. One CTA per 32 packed rows and some heads, K or V; a thread's 16-byte
+// stores cover neighbouring elements of a row.
 
 #include "apr_internal.h"
 #include "host_common.h"
@@ -19,180 +25,317 @@
 namespace apr {
 namespace {
 
-constexpr int A_THREADS = 256;
-constexpr int A_HELD = 4;  // vectors of 8 values a thread keeps between the passes
+constexpr int A_THREADS = 128;
+constexpr int A_WARPS = A_THREADS / 32;
 
+// The largest magnitude; NaN is passed over, an infinity is not (the caller
+// looks again then, finite values only).
+__device__ __forceinline__ float amax_of(const Vec8<float>& e, float m) {
+  m = fmaxf(m, fmaxf(fmaxf(fabsf(e.a.x), fabsf(e.a.y)), fmaxf(fabsf(e.a.z), fabsf(e.a.w))));
+  return fmaxf(m, fmaxf(fmaxf(fabsf(e.b.x), fabsf(e.b.y)), fmaxf(fabsf(e.b.z), fabsf(e.b.w))));
+}
+template <typename T2>
+__device__ __forceinline__ float amax_of_pairs(const uint4& w, float m) {
+  const T2* h = reinterpret_cast<const T2*>(&w);
+  const T2 t = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
+  return fmaxf(m, fmaxf(__low2float(t), __high2float(t)));
+}
+__device__ __forceinline__ float amax_of(const Vec8<__half>& e, float m) { return amax_of_pairs<__half2>(e.a, m); }
+__device__ __forceinline__ float amax_of(const Vec8<__nv_bfloat16>& e, float m) {
+  return amax_of_pairs<__nv_bfloat162>(e.a, m);
+}
 template <typename T>
-__device__ __forceinline__ float amax_of(const Elems<T, 8>& e, float m) {
+__device__ __forceinline__ float finite_amax_of(const Vec8<T>& e, float m) {
+  float x[8];
+  values8(e, x);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_abs(to_f32<T>(e.x[i])));
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_abs(x[i]));
   return m;
 }
 
 template <typename T>
-__device__ __forceinline__ uint2 codes_of(const Elems<T, 8>& e, float s, float inv) {
-  int c[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] = kv8_code(to_f32<T>(e.x[i]), s, inv);
-  return make_uint2(kv8_pack4(c[0], c[1], c[2], c[3]), kv8_pack4(c[4], c[5], c[6], c[7]));
+__device__ __forceinline__ uint2 codes_of(const Vec8<T>& e, const Kv8Scale& s) {
+  float x[8];
+  values8(e, x);
+  return kv8_codes8(x, s);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(A_THREADS) kv8_append_kernel(Kv8View v, const T* __restrict__ k,
-                                                               const T* __restrict__ vv, long long ld) {
-  __shared__ float s_max[A_THREADS / 32];
-  const int b = blockIdx.z, g = (int)(blockIdx.x % v.kv_heads), slot = (int)(blockIdx.x / v.kv_heads);
-  const bool is_v = blockIdx.y != 0;
-  const int len = kv8_len(v, b);
-  const Kv8Span span = kv8_rows(v, b);
+// The largest value over the CTA.
+template <int WARPS>
+__device__ __forceinline__ float block_max(float m, float* warp_max) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) m = fmaxf(m, warp_max[w]);
+  return m;
+}
+
+// Pages that the rows of sequence b go to.
+__device__ __forceinline__ int pages_touched(const Kv8View& v, int b) {
+  const int len = kv8_len(v, b), n = kv8_rows(v, b).n;
+  return n == 0 || len == 0 ? 0 : ((len - 1) >> v.page_shift) - (max(len - n, 0) >> v.page_shift) + 1;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(A_THREADS) kv8_append_kernel(const __grid_constant__ Kv8View v,
+                                                               const T* __restrict__ k, const T* __restrict__ vv,
+                                                               long long ld, int heads_a_cta) {
+  constexpr int HELD = 16 / sizeof(T);  // vectors of 8 values a thread keeps between the passes, 32 registers
+  constexpr int ROW = D / 8;            // vectors of a row
+  __shared__ float s_max[3][A_WARPS];
+  __shared__ int s_scan[A_WARPS];
+  __shared__ int s_find[2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool is_v = blockIdx.y & 1;
+  const int g0 = (int)(blockIdx.y >> 1) * heads_a_cta, g1 = min(g0 + heads_a_cta, v.kv_heads);
+
+  // ---- which page: the blockIdx.x-th of those that the sequences touch
+  int b = (int)blockIdx.x, slot = 0;
+  if (v.row_start) {
+    const int run = (v.num_seqs + A_THREADS - 1) / A_THREADS;
+    const int b0 = min((int)threadIdx.x * run, v.num_seqs), b1 = min(b0 + run, v.num_seqs);
+    int mine = 0;
+    for (int i = b0; i < b1; ++i) mine += pages_touched(v, i);
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) s_scan[warp] = inc;
+    if (threadIdx.x == 0) s_find[0] = -1;
+    __syncthreads();
+    int at = inc - mine;
+    for (int w = 0; w < warp; ++w) at += s_scan[w];
+    const int want = (int)blockIdx.x;
+    if (at <= want && want < at + mine) {
+      int i = b0;
+      for (int n; at + (n = pages_touched(v, i)) <= want; ++i) at += n;
+      s_find[0] = i;
+      s_find[1] = want - at;
+    }
+    __syncthreads();
+    b = s_find[0];
+    slot = s_find[1];
+  }
+  // (the grid is for the most pages that the rows can touch: there may be none)
+  const int len = b < 0 ? 0 : kv8_len(v, b);
+  const Kv8Span span = b < 0 ? Kv8Span{0, 0} : kv8_rows(v, b);
   const int first = len - span.n;  // position of row r0; rows of negative positions are skipped
-  if (span.n == 0 || len == 0) return;
   const int index = (max(first, 0) >> v.page_shift) + slot;
-  if (index > (len - 1) >> v.page_shift) return;
-  const int page = kv8_page(v, b, index);
-  if (page < 0) return;
+  const int page = span.n == 0 || len == 0 ? -1 : kv8_page(v, b, index);
   kv8_ready();
   grid_launch_dependents();
+  if (page < 0) return;
+
   const int page0 = index << v.page_shift;
   const int lo = max(max(first, 0), page0), hi = min(len, page0 + (1 << v.page_shift));
   const int held = lo - page0;
-  const int vshift = 31 - __clz(v.dim / 8);  // vectors of 8 values a row
-  const T* src = (is_v ? vv : k) + (long long)(span.r0 + lo - first) * ld + (size_t)g * v.dim;
-  int8_t* codes = (is_v ? v.V : v.K) + kv8_codes_at(v, page, g);
-  float* scale = (is_v ? v.v_scale : v.k_scale) + kv8_scale_at(v, page, g);
-  const float s_old = held > 0 ? *scale : 0.f;
-  const int nvec = (hi - lo) << vshift;
-  const int cmask = (1 << vshift) - 1;
-  auto at = [&](int i) {
-    return reinterpret_cast<const Elems<T, 8>*>(src + (long long)(i >> vshift) * ld + (i & cmask) * 8);
-  };
-
-  // ---- the largest magnitude
-  Elems<T, 8> keep[A_HELD];
-  float m = 0.f;
+  const int nvec = (hi - lo) * ROW;
+  // this thread's vectors: column (threadIdx.x % ROW), every (A_THREADS / ROW)-th row
+  const long long step = ld * (A_THREADS / ROW);
+  const T* src = (is_v ? vv : k) + (long long)(span.r0 + lo - first + (int)threadIdx.x / ROW) * ld +
+                 (int)threadIdx.x % ROW * 8;
+  int8_t* codes = (is_v ? v.V : v.K) + kv8_codes_at(v, page, g0);
+  float* scale = (is_v ? v.v_scale : v.k_scale) + kv8_scale_at(v, page, g0);
+  src += (size_t)g0 * D;
+  for (int g = g0; g < g1; ++g, src += D, codes += (size_t)D << v.page_shift, ++scale) {
+    Vec8<T> keep[HELD];
 #pragma unroll
-  for (int j = 0; j < A_HELD; ++j) {
-    const int i = threadIdx.x + j * A_THREADS;
-    if (i < nvec) keep[j] = *at(i);
-  }
+    for (int j = 0; j < HELD; ++j)
+      if ((int)threadIdx.x + j * A_THREADS < nvec) keep[j] = load8(src + j * step);
+    const float s_old = held > 0 ? *scale : 0.f;
+    // ---- the largest magnitude
+    float m = 0.f;
 #pragma unroll
-  for (int j = 0; j < A_HELD; ++j)
-    if ((int)threadIdx.x + j * A_THREADS < nvec) m = amax_of<T>(keep[j], m);
+    for (int j = 0; j < HELD; ++j)
+      if ((int)threadIdx.x + j * A_THREADS < nvec) m = amax_of(keep[j], m);
 #pragma unroll 4
-  for (int i = threadIdx.x + A_HELD * A_THREADS; i < nvec; i += A_THREADS) m = amax_of<T>(*at(i), m);
+    for (int i = HELD; (int)threadIdx.x + i * A_THREADS < nvec; ++i) m = amax_of(load8(src + i * step), m);
+    m = block_max<A_WARPS>(m, s_max[g & 1]);  // (the next head writes the other: one barrier a head)
+    if (m > FLT_MAX) {                        // an infinity among them, for the whole CTA
+      m = 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < A_THREADS / 32; ++w) m = fmaxf(m, s_max[w]);
-
-  // ---- the scale, and what the page held under a raised one
-  const float s = fmaxf(s_old, kv8_scale_of(m));
-  const float inv = __fdiv_rn(1.0f, s);
-  if (threadIdx.x == 0 && (held == 0 || s > s_old)) *scale = s;
-  if (held > 0 && s > s_old) {
-    uint4* old = reinterpret_cast<uint4*>(codes);
-    for (int i = threadIdx.x; i < held * v.dim / 16; i += A_THREADS) {
-      uint4 w = old[i];
-      uint32_t* u = reinterpret_cast<uint32_t*>(&w);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        int c[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) c[t] = kv8_code((float)kv8_byte(u[j], t) * s_old, s, inv);
-        u[j] = kv8_pack4(c[0], c[1], c[2], c[3]);
-      }
-      old[i] = w;
+      for (int j = 0; j < HELD; ++j)
+        if ((int)threadIdx.x + j * A_THREADS < nvec) m = finite_amax_of<T>(keep[j], m);
+      for (int i = HELD; (int)threadIdx.x + i * A_THREADS < nvec; ++i) m = finite_amax_of<T>(load8(src + i * step), m);
+      __syncthreads();
+      m = block_max<A_WARPS>(m, s_max[2]);
     }
-  }
 
-  // ---- the new codes
-  uint2* dst = reinterpret_cast<uint2*>(codes + (size_t)held * v.dim);
+    // ---- the scale, and what the page held under a raised one
+    const Kv8Scale s = kv8_rounding_to(fmaxf(s_old, kv8_scale_of(m)));
+    if (threadIdx.x == 0 && (held == 0 || s.s > s_old)) *scale = s.s;
+    if (held > 0 && s.s > s_old) {
+      uint4* old = reinterpret_cast<uint4*>(codes);
+      for (int i = threadIdx.x; i < held * D / 16; i += A_THREADS) {
+        const uint4 w = old[i];
+        uint4 y = kv8_requantise16(w, s_old, s);
+        // (a code of -128 may have come from elsewhere)
+        y.x = __vmaxs4(y.x, 0x81818181u), y.y = __vmaxs4(y.y, 0x81818181u);
+        y.z = __vmaxs4(y.z, 0x81818181u), y.w = __vmaxs4(y.w, 0x81818181u);
+        old[i] = y;
+      }
+    }
+
+    // ---- the new codes
+    uint2* dst = reinterpret_cast<uint2*>(codes + (size_t)held * D) + threadIdx.x;
 #pragma unroll
-  for (int j = 0; j < A_HELD; ++j) {
-    const int i = threadIdx.x + j * A_THREADS;
-    if (i < nvec) dst[i] = codes_of<T>(keep[j], s, inv);
+    for (int j = 0; j < HELD; ++j)
+      if ((int)threadIdx.x + j * A_THREADS < nvec) dst[j * A_THREADS] = codes_of<T>(keep[j], s);
+#pragma unroll 2
+    for (int i = HELD; (int)threadIdx.x + i * A_THREADS < nvec; ++i)
+      dst[i * A_THREADS] = codes_of<T>(load8(src + i * step), s);
   }
-  for (int i = threadIdx.x + A_HELD * A_THREADS; i < nvec; i += A_THREADS) dst[i] = codes_of<T>(*at(i), s, inv);
 }
 
 // ---------------------------------------------------------------- read
 constexpr int R_THREADS = 256;
+constexpr int R_ROWS = 32;  // packed rows of a CTA
 
-// tokens of a CTA's run: a page's, at most 128
-__host__ __device__ inline int read_run_shift(int page_shift) { return page_shift < 7 ? page_shift : 7; }
-
-template <typename T>
-__global__ void __launch_bounds__(R_THREADS) kv8_read_kernel(Kv8View v, T* __restrict__ k, T* __restrict__ vv,
-                                                             long long ld) {
-  constexpr int N = 16 / sizeof(T);  // values of a 16-byte store
-  const int b = blockIdx.z, g = (int)(blockIdx.x % v.kv_heads), run = (int)(blockIdx.x / v.kv_heads);
-  const bool is_v = blockIdx.y != 0;
-  const int len = kv8_len(v, b);
-  const Kv8Span span = kv8_rows(v, b);
-  if (span.n == 0) return;
-  const int first = len - span.n;
-  const int rshift = read_run_shift(v.page_shift);
-  const int vshift = 31 - __clz(v.dim / N), cmask = (1 << vshift) - 1;
-  T* out = (is_v ? vv : k) + (long long)span.r0 * ld + (size_t)g * v.dim;
-  const int index = (max(first, 0) >> rshift) + run;
+template <typename T, int D>
+__global__ void __launch_bounds__(R_THREADS) kv8_read_kernel(const __grid_constant__ Kv8View v, T* __restrict__ k,
+                                                             T* __restrict__ vv, long long ld, int heads_a_cta) {
+  constexpr int N = 16 / sizeof(T);             // values of a 16-byte store
+  constexpr int ROW = D / N;                    // stores of a row
+  constexpr int STEP = R_THREADS / ROW;         // rows between a thread's stores
+  constexpr int EACH = (R_ROWS + STEP - 1) / STEP;
+  __shared__ const int8_t* s_codes[R_ROWS];     // a row's codes of head g0; nullptr: none
+  __shared__ const float* s_scale[R_ROWS];
+  __shared__ int s_zero[R_ROWS];                // a row before its sequence's start
+  const int row0 = (int)blockIdx.x * R_ROWS;
+  const bool is_v = blockIdx.y & 1;
+  const int g0 = (int)(blockIdx.y >> 1) * heads_a_cta, g1 = min(g0 + heads_a_cta, v.kv_heads);
+  if (threadIdx.x < R_ROWS) {
+    const int row = row0 + (int)threadIdx.x;
+    int b = row;
+    if (v.row_start) {  // the last sequence that begins at the row or before it
+      int end = v.num_seqs;
+      b = 0;
+      while (end - b > 1) {
+        const int mid = (b + end) / 2;
+        if (v.row_start[mid] <= row)
+          b = mid;
+        else
+          end = mid;
+      }
+    }
+    const int8_t* codes = nullptr;
+    const float* scale = nullptr;
+    bool zero = false;
+    if (row < v.num_rows) {
+      const Kv8Span span = kv8_rows(v, b);
+      if (row >= span.r0 && row < span.r0 + span.n) {
+        const int pos = kv8_len(v, b) - span.n + (row - span.r0);  // negative: before the sequence's start
+        const int page = pos < 0 ? -1 : kv8_page(v, b, pos >> v.page_shift);
+        zero = pos < 0;
+        if (page >= 0) {
+          codes = (is_v ? v.V : v.K) + kv8_codes_at(v, page, g0) + (size_t)(pos & ((1 << v.page_shift) - 1)) * D;
+          scale = (is_v ? v.v_scale : v.k_scale) + kv8_scale_at(v, page, g0);
+        }
+      }
+    }
+    s_codes[threadIdx.x] = codes;
+    s_scale[threadIdx.x] = scale;
+    s_zero[threadIdx.x] = zero;
+  }
   kv8_ready();
   grid_launch_dependents();
-  if (run == 0 && first < 0) {  // rows before the sequence's start
-    Elems<T, N> zero;
+  __syncthreads();
+  const int col = (int)threadIdx.x % ROW * N, r0 = (int)threadIdx.x / ROW;
+  T* out = (is_v ? vv : k) + (long long)(row0 + r0) * ld + (size_t)g0 * D + col;
+  const int8_t* from[EACH];
+  const float* scale[EACH];
 #pragma unroll
-    for (int t = 0; t < N; ++t) zero.x[t] = from_f32<T>(0.f);
-    for (int i = threadIdx.x; i < (min(-first, span.n) << vshift); i += R_THREADS)
-      *reinterpret_cast<Elems<T, N>*>(out + (long long)(i >> vshift) * ld + (i & cmask) * N) = zero;
+  for (int j = 0; j < EACH; ++j) {
+    const int r = r0 + j * STEP;
+    from[j] = r < R_ROWS && s_codes[r] ? s_codes[r] + col : nullptr;
+    scale[j] = from[j] ? s_scale[r] : nullptr;
+    if (r < R_ROWS && s_zero[r])
+      for (int g = 0; g < g1 - g0; ++g)
+        *reinterpret_cast<uint4*>(out + (long long)j * STEP * ld + (size_t)g * D) = make_uint4(0, 0, 0, 0);
   }
-  const int lo = max(max(first, 0), index << rshift), hi = min(len, (index + 1) << rshift);
-  if (lo >= hi) return;
-  const int page = kv8_page(v, b, lo >> v.page_shift);
-  if (page < 0) return;
-  const float s = (is_v ? v.v_scale : v.k_scale)[kv8_scale_at(v, page, g)];
-  const int8_t* codes = (is_v ? v.V : v.K) + kv8_codes_at(v, page, g) +
-                        (size_t)(lo & ((1 << v.page_shift) - 1)) * v.dim;
-  out += (long long)(lo - first) * ld;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < (hi - lo) << vshift; i += R_THREADS) {
-    uint32_t w[N / 4];
-    if (N == 4)
-      w[0] = __ldg(reinterpret_cast<const uint32_t*>(codes) + i);
-    else
-      *reinterpret_cast<uint2*>(w) = __ldg(reinterpret_cast<const uint2*>(codes) + i);
-    Elems<T, N> e;
+  const size_t head = (size_t)D << v.page_shift;
+#pragma unroll 2
+  for (int g = 0; g < g1 - g0; ++g, out += D) {
+    uint2 w[EACH];
+    float s[EACH];
 #pragma unroll
-    for (int t = 0; t < N; ++t) e.x[t] = from_f32<T>((float)kv8_byte(w[t / 4], t % 4) * s);
-    *reinterpret_cast<Elems<T, N>*>(out + (long long)(i >> vshift) * ld + (i & cmask) * N) = e;
+    for (int j = 0; j < EACH; ++j) {
+      w[j] = make_uint2(0, 0);
+      s[j] = 0.f;
+      if (from[j]) {
+        if (N == 4)
+          w[j].x = *reinterpret_cast<const uint32_t*>(from[j] + g * head);
+        else
+          w[j] = *reinterpret_cast<const uint2*>(from[j] + g * head);
+        s[j] = scale[j][g];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < EACH; ++j) {
+      if (!from[j]) continue;
+      const uint32_t words[2] = {w[j].x ^ 0x80808080u, w[j].y ^ 0x80808080u};
+      float2 x[4];
+#pragma unroll
+      for (int t = 0; t < N / 2; ++t)
+        x[t] = __fmul2_rn(kv8_bytes_f32(words[t / 2], t % 2 * 2), make_float2(s[j], s[j]));
+      uint4 y;
+      if constexpr (N == 4)
+        y = make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x), __float_as_uint(x[1].y));
+      else
+        y = make_uint4(pack2<T>(x[0].x, x[0].y), pack2<T>(x[1].x, x[1].y), pack2<T>(x[2].x, x[2].y),
+                       pack2<T>(x[3].x, x[3].y));
+      *reinterpret_cast<uint4*>(out + (long long)j * STEP * ld) = y;
+    }
   }
 }
 
-template <typename T>
-cudaError_t append_typed(const Kv8View& v, const void* k, const void* vv, long long ld, cudaStream_t s) {
-  // pages that max_rows rows can touch
-  const int page = 1 << v.page_shift, slots = (int)(((long long)v.max_rows + page - 2) / page + 1);
+// Heads of a CTA: all, or as few as it takes to give every SM `most` CTAs.
+int heads_a_cta(long long units, int kv_heads, int most) {
+  const long long want = (long long)most * num_sms() / (2 * units > 0 ? 2 * units : 1);  // CTAs of a unit, K or V
+  return want <= 1 ? kv_heads : (int)(want >= kv_heads ? 1 : (kv_heads + want - 1) / want);
+}
+
+template <typename T, int D>
+cudaError_t append_shape(const Kv8View& v, const void* k, const void* vv, long long ld, cudaStream_t s) {
+  // the most pages that the rows can touch
+  const long long pages = v.row_start ? (v.num_rows >> v.page_shift) + 2ll * v.num_seqs : v.num_seqs;
+  const int heads = heads_a_cta(pages, v.kv_heads, 12);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)slots * v.kv_heads, 2, (unsigned)v.num_seqs);
+  cfg.gridDim = dim3((unsigned)pages, 2u * ((v.kv_heads + heads - 1) / heads));
   cfg.blockDim = dim3(A_THREADS);
   cfg.stream = s;
   cudaLaunchAttribute attr[1] = {pdl_attr()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_append_kernel<T>, v, (const T*)k, (const T*)vv, ld);
+  return cudaLaunchKernelEx(&cfg, kv8_append_kernel<T, D>, v, (const T*)k, (const T*)vv, ld, heads);
 }
 
-template <typename T>
-cudaError_t read_typed(const Kv8View& v, void* k, void* vv, long long ld, cudaStream_t s) {
-  const int run = 1 << read_run_shift(v.page_shift), runs = (int)(((long long)v.max_rows + run - 2) / run + 1);
+template <typename T, int D>
+cudaError_t read_shape(const Kv8View& v, void* k, void* vv, long long ld, cudaStream_t s) {
+  const int units = (v.num_rows + R_ROWS - 1) / R_ROWS, heads = heads_a_cta(units, v.kv_heads, 4);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)runs * v.kv_heads, 2, (unsigned)v.num_seqs);
+  cfg.gridDim = dim3((unsigned)units, 2u * ((v.kv_heads + heads - 1) / heads));
   cfg.blockDim = dim3(R_THREADS);
   cfg.stream = s;
   cudaLaunchAttribute attr[1] = {pdl_attr()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_read_kernel<T>, v, (T*)k, (T*)vv, ld);
+  return cudaLaunchKernelEx(&cfg, kv8_read_kernel<T, D>, v, (T*)k, (T*)vv, ld, heads);
+}
+
+template <typename T>
+cudaError_t append_typed(const Kv8View& v, const void* k, const void* vv, long long ld, cudaStream_t s) {
+  return v.dim == 64 ? append_shape<T, 64>(v, k, vv, ld, s)
+                     : (v.dim == 128 ? append_shape<T, 128>(v, k, vv, ld, s) : append_shape<T, 256>(v, k, vv, ld, s));
+}
+template <typename T>
+cudaError_t read_typed(const Kv8View& v, void* k, void* vv, long long ld, cudaStream_t s) {
+  return v.dim == 64 ? read_shape<T, 64>(v, k, vv, ld, s)
+                     : (v.dim == 128 ? read_shape<T, 128>(v, k, vv, ld, s) : read_shape<T, 256>(v, k, vv, ld, s));
 }
 
 }  // namespace

@@ -275,7 +275,10 @@ __global__ void __launch_bounds__(Shape<D, MT>::THREADS, Shape<D, MT>::CTAS) kv8
     total += s_scan[w];
   }
   const int ctas = sharing_ctas(a, total);
-  if ((int)blockIdx.x >= ctas) return;
+  if ((int)blockIdx.x >= ctas) {
+    if (blockIdx.x == 0) kv8_ready();
+    return;
+  }
   int u = first_unit(blockIdx.x, ctas, total);
   const int u_begin = u, u_end = first_unit(blockIdx.x + 1, ctas, total);
   if (my_u0 <= u && u < my_u0 + my_units) {
@@ -430,9 +433,9 @@ __global__ void __launch_bounds__(Shape<D, MT>::THREADS, Shape<D, MT>::CTAS) kv8
                   ((size_t)(span.r0 + pair / a.group) * a.heads + g * a.group + pair % a.group) * a.scores_ld + 2 * c;
 
     float ref = -INFINITY, l = 0.f;
-    float sum[D / 8][2];  // [column 4 w + t of each 128 dims]: dims 32 c + (4 w + t) and + 16 (D = 64: 16 c and + 8)
+    float2 sum[D / 8];  // [column 4 w + t of each 128 dims]: dims 32 c + (4 w + t) and + 16 (D = 64: 16 c and + 8)
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) sum[i][0] = sum[i][1] = 0.f;
+    for (int i = 0; i < D / 8; ++i) sum[i] = make_float2(0.f, 0.f);
 
 #pragma unroll 1
     for (int i = 0; i < mine; ++i) {
@@ -481,8 +484,10 @@ __global__ void __launch_bounds__(Shape<D, MT>::THREADS, Shape<D, MT>::CTAS) kv8
       float top = -INFINITY;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        s[t][0] = (s[t][0] + s[t][2]) * kf;
-        s[t][1] = (s[t][1] + s[t][3]) * kf;
+        const float2 both = __fmul2_rn(__fadd2_rn(make_float2(s[t][0], s[t][1]), make_float2(s[t][2], s[t][3])),
+                                       make_float2(kf, kf));
+        s[t][0] = both.x;
+        s[t][1] = both.y;
       }
       if (k + TILE > least) {
 #pragma unroll
@@ -505,10 +510,8 @@ __global__ void __launch_bounds__(Shape<D, MT>::THREADS, Shape<D, MT>::CTAS) kv8
         const float f = ref == -INFINITY ? 0.f : exp2_fast(ref - now);
         l *= f;
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j) {
-          sum[j][0] *= f;
-          sum[j][1] *= f;
-        }
+        for (int j = 0; j < D / 8; ++j)
+          sum[j] = __fmul2_rn(sum[j], make_float2(f, f));
         ref = now;
       }
       const float shift = ref == -INFINITY ? 0.f : ref - HEADROOM;
@@ -570,9 +573,8 @@ __global__ void __launch_bounds__(Shape<D, MT>::THREADS, Shape<D, MT>::CTAS) kv8
           }
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            float* to = sum[COLS * dc + 4 * w + t];
-            to[0] = fmaf(vs, o[t][0] + o[t][2], to[0]);
-            to[1] = fmaf(vs, o[t][1] + o[t][3], to[1]);
+            float2& to = sum[COLS * dc + 4 * w + t];
+            to = __ffma2_rn(make_float2(vs, vs), __fadd2_rn(make_float2(o[t][0], o[t][1]), make_float2(o[t][2], o[t][3])), to);
           }
         }
       }
@@ -599,8 +601,8 @@ __global__ void __launch_bounds__(Shape<D, MT>::THREADS, Shape<D, MT>::CTAS) kv8
 #pragma unroll
           for (int i = 0; i < COLS; i += 4)
             *reinterpret_cast<float4*>(to + 128 * dc + (2 * c + h) * COLS + i) =
-                make_float4(sum[COLS * dc + i][h], sum[COLS * dc + i + 1][h], sum[COLS * dc + i + 2][h],
-                            sum[COLS * dc + i + 3][h]);
+                h ? make_float4(sum[COLS * dc + i].y, sum[COLS * dc + i + 1].y, sum[COLS * dc + i + 2].y, sum[COLS * dc + i + 3].y)
+                  : make_float4(sum[COLS * dc + i].x, sum[COLS * dc + i + 1].x, sum[COLS * dc + i + 2].x, sum[COLS * dc + i + 3].x);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < done_np * (D / 4); i += THREADS) {

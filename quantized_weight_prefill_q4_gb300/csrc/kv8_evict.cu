@@ -1,19 +1,24 @@
 // Eviction from the 8-bit paged KV cache (include/apr_kv8.h): which positions
 // a sequence keeps, and their move into fresh pages.
 //
-// Selection. One cluster of CTAs per (sequence, KV head), each CTA a
-// contiguous share of the positions. The weights are mapped to unsigned keys
-// that order as the numbers do, and the key of the last one kept is found by
-// three rounds of histograms over 11, 11 and 10 bits of it, each round's
-// counts added up over the cluster through distributed shared memory. A second
-// pass writes the kept positions in order: each CTA knows from its peers'
-// counts how many it has before it, and takes the equal keys lowest position
-// first. Every count is a whole number, so the result does not depend on the
-// order of the atomics. The weights (4 bytes a position) are read five times,
-// from DRAM once: they fit L2.
+// Selection. One cluster of 1 to 8 CTAs per (sequence, KV head), each CTA a
+// contiguous share of the positions, whose weights it reads once: mapped to
+// unsigned keys that order as the numbers do they stay in shared memory (a
+// share of more than 16384 is read again for each pass, from L2). The key of
+// the last one kept is found by up to three rounds of histograms over 11, 11
+// and 10 bits of it, each round's counts added up over the cluster through
+// distributed shared memory; a round whose border falls between two bins ends
+// the search. The kept positions are then written in order: each CTA knows from
+// its peers' counts how many come before its own, and of equal keys the lowest
+// positions are taken. Every count is a whole number, so the result does not
+// depend on the order of the atomics. Bound by latency: barriers and dependent
+// passes of a few hundred cycles each.
 //
-// Move. One CTA per (fresh page, KV head, K or V): the kept rows' codes are
-// gathered once for the largest value, once (from L1) to be quantised anew.
+// Move. One CTA per (fresh page, KV head), K or V: the kept rows' codes are
+// gathered into registers, their largest value gives the scale, and they are
+// written under it, five instructions and a byte permute a value
+// (kv8_requantise16). What a large page has more than the registers hold is
+// gathered again, from L1.
 
 #include "apr_internal.h"
 #include "host_common.h"
@@ -22,10 +27,11 @@
 namespace apr {
 namespace {
 
-constexpr int S_CTAS = 8;  // CTAs of a cluster, the portable size
-constexpr int S_THREADS = 512;
+constexpr int S_MOST = 8;        // CTAs of a cluster, the portable size
+constexpr int S_THREADS = 1024;
 constexpr int S_WARPS = S_THREADS / 32;
 constexpr int S_BINS = 2048;
+constexpr int S_KEYS = 16384;    // keys that a CTA holds
 
 // Unsigned keys in the numbers' order: NaN above all, -0 as 0.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -39,31 +45,37 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(const void* p, int rank) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(r) : "r"(mapa_shared(smem_u32(p), (uint32_t)rank)) : "memory");
   return r;
 }
-__device__ __forceinline__ void cluster_sync_all() {
-  cluster_arrive();
-  cluster_wait();
+// The barrier of a cluster of `ranks` CTAs.
+__device__ __forceinline__ void cluster_sync_all(int ranks) {
+  if (ranks == 1) {
+    __syncthreads();
+  } else {
+    cluster_arrive();
+    cluster_wait();
+  }
 }
 
 // Sum of x over the threads before this one, and over all of them (*total).
-__device__ __forceinline__ int block_scan(int x, int* warp_sums, int* total) {
+// `sums` [S_WARPS] must not be in use by the scan before.
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* sums, uint32_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int inc = x;
+  uint32_t inc = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
   }
-  if (lane == 31) warp_sums[warp] = inc;
+  if (lane == 31) sums[warp] = inc;
   __syncthreads();
-  int before = 0, all = 0;
+  uint32_t w = sums[lane];
 #pragma unroll
-  for (int w = 0; w < S_WARPS; ++w) {
-    if (w < warp) before += warp_sums[w];
-    all += warp_sums[w];
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
   }
-  __syncthreads();
-  *total = all;
-  return before + inc - x;
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  const uint32_t before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+  return (warp ? before : 0) + inc - x;
 }
 
 struct EvictArgs {
@@ -78,21 +90,23 @@ struct EvictArgs {
   int* kept;
 };
 
-__global__ void __launch_bounds__(S_THREADS) kv8_select_kernel(Kv8View v, EvictArgs a) {
-  kv8_ready();
-  grid_launch_dependents();  // of the move, which waits for this grid's end and lets nothing start before its own
+__global__ void __launch_bounds__(S_THREADS) kv8_select_kernel(const __grid_constant__ Kv8View v,
+                                                               const __grid_constant__ EvictArgs a) {
+  extern __shared__ uint32_t s_keys[];
   __shared__ uint32_t hist[S_BINS];
   __shared__ uint32_t chosen[2];  // the round's bin, and how many of it are kept
   __shared__ uint32_t counts[2];  // this CTA's keys above the border, and equal to it
-  __shared__ int warp_sums[S_WARPS];
-  const int rank = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
+  __shared__ uint32_t sums[2][S_WARPS];
+  const int ranks = gridDim.x, rank = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
   const int len = kv8_len(v, b);
+  kv8_ready();
+  grid_launch_dependents();  // of the move, which waits for this grid's end and lets nothing start before its own
   const size_t bg = (size_t)b * v.kv_heads + g;
   const float* w = a.weights + bg * a.weights_ld;
   float* wo = a.weights_out + bg * a.weights_out_ld;
   int* kept = a.kept + bg * a.budget;
   const int now = min(len, a.budget);
-  const int all = S_CTAS * S_THREADS, tid = rank * S_THREADS + threadIdx.x;
+  const int all = ranks * S_THREADS, tid = rank * S_THREADS + threadIdx.x;
   if (g == 0) {  // the sequence's table row and length
     const int pages = (now + (1 << v.page_shift) - 1) >> v.page_shift;
     const int* own = v.table + (size_t)b * v.table_ld;
@@ -117,8 +131,15 @@ __global__ void __launch_bounds__(S_THREADS) kv8_select_kernel(Kv8View v, EvictA
     kept[need + j] = old + j;
   }
   if (need == 0) return;
-  const int share = ((old + S_CTAS - 1) / S_CTAS + 3) & ~3;
-  const int lo = min(rank * share, old), hi = min(lo + share, old);
+  const int share = (old + ranks - 1) / ranks;
+  const int lo = min(rank * share, old), n = min(share, old - lo);
+  w += lo;
+  const bool held = share <= S_KEYS;
+  if (held) {
+#pragma unroll 4
+    for (int j = threadIdx.x; j < n; j += S_THREADS) s_keys[j] = order_key(w[j]);
+  }
+  auto key_at = [&](int j) { return held ? s_keys[j] : order_key(w[j]); };
 
   // ---- the key of the last position kept: border, of whose equals `take` are kept
   uint32_t border = 0, take = (uint32_t)need;
@@ -129,169 +150,188 @@ __global__ void __launch_bounds__(S_THREADS) kv8_select_kernel(Kv8View v, EvictA
     __syncthreads();
     const uint32_t above = round == 0 ? 0 : 0xffffffffu << (shift + bits);  // the bits already settled
 #pragma unroll 4
-    for (int j = lo + threadIdx.x; j < hi; j += S_THREADS) {
-      const uint32_t key = order_key(w[j]);
+    for (int j = threadIdx.x; j < n; j += S_THREADS) {
+      const uint32_t key = key_at(j);
       if ((key & above) == border) atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1)], 1u);
     }
-    cluster_sync_all();
-    // every CTA adds up all of them: thread t the bins 4t .. 4t + 3 from the top
-    uint32_t c[4];
+    cluster_sync_all(ranks);
+    // every CTA adds up all of them: thread t the bins 2 t and 2 t + 1 from the top
+    const int bin = S_BINS - 2 - 2 * (int)threadIdx.x;
+    uint32_t hi = 0, low = 0;
+    if (ranks == 1) {
+      hi = hist[bin + 1];
+      low = hist[bin];
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int bin = S_BINS - 1 - (4 * (int)threadIdx.x + i);
-      c[i] = 0;
-#pragma unroll
-      for (int r = 0; r < S_CTAS; ++r) c[i] += ld_cluster_u32(&hist[bin], r);
-    }
-    int total;
-    uint32_t before = (uint32_t)block_scan((int)(c[0] + c[1] + c[2] + c[3]), warp_sums, &total);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (before < take && take <= before + c[i]) {
-        chosen[0] = (uint32_t)(S_BINS - 1 - (4 * (int)threadIdx.x + i));
-        chosen[1] = take - before;
+      for (int r = 0; r < S_MOST; ++r) {
+        if (r < ranks) {
+          hi += ld_cluster_u32(&hist[bin + 1], r);
+          low += ld_cluster_u32(&hist[bin], r);
+        }
       }
-      before += c[i];
     }
-    cluster_sync_all();  // chosen is written; every CTA has read the histograms
-    border |= chosen[0] << shift;
+    uint32_t total;
+    const uint32_t before = block_scan(hi + low, sums[round & 1], &total);
+    const bool in_hi = before < take && take <= before + hi, in_low = before + hi < take && take <= before + hi + low;
+    if (in_hi || in_low) {
+      const uint32_t at = before + (in_hi ? 0 : hi);
+      chosen[0] = ((uint32_t)(in_hi ? bin + 1 : bin) << 1) | (take - at == (in_hi ? hi : low));
+      chosen[1] = take - at;
+    }
+    cluster_sync_all(ranks);  // chosen is written; every CTA has read the histograms
+    border |= (chosen[0] >> 1) << shift;
     take = chosen[1];
+    if (chosen[0] & 1) {  // the whole bin is kept: the border lies just below it
+      border -= 1;        // (not below 0: then every position would be kept)
+      take = 0;
+      break;
+    }
+  }
+
+  // ---- how many of the CTAs before are kept
+  uint32_t gt_before = 0, eq_before = 0;
+  if (ranks > 1) {
+    if (threadIdx.x < 2) counts[threadIdx.x] = 0;
     __syncthreads();
-  }
-
-  // ---- how many each CTA keeps
-  if (threadIdx.x < 2) counts[threadIdx.x] = 0;
-  __syncthreads();
-  uint32_t gt = 0, eq = 0;
+    uint32_t gt = 0, eq = 0;
 #pragma unroll 4
-  for (int j = lo + threadIdx.x; j < hi; j += S_THREADS) {
-    const uint32_t key = order_key(w[j]);
-    gt += key > border;
-    eq += key == border;
-  }
+    for (int j = threadIdx.x; j < n; j += S_THREADS) {
+      const uint32_t key = key_at(j);
+      gt += key > border;
+      eq += key == border;
+    }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    gt += __shfl_xor_sync(0xffffffffu, gt, o);
-    eq += __shfl_xor_sync(0xffffffffu, eq, o);
+    for (int o = 16; o > 0; o >>= 1) {
+      gt += __shfl_xor_sync(0xffffffffu, gt, o);
+      eq += __shfl_xor_sync(0xffffffffu, eq, o);
+    }
+    if ((threadIdx.x & 31) == 0) {
+      atomicAdd(&counts[0], gt);
+      atomicAdd(&counts[1], eq);
+    }
+    cluster_sync_all(ranks);
+    for (int r = 0; r < rank; ++r) {
+      gt_before += ld_cluster_u32(&counts[0], r);
+      eq_before += ld_cluster_u32(&counts[1], r);
+    }
+    cluster_sync_all(ranks);  // no CTA ends while its counts are read
   }
-  if ((threadIdx.x & 31) == 0) {
-    atomicAdd(&counts[0], gt);
-    atomicAdd(&counts[1], eq);
-  }
-  cluster_sync_all();
-  uint32_t at = 0, eq_before = 0;
-  for (int r = 0; r < rank; ++r) {
-    at += ld_cluster_u32(&counts[0], r);
-    eq_before += ld_cluster_u32(&counts[1], r);
-  }
-  at += min(eq_before, take);
-  cluster_sync_all();  // no CTA ends while its counts are read
+  __syncthreads();
 
-  // ---- the kept positions in order, four a thread at a time
-  for (int j0 = lo; j0 < hi; j0 += 4 * S_THREADS) {
+  // ---- the kept positions in order, four neighbours a thread at a time; the
+  // scan counts those above the border in its low half, those equal in its high
+  int half = 0;
+  for (int j0 = 0; j0 < n; j0 += 4 * S_THREADS, half ^= 1) {
     const int j = j0 + 4 * (int)threadIdx.x;
-    float x[4];
-    uint32_t key[4];
-    int eqs = 0;
+    uint32_t key[4], mine = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[i] = j + i < hi ? w[j + i] : 0.f;
-      key[i] = order_key(x[i]);
-      eqs += j + i < hi && key[i] == border;
+      key[i] = j + i < n ? key_at(j + i) : 0u;
+      mine += j + i < n ? (key[i] > border ? 1u : (key[i] == border ? 1u << 16 : 0u)) : 0u;
     }
-    int total;
-    uint32_t e = eq_before + (uint32_t)block_scan(eqs, warp_sums, &total);
-    eq_before += (uint32_t)total;
-    bool keep[4];
-    int n = 0;
+    uint32_t total;
+    const uint32_t before = block_scan(mine, sums[half], &total);
+    uint32_t gt = gt_before + (before & 0xffffu), eq = eq_before + (before >> 16);
+    gt_before += total & 0xffffu;
+    eq_before += total >> 16;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const bool same = j + i < hi && key[i] == border;
-      keep[i] = j + i < hi && (key[i] > border || (same && e < take));
-      e += same;
-      n += keep[i];
-    }
-    uint32_t o = at + (uint32_t)block_scan(n, warp_sums, &total);
-    at += (uint32_t)total;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (keep[i]) {
-        kept[o] = j + i;
-        wo[o] = x[i];
-        ++o;
+      if (j + i >= n) break;
+      const bool same = key[i] == border;
+      if (key[i] > border || (same && eq < take)) {
+        const uint32_t o = gt + min(eq, take);
+        kept[o] = lo + j + i;
+        wo[o] = w[j + i];
       }
+      gt += key[i] > border;
+      eq += same;
+    }
   }
 }
 
-constexpr int M_THREADS = 256;
+constexpr int M_THREADS = 128;
 constexpr int M_PAGE = 256;  // most tokens of a page
+constexpr int M_HELD = 4;    // vectors of 16 codes that a thread holds
 
-__global__ void __launch_bounds__(M_THREADS) kv8_move_kernel(Kv8View v, EvictArgs a) {
-  kv8_ready();
-  __shared__ const int8_t* row_codes[M_PAGE];
+// The largest |code| of a vector times its scale: rounding to float32 keeps
+// order, so that is the largest |value|. Two codes at a time, sign-extended to
+// 16 bits by one byte permute.
+__device__ __forceinline__ float amax_of_codes(const uint4& in, float scale) {
+  const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+  uint32_t top = 0, low = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t a, b;  // (8 + i in a selector repeats byte i's sign)
+    asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(a) : "r"(w[i]));
+    asm("prmt.b32 %0, %1, 0, 0xb3a2;" : "=r"(b) : "r"(w[i]));
+    top = __vimax3_s16x2(top, a, b);
+    low = __vimin3_s16x2(low, a, b);
+  }
+  const int hi = max((int)(int16_t)top, (int)top >> 16), lo = min((int)(int16_t)low, (int)low >> 16);
+  return finite_abs((float)max(hi, -lo) * scale);
+}
+
+template <int D>
+__global__ void __launch_bounds__(M_THREADS) kv8_move_kernel(const __grid_constant__ Kv8View v,
+                                                             const __grid_constant__ EvictArgs a) {
+  __shared__ long long row_at[M_PAGE];  // offset of a row's codes; -1: none
   __shared__ float row_scale[M_PAGE];
   __shared__ float s_max[M_THREADS / 32];
   const int b = blockIdx.z, g = (int)(blockIdx.x % v.kv_heads), index = (int)(blockIdx.x / v.kv_heads);
   const bool is_v = blockIdx.y != 0;
   const int len = kv8_len(v, b);
-  if (len <= a.budget) return;
-  const int to = a.fresh[(size_t)b * a.fresh_w + index];
-  if (to < 0 || to >= v.num_pages) {
-    if (threadIdx.x == 0) kv8_flag(v);
-    return;
-  }
+  const int to = len > a.budget ? a.fresh[(size_t)b * a.fresh_w + index] : -1;
+  if (len > a.budget && (to < 0 || to >= v.num_pages) && threadIdx.x == 0) kv8_flag(v);
+  kv8_ready();
+  if (to < 0 || to >= v.num_pages) return;
   const int* kept = a.kept + ((size_t)b * v.kv_heads + g) * a.budget + ((size_t)index << v.page_shift);
   const int rows = min(1 << v.page_shift, a.budget - (index << v.page_shift));
-  int8_t* base = is_v ? v.V : v.K;
+  int8_t* codes = is_v ? v.V : v.K;
   float* scales = is_v ? v.v_scale : v.k_scale;
-  const int vshift = 31 - __clz(v.dim / 16);
-  const int mask = (1 << v.page_shift) - 1;
+  constexpr int ROW = D / 16;  // vectors of a row
   for (int r = threadIdx.x; r < rows; r += M_THREADS) {
     const int j = kept[r];  // within 0 .. len - 1: written by the selection
     const int page = kv8_page(v, b, j >> v.page_shift);
-    row_codes[r] = page < 0 ? nullptr : base + kv8_codes_at(v, page, g) + (size_t)(j & mask) * v.dim;
+    row_at[r] = page < 0 ? -1 : (long long)(kv8_codes_at(v, page, g) + (size_t)(j & ((1 << v.page_shift) - 1)) * D);
     row_scale[r] = page < 0 ? 0.f : scales[kv8_scale_at(v, page, g)];
   }
   __syncthreads();
-  const int nvec = rows << vshift, cmask = (1 << vshift) - 1;
+  const int nvec = rows * ROW, col = (int)threadIdx.x % ROW * 16;
   auto load = [&](int i) {
-    const int8_t* p = row_codes[i >> vshift];
-    return p ? __ldg(reinterpret_cast<const uint4*>(p) + (i & cmask)) : make_uint4(0, 0, 0, 0);
+    const long long at = row_at[i / ROW];
+    return at < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(codes + at + col);
   };
-  float m = 0.f;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < nvec; i += M_THREADS) {
-    const uint4 w = load(i);
-    // the largest |code| of the 16: rounding to float32 keeps order, so the
-    // largest |value| is the value of the largest |code|
-    uint32_t c = __vmaxu4(__vmaxu4(__vabs4(w.x), __vabs4(w.y)), __vmaxu4(__vabs4(w.z), __vabs4(w.w)));
-    c = __vmaxu4(c, c >> 16);
-    const uint32_t top = max(c & 255u, (c >> 8) & 255u);
-    m = fmaxf(m, finite_abs((float)top * row_scale[i >> vshift]));
+  uint4 keep[M_HELD];
+#pragma unroll
+  for (int j = 0; j < M_HELD; ++j) {
+    const int i = threadIdx.x + j * M_THREADS;
+    keep[j] = i < nvec ? load(i) : make_uint4(0, 0, 0, 0);
   }
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < M_HELD; ++j) {
+    const int i = threadIdx.x + j * M_THREADS;
+    if (i < nvec) m = fmaxf(m, amax_of_codes(keep[j], row_scale[i / ROW]));
+  }
+  for (int i = threadIdx.x + M_HELD * M_THREADS; i < nvec; i += M_THREADS)
+    m = fmaxf(m, amax_of_codes(load(i), row_scale[i / ROW]));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < M_THREADS / 32; ++w) m = fmaxf(m, s_max[w]);
-  const float s = kv8_scale_of(m), inv = __fdiv_rn(1.0f, s);
-  if (threadIdx.x == 0) scales[kv8_scale_at(v, to, g)] = s;
-  uint4* dst = reinterpret_cast<uint4*>(base + kv8_codes_at(v, to, g));
-#pragma unroll 2
-  for (int i = threadIdx.x; i < nvec; i += M_THREADS) {
-    uint4 w = load(i);
-    const float so = row_scale[i >> vshift];
-    uint32_t* u = reinterpret_cast<uint32_t*>(&w);
+  const Kv8Scale s = kv8_rounding_to(kv8_scale_of(m));
+  if (threadIdx.x == 0) scales[kv8_scale_at(v, to, g)] = s.s;
+  uint4* dst = reinterpret_cast<uint4*>(codes + kv8_codes_at(v, to, g));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      int c[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) c[t] = kv8_code((float)kv8_byte(u[j], t) * so, s, inv);
-      u[j] = kv8_pack4(c[0], c[1], c[2], c[3]);
-    }
-    dst[i] = w;
+  for (int j = 0; j < M_HELD; ++j) {
+    const int i = threadIdx.x + j * M_THREADS;
+    if (i < nvec) dst[i] = kv8_requantise16(keep[j], row_scale[i / ROW], s);
   }
+#pragma unroll 1
+  for (int i = threadIdx.x + M_HELD * M_THREADS; i < nvec; i += M_THREADS)
+    dst[i] = kv8_requantise16(load(i), row_scale[i / ROW], s);
 }
 
 }  // namespace
@@ -302,18 +342,32 @@ cudaError_t launch_kv8_evict(const Kv8View& v, const float* weights, long long w
   const int page = 1 << v.page_shift, fresh_w = (int)(((long long)budget + page - 1) / page);
   const EvictArgs a{weights,   weights_ld, budget,      recent,         fresh_w, fresh,
                     table_out, lens_out,   weights_out, weights_out_ld, kept};
+  // As few CTAs of a cluster as hold the keys of the longest sequence: a barrier
+  // of the cluster costs more than a pass over some thousand keys.
+  int ranks = 1;
+  while (ranks < S_MOST && (v.max_len + ranks - 1) / ranks > S_KEYS) ranks *= 2;
+  const int share = (v.max_len + ranks - 1) / ranks;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(S_CTAS, (unsigned)v.kv_heads, (unsigned)v.num_seqs);
+  cfg.gridDim = dim3((unsigned)ranks, (unsigned)v.kv_heads, (unsigned)v.num_seqs);
   cfg.blockDim = dim3(S_THREADS);
+  cfg.dynamicSmemBytes = (size_t)(share < S_KEYS ? share : S_KEYS) * sizeof(uint32_t);
   cfg.stream = s;
   cudaLaunchAttribute attr[2] = {pdl_attr()};
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = S_CTAS;
+  attr[1].val.clusterDim.x = (unsigned)ranks;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_select_kernel, v, a);
+  static bool ready[64] = {};  // the attribute is set once for each device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev < 0 || dev >= 64 || !ready[dev])) {
+    e = cudaFuncSetAttribute(kv8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             S_KEYS * (int)sizeof(uint32_t));
+    if (e == cudaSuccess && dev >= 0 && dev < 64) ready[dev] = true;
+  }
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kv8_select_kernel, v, a);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t mcfg = {};
   mcfg.gridDim = dim3((unsigned)fresh_w * v.kv_heads, 2, (unsigned)v.num_seqs);
@@ -321,7 +375,9 @@ cudaError_t launch_kv8_evict(const Kv8View& v, const float* weights, long long w
   mcfg.stream = s;
   mcfg.attrs = attr;
   mcfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&mcfg, kv8_move_kernel, v, a);
+  if (v.dim == 64) return cudaLaunchKernelEx(&mcfg, kv8_move_kernel<64>, v, a);
+  if (v.dim == 128) return cudaLaunchKernelEx(&mcfg, kv8_move_kernel<128>, v, a);
+  return cudaLaunchKernelEx(&mcfg, kv8_move_kernel<256>, v, a);
 }
 
 }  // namespace apr
