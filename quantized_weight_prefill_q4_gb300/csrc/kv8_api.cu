@@ -261,7 +261,7 @@ int run_evict(const apr_kv8_cache* cache, const apr_kv8_rows* rows, const float*
     if (!on4(p)) return set_error(APR_E_ALIGN, "an argument is not 4-byte aligned");
   const size_t bg = (size_t)w.num_seqs * w.kv_heads, page = (size_t)1 << w.page_shift;
   const size_t fresh = (budget + page - 1) / page;
-  if (fresh * w.kv_heads > 0x7fffffffull) return set_error(APR_E_INVAL, "sizes beyond the supported limits");
+  if (2 * fresh * w.kv_heads > 0x7fffffffull) return set_error(APR_E_INVAL, "sizes beyond the supported limits");
   const size_t cb = code_bytes(w), sb = scale_bytes(w);
   const Range outs[] = {{table_out, table_bytes(w), "table_out"},
                         {lens_out, (size_t)w.num_seqs * 4, "lens_out"},

@@ -15,8 +15,8 @@
 // time) and one byte a value written; the rounding is five instructions and a
 // byte permute a value (kv8_codes8).
 //
-// Read. One CTA per 32 packed rows and some heads, K or V; a thread's 16-byte
-// stores cover neighbouring elements of a row.
+// Read. One CTA per 16 or 32 packed rows and some heads, K or V; a thread's
+// 16-byte stores cover neighbouring elements of a row.
 
 #include "apr_internal.h"
 #include "host_common.h"
@@ -82,17 +82,20 @@ template <typename T, int D>
 __global__ void __launch_bounds__(A_THREADS) kv8_append_kernel(const __grid_constant__ Kv8View v,
                                                                const T* __restrict__ k, const T* __restrict__ vv,
                                                                long long ld, int heads_a_cta) {
+  // the CTAs of a page, K and V and all heads, are neighbours: the rows they read are
+  const int parts = 2 * ((v.kv_heads + heads_a_cta - 1) / heads_a_cta);
+  const int unit = (int)(blockIdx.x / parts), part = (int)(blockIdx.x % parts);
   constexpr int HELD = 16 / sizeof(T);  // vectors of 8 values a thread keeps between the passes, 32 registers
   constexpr int ROW = D / 8;            // vectors of a row
   __shared__ float s_max[3][A_WARPS];
   __shared__ int s_scan[A_WARPS];
   __shared__ int s_find[2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool is_v = blockIdx.y & 1;
-  const int g0 = (int)(blockIdx.y >> 1) * heads_a_cta, g1 = min(g0 + heads_a_cta, v.kv_heads);
+  const bool is_v = part & 1;
+  const int g0 = (part >> 1) * heads_a_cta, g1 = min(g0 + heads_a_cta, v.kv_heads);
 
-  // ---- which page: the blockIdx.x-th of those that the sequences touch
-  int b = (int)blockIdx.x, slot = 0;
+  // ---- which page: the unit-th of those that the sequences touch
+  int b = unit, slot = 0;
   if (v.row_start) {
     const int run = (v.num_seqs + A_THREADS - 1) / A_THREADS;
     const int b0 = min((int)threadIdx.x * run, v.num_seqs), b1 = min(b0 + run, v.num_seqs);
@@ -109,12 +112,11 @@ __global__ void __launch_bounds__(A_THREADS) kv8_append_kernel(const __grid_cons
     __syncthreads();
     int at = inc - mine;
     for (int w = 0; w < warp; ++w) at += s_scan[w];
-    const int want = (int)blockIdx.x;
-    if (at <= want && want < at + mine) {
+    if (at <= unit && unit < at + mine) {
       int i = b0;
-      for (int n; at + (n = pages_touched(v, i)) <= want; ++i) at += n;
+      for (int n; at + (n = pages_touched(v, i)) <= unit; ++i) at += n;
       s_find[0] = i;
-      s_find[1] = want - at;
+      s_find[1] = unit - at;
     }
     __syncthreads();
     b = s_find[0];
@@ -193,9 +195,9 @@ __global__ void __launch_bounds__(A_THREADS) kv8_append_kernel(const __grid_cons
 
 // ---------------------------------------------------------------- read
 constexpr int R_THREADS = 256;
-constexpr int R_ROWS = 32;  // packed rows of a CTA
 
-template <typename T, int D>
+// R_ROWS: packed rows of a CTA.
+template <typename T, int D, int R_ROWS>
 __global__ void __launch_bounds__(R_THREADS) kv8_read_kernel(const __grid_constant__ Kv8View v, T* __restrict__ k,
                                                              T* __restrict__ vv, long long ld, int heads_a_cta) {
   constexpr int N = 16 / sizeof(T);             // values of a 16-byte store
@@ -205,9 +207,10 @@ __global__ void __launch_bounds__(R_THREADS) kv8_read_kernel(const __grid_consta
   __shared__ const int8_t* s_codes[R_ROWS];     // a row's codes of head g0; nullptr: none
   __shared__ const float* s_scale[R_ROWS];
   __shared__ int s_zero[R_ROWS];                // a row before its sequence's start
-  const int row0 = (int)blockIdx.x * R_ROWS;
-  const bool is_v = blockIdx.y & 1;
-  const int g0 = (int)(blockIdx.y >> 1) * heads_a_cta, g1 = min(g0 + heads_a_cta, v.kv_heads);
+  const int parts = 2 * ((v.kv_heads + heads_a_cta - 1) / heads_a_cta), part = (int)(blockIdx.x % parts);
+  const int row0 = (int)(blockIdx.x / parts) * R_ROWS;
+  const bool is_v = part & 1;
+  const int g0 = (part >> 1) * heads_a_cta, g1 = min(g0 + heads_a_cta, v.kv_heads);
   if (threadIdx.x < R_ROWS) {
     const int row = row0 + (int)threadIdx.x;
     int b = row;
@@ -305,7 +308,7 @@ cudaError_t append_shape(const Kv8View& v, const void* k, const void* vv, long l
   const long long pages = v.row_start ? (v.num_rows >> v.page_shift) + 2ll * v.num_seqs : v.num_seqs;
   const int heads = heads_a_cta(pages, v.kv_heads, 12);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)pages, 2u * ((v.kv_heads + heads - 1) / heads));
+  cfg.gridDim = dim3((unsigned)(pages * 2 * ((v.kv_heads + heads - 1) / heads)));
   cfg.blockDim = dim3(A_THREADS);
   cfg.stream = s;
   cudaLaunchAttribute attr[1] = {pdl_attr()};
@@ -314,17 +317,26 @@ cudaError_t append_shape(const Kv8View& v, const void* k, const void* vv, long l
   return cudaLaunchKernelEx(&cfg, kv8_append_kernel<T, D>, v, (const T*)k, (const T*)vv, ld, heads);
 }
 
-template <typename T, int D>
-cudaError_t read_shape(const Kv8View& v, void* k, void* vv, long long ld, cudaStream_t s) {
-  const int units = (v.num_rows + R_ROWS - 1) / R_ROWS, heads = heads_a_cta(units, v.kv_heads, 4);
+template <typename T, int D, int R_ROWS>
+cudaError_t launch_read(const Kv8View& v, void* k, void* vv, long long ld, cudaStream_t s) {
+  const long long units = (v.num_rows + R_ROWS - 1) / R_ROWS;
+  const int heads = heads_a_cta(units, v.kv_heads, 4);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)units, 2u * ((v.kv_heads + heads - 1) / heads));
+  cfg.gridDim = dim3((unsigned)(units * 2 * ((v.kv_heads + heads - 1) / heads)));
   cfg.blockDim = dim3(R_THREADS);
   cfg.stream = s;
   cudaLaunchAttribute attr[1] = {pdl_attr()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_read_kernel<T, D>, v, (T*)k, (T*)vv, ld, heads);
+  return cudaLaunchKernelEx(&cfg, kv8_read_kernel<T, D, R_ROWS>, v, (T*)k, (T*)vv, ld, heads);
+}
+
+// 16 rows a CTA where 32 would leave an SM few CTAs, whose start and end then
+// show (6007 float32 rows of 4 heads of 256: 10.4 us, 13.7 with 32); 32 where
+// there are many (33700 bf16 rows of 8 of 128: 37 us, 39 with 16).
+template <typename T, int D>
+cudaError_t read_shape(const Kv8View& v, void* k, void* vv, long long ld, cudaStream_t s) {
+  return v.num_rows < 32 * 3 * num_sms() / 2 ? launch_read<T, D, 16>(v, k, vv, ld, s) : launch_read<T, D, 32>(v, k, vv, ld, s);
 }
 
 template <typename T>

@@ -29,17 +29,17 @@
 // maximum and total, and a second kernel combines the pieces in order, a CTA for
 // each pair. (Having the last CTA of a segment combine them instead took 3 to 9
 // us more at the end of the measured cases: a fence behind every piece, and one
-// CTA's loads instead of all SMs'.) A third kernel, where the weights are wanted,
-// turns the scores that the first one kept into them once the totals are known.
+// CTA's loads instead of all SMs'.) Where the weights are wanted, more CTAs of the
+// second kernel turn the scores that the first one kept into them.
 //
-// A CTA. Its WARPS warps form WARPS / MT key groups; the groups take the tiles
-// of TILE positions in turn, and each of a group's MT warps 8 of the pairs. A group
-// streams its tiles through a ring of its own in shared memory by asynchronous
-// 16-byte copies (a tile's K, its V, the next tile's K, ...), so that warps do
-// not wait for one another. A row's 16-byte chunks are stored exclusive-or'ed
-// with bits of the row so that both products' reads are free of bank
-// conflicts: for K a quarter warp reads 4 chunks of 2 neighbouring rows, for V
-// 2 chunks of every other row of 8.
+// A CTA. Its warps take the piece's tiles of TILE positions in turn, each for
+// all the segment's pairs. A warp streams its tiles through a ring of its own in
+// shared memory by asynchronous 16-byte copies (a tile's K, its V, the next
+// tile's K, ...), so that warps do not wait for one another before the piece's
+// end, and the next piece's first chunks are on their way by then. A row's
+// 16-byte chunks are stored exclusive-or'ed with bits of the row so that both
+// products' reads are free of bank conflicts: for K a quarter warp reads 4
+// chunks of 2 neighbouring rows, for V 2 chunks of every other row of 8.
 // Lane (r, c) = (lane / 4, lane % 4) reads K's row 8 t + r, dims 16 c .. + 15 of
 // each 64: word w holds its 4 dims of k-step w, an order of the dims that the
 // query's fragments share. For V it reads dims 16 r .. + 15 of each 128 of the
@@ -50,10 +50,12 @@
 //
 // Measured (GB300, back to back in a graph): 48 sequences of 130 to 9000 tokens,
 // 32 heads over 8 of 128: 43.5 us, 207 MB (0.71 of the HBM rate); 3 of 100000 to
-// 131000, 16 over 4 of 256: 116 us (0.90); one of 700: 8.9 us. Of the 43.5 us the
-// tiles stream at 6.3 TB/s for 33; the rest is the way to the first codes
-// (length, table, codes: 3 us), CTAs of equal shares that end up to 5 us apart,
-// and the combination (3 us).
+// 131000, 16 over 4 of 256: 116 us (0.90); one of 700: 8.5 us; with weights 16 of
+// 2000 to 12000, 32 over 4 of 128: 30 us, and 9 rows of each of 4 of 5000 to 8200,
+// 16 over 8 of 64: 26.5 us. Of the 43.5 us the tiles stream at 6.3 TB/s for 33;
+// the rest is the way to the first codes (length, table, codes: 3 us), CTAs of
+// equal shares that end up to 5 us apart, and the combination (3 us). The 9 rows
+// (18 pairs) are bound by the warps' instructions, 330 a tile and 8 pairs.
 
 #include "apr_internal.h"
 #include "host_common.h"
@@ -85,8 +87,10 @@ struct AttnArgs {
   int* prefix;       // [num_seqs + 1] first unit of each sequence, all units (written by CTA 0)
   float2* part_ml;   // [2 ctas][pairs] reference maximum and total of a piece
   float* part_o;     // [2 ctas][pairs][dim]
-  float2* final_ml;  // [rows][heads] maximum and 1 / total, or nullptr
-  float* scores;     // [rows][heads][scores_ld] scores in base 2, or nullptr
+  // For the weights, or nullptr. A sequence's (row, head) pairs are in the order
+  // of the KV heads they read, pair_at() says where.
+  float2* final_ml;  // [rows * heads] maximum and 1 / total
+  float* scores;     // [rows * heads][scores_ld] scores in base 2
   int scores_ld;     // max_len rounded up to whole tiles
   float* weights;
   long long weights_ld;
@@ -197,48 +201,57 @@ __device__ __forceinline__ void store4_any(void* p, int type, size_t i, const fl
 __device__ __forceinline__ float piece_factor(float2 ml, float m) {
   return ml.y > 0.f ? exp2f(ml.x - m) : (ml.y != ml.y ? 1.f : 0.f);
 }
-// Four dims from d of a (row, head)'s output, from its unnormalised sums and total.
-__device__ __forceinline__ void finish4(const AttnArgs& a, size_t row, size_t head, int dim, int d, const float4& o,
-                                        float m, float total) {
-  const float inv = total > 0.f || total != total ? 1.f / total : 0.f;  // no position seen: zeros
-  store4_any(a.out, a.type, row * a.ldo + head * dim + d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-  if (a.final_ml && d == 0) a.final_ml[row * a.heads + head] = make_float2(m, inv);
+// Where the weights' arrays have pair 0 of a sequence's rows and KV head.
+__device__ __forceinline__ size_t pair_at(const AttnArgs& a, int r0, int n, int g) {
+  return (size_t)r0 * a.heads + (size_t)g * n * a.group;
 }
 
-// CTAs on an SM: 12 warps, 8 at 256 dims, as registers (168 a thread, 255) and
-// shared memory allow. (At 128 dims 16 warps of 128 registers took 96 us for 4
-// sequences of 60000 where 12 take 83.)
-__host__ __device__ constexpr int ctas_per_sm(int dim, int mt) {
-  return dim <= 128 ? (mt == 1 ? 3 : 2) : (mt == 1 ? 2 : 1);
+// Four dims from d of a (row, head)'s output, from its unnormalised sums and total.
+__device__ __forceinline__ void finish4(const AttnArgs& a, int r0, int n, int g, int pair, int dim, int d,
+                                        const float4& o, float m, float total) {
+  const float inv = total > 0.f || total != total ? 1.f / total : 0.f;  // no position seen: zeros
+  const size_t row = r0 + pair / a.group, head = g * a.group + pair % a.group;
+  store4_any(a.out, a.type, row * a.ldo + head * dim + d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+  if (a.final_ml && d == 0) a.final_ml[pair_at(a, r0, n, g) + pair] = make_float2(m, inv);
 }
+
+// A warp's M tiles, MT: 1, or 2 where that leaves less to do for the longest
+// row group of a sequence: the codes are turned into fp16 once for both tiles,
+// so that a segment of two costs about 1.5 of one (16 pairs over 4 x 60000
+// positions of 128 dims: 112 us, 140 as two segments; 18 pairs over 4 x 8000 of
+// 64: 32 us, 29 as three). Only up to 128 dims, where the registers hold the sums
+// of 16 pairs. (The warps of a CTA sharing tiles between them, 8 pairs each, took
+// longer than more segments for any number of pairs: 152 us for the 16.)
+__host__ __device__ constexpr int m_tiles(int dim, long long pairs) {
+  return dim <= 128 && (pairs + 15) / 16 * 3 < (pairs + 7) / 8 * 2 ? 2 : 1;
+}
+
+// CTAs of 4 warps on an SM, as registers (168 a thread, 255) and shared memory
+// allow. (At 128 dims 16 warps of 128 registers took 96 us for 4 sequences of
+// 60000 where 12 take 83.)
+constexpr int WARPS = 4;
+constexpr int THREADS = 32 * WARPS;
+__host__ __device__ constexpr int ctas_per_sm(int dim, int mt) { return dim == 64 || (dim == 128 && mt == 1) ? 3 : 2; }
 
 template <int D, int MT>
 struct Shape {
   static constexpr int PAIRS = 8 * MT;
-  // small CTAs, several on an SM, so that one's start and end overlap the
-  // others' streams; more warps where the pairs take several for each tile
-  static constexpr int WARPS = MT == 1 ? 4 : 8;
-  static constexpr int THREADS = 32 * WARPS;
-  static constexpr int CTAS = ctas_per_sm(D, MT);
-  static constexpr int GROUPS = WARPS / MT;          // key groups
-  static constexpr int SLOT = TILE * D;              // bytes of a tile's K or V
-  static constexpr int SLOTS = MT == 1 ? 3 : 4;      // of a group's ring
-  static constexpr int CHUNKS = SLOT / 16 / (32 * MT);  // 16-byte copies a lane and slot
-  static constexpr int STEPS = D / 16;               // k-steps of a score
-  static constexpr int RING = GROUPS * SLOTS * SLOT;
-  static constexpr int OFF_Q = RING;
-  // the warps' sums, 8 rows each: with one M tile in the last slot of the
-  // warp's own ring (of the same size), which the next piece's first chunks do not use
-  static constexpr int OFF_M = MT == 1 ? (SLOTS - 1) * SLOT : OFF_Q + MT * STEPS * 512;
-  static constexpr int M_STEP = MT == 1 ? SLOTS * SLOT : 8 * D * 4;
-  static constexpr int BYTES = OFF_Q + MT * STEPS * 512 + (MT == 1 ? 0 : WARPS * 8 * D * 4);
-  static_assert(8 * D * 4 == SLOT && CHUNKS >= 1, "a warp's sums fill a slot");
+  static constexpr int SLOT = TILE * D;     // bytes of a tile's K or V
+  static constexpr int SLOTS = 3;           // of a warp's ring
+  static constexpr int STEPS = D / 16;      // k-steps of a score
+  static constexpr int OFF_Q = WARPS * SLOTS * SLOT;
+  // A warp's sums of an M tile, 8 rows, are as large as a slot: those of the
+  // first lie in the last slot of its own ring, which the next piece's first
+  // chunks do not use.
+  static constexpr int OFF_M = OFF_Q + MT * STEPS * 512;
+  static constexpr int BYTES = OFF_M + (MT - 1) * WARPS * SLOT;
+  static_assert(8 * D * 4 == SLOT, "a warp's sums fill a slot");
 };
 
 template <int D, int MT>
-__global__ void __launch_bounds__(Shape<D, MT>::THREADS, Shape<D, MT>::CTAS) kv8_attention_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(THREADS, ctas_per_sm(D, MT))
+    kv8_attention_kernel(const __grid_constant__ AttnArgs a) {
   using S = Shape<D, MT>;
-  constexpr int WARPS = S::WARPS, THREADS = S::THREADS;
   // no early launch of the next kernel: its CTAs would take the places of this
   // grid's as they free up, and those of the next call's grid would find some
   // SMs full (48 ragged sequences: 50 us so, 64 us with it)
@@ -246,13 +259,12 @@ __global__ void __launch_bounds__(Shape<D, MT>::THREADS, Shape<D, MT>::CTAS) kv8
   __shared__ int s_scan[WARPS];
   __shared__ int s_find[2];
   __shared__ float s_factor[S::PAIRS];          // score of a pair = factor * (K scale) * sum of products
-  __shared__ float2 s_ml[WARPS][8];
+  __shared__ float2 s_ml[WARPS][S::PAIRS];
   const Kv8View& v = a.v;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
-  const int mt = warp % MT, kg = warp / MT;
-  uint8_t* ring = smem + kg * S::SLOTS * S::SLOT;
+  uint8_t* ring = smem + warp * S::SLOTS * S::SLOT;
   const uint32_t ring_u32 = smem_u32(ring);
-  const uint4* sq = reinterpret_cast<const uint4*>(smem + S::OFF_Q) + mt * S::STEPS * 32 + lane;
+  const uint4* sq = reinterpret_cast<const uint4*>(smem + S::OFF_Q) + lane;
 
   // ---- the units of the sequences, and where this CTA's share begins: a
   // thread counts the units of `run` neighbouring sequences
@@ -293,7 +305,7 @@ __global__ void __launch_bounds__(Shape<D, MT>::THREADS, Shape<D, MT>::CTAS) kv8
   // ---- the piece of work at hand
   int len, g, p0, np, first, seg_end, ue, k0, mine;
   Kv8Span span;
-  uint32_t at_next = 0;           // lane i: the place in the cache, in tiles, of the group's tile 32 n + i
+  uint32_t at_next = 0;           // lane i: the place in the cache, in tiles, of the warp's tile 32 n + i
   float ks_all = 0.f, vs_all = 0.f;  // and its scales
   constexpr int QP = S::PAIRS / WARPS, QV = (D + 127) / 128;
   float4 x[QP][QV];               // the pairs' query rows, on their way
@@ -301,12 +313,12 @@ __global__ void __launch_bounds__(Shape<D, MT>::THREADS, Shape<D, MT>::CTAS) kv8
   const int in_page = (1 << v.page_shift) / TILE - 1;
   // (page ids out of range read page 0, and are flagged)
   auto tile_of = [&](int i, size_t* scale_at) {
-    const int k = k0 + (kg + min(i, mine - 1) * S::GROUPS) * TILE;
+    const int k = k0 + (warp + min(i, mine - 1) * WARPS) * TILE;
     const int page = max(kv8_page(v, b, k >> v.page_shift), 0);
     *scale_at = kv8_scale_at(v, page, g);
     return (uint32_t)(*scale_at << (v.page_shift - 5)) + (uint32_t)((k / TILE) & in_page);
   };
-  // sends chunk n of the group (tile n / 2; its K, then its V) into the ring
+  // sends chunk n of the warp's (tile n / 2; its K, then its V) into the ring
   auto send = [&](int n) {
     if (n < 2 * mine) {
       const int i = n >> 1;
@@ -318,18 +330,12 @@ __global__ void __launch_bounds__(Shape<D, MT>::THREADS, Shape<D, MT>::CTAS) kv8
       const int8_t* src = (n & 1 ? v.V : v.K) + (size_t)at * S::SLOT;
       const uint32_t dst = ring_u32 + (n % S::SLOTS) * S::SLOT;
 #pragma unroll
-      for (int j = 0; j < S::CHUNKS; ++j) {
-        const int y = (j * MT + mt) * 32 + lane;
+      for (int j = 0; j < S::SLOT / 512; ++j) {
+        const int y = j * 32 + lane;
         copy_async_16(dst + swizzled<D>(y) * 16, src + y * 16);
       }
     }
     copy_commit();
-  };
-  auto group_sync = [&] {
-    if (MT == 1)
-      __syncwarp();
-    else
-      named_sync(1 + kg, 32 * MT);
   };
   // the next piece of this CTA's share, if there is one: its first tiles and its query rows under way
   auto begin = [&]() -> bool {
@@ -355,9 +361,9 @@ __global__ void __launch_bounds__(Shape<D, MT>::THREADS, Shape<D, MT>::CTAS) kv8
     }
     k0 = max(u - first, 0) * UNIT;
     const int k1 = min(len, (ue - first) * UNIT);
-    // this group's tiles: kg, kg + GROUPS, ... of the piece's
+    // this warp's tiles: every WARPS-th of the piece's
     const int tiles = k1 > k0 ? (k1 - k0 + TILE - 1) / TILE : 0;
-    mine = tiles > kg ? (tiles - kg + S::GROUPS - 1) / S::GROUPS : 0;
+    mine = tiles > warp ? (tiles - warp + WARPS - 1) / WARPS : 0;
     if (mine > 0) {
       size_t scale_at;
       at_next = tile_of(lane, &scale_at);
@@ -421,21 +427,31 @@ __global__ void __launch_bounds__(Shape<D, MT>::THREADS, Shape<D, MT>::CTAS) kv8
     }
     __syncthreads();
 
-    // this lane's pair: row r of its M tile
-    const int pair = p0 + 8 * mt + r;
-    const bool live = 8 * mt + r < np;
-    const int limit = live ? min(len, len - span.n + pair / a.group + 1) : 0;  // positions the pair sees
-    const int least = len - span.n + (p0 + 8 * mt) / a.group + 1;              // the fewest of this M tile's
-    const float factor = s_factor[8 * mt + r];
-    float* score_row = nullptr;
-    if (a.scores && live)
-      score_row = a.scores +
-                  ((size_t)(span.r0 + pair / a.group) * a.heads + g * a.group + pair % a.group) * a.scores_ld + 2 * c;
-
-    float ref = -INFINITY, l = 0.f;
-    float2 sum[D / 8];  // [column 4 w + t of each 128 dims]: dims 32 c + (4 w + t) and + 16 (D = 64: 16 c and + 8)
+    // this lane's pairs: row r of each M tile
+    int limit[MT];        // positions that the pair sees
+    float factor[MT];
+    float* score_row[MT];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) sum[i] = make_float2(0.f, 0.f);
+    for (int t = 0; t < MT; ++t) {
+      const int pair = p0 + 8 * t + r;
+      const bool live = 8 * t + r < np;
+      limit[t] = live ? min(len, len - span.n + pair / a.group + 1) : 0;
+      factor[t] = s_factor[8 * t + r];
+      score_row[t] = nullptr;
+      if (a.scores && live)
+        score_row[t] = a.scores + (pair_at(a, span.r0, span.n, g) + pair) * a.scores_ld + 2 * c;
+    }
+    const int least = len - span.n + p0 / a.group + 1;  // the fewest of these pairs'
+
+    float ref[MT], l[MT];
+    float2 sum[MT][D / 8];  // [column 4 w + t of each 128 dims]: dims 32 c + (4 w + t) and + 16 (D = 64: 16 c and + 8)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      ref[t] = -INFINITY;
+      l[t] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) sum[t][i] = make_float2(0.f, 0.f);
+    }
 
 #pragma unroll 1
     for (int i = 0; i < mine; ++i) {
@@ -446,22 +462,18 @@ __global__ void __launch_bounds__(Shape<D, MT>::THREADS, Shape<D, MT>::CTAS) kv8
         vs_all = v.v_scale[scale_at];
       }
       const float ks = __shfl_sync(0xffffffffu, ks_all, i & 31), vs = __shfl_sync(0xffffffffu, vs_all, i & 31);
-      const int k = k0 + (kg + i * S::GROUPS) * TILE;
+      const int k = k0 + (warp + i * WARPS) * TILE;
 
       // ---- scores of the tile's 32 positions: 4 columns of 8
       copy_wait<S::SLOTS - 2>();
-      group_sync();
+      __syncwarp();
       send(2 * i + S::SLOTS - 1);
-      if (MT > 1 && 8 * mt >= np) {  // no pair of this warp's M tile: it only copies
-        copy_wait<S::SLOTS - 2>();
-        group_sync();
-        send(2 * i + S::SLOTS);
-        continue;
-      }
       const uint8_t* kt = ring + (2 * i) % S::SLOTS * S::SLOT;
-      float s[4][4];
+      float s[MT][4][4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) s[m][t][0] = s[m][t][1] = s[m][t][2] = s[m][t][3] = 0.f;
 #pragma unroll
       for (int d64 = 0; d64 < D / 64; ++d64) {
         uint4 kw[4];
@@ -470,69 +482,76 @@ __global__ void __launch_bounds__(Shape<D, MT>::THREADS, Shape<D, MT>::CTAS) kv8
           kw[t] = *reinterpret_cast<const uint4*>(kt + swizzled<D>((8 * t + r) * (D / 16) + 4 * d64 + c) * 16);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const uint4 qa = sq[(4 * d64 + w) * 32];
+          uint4 qa[MT];
+#pragma unroll
+          for (int m = 0; m < MT; ++m) qa[m] = sq[(m * S::STEPS + 4 * d64 + w) * 32];
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
             const uint32_t x = (w == 0 ? kw[t].x : w == 1 ? kw[t].y : w == 2 ? kw[t].z : kw[t].w) ^ 0x80808080u;
-            mma16816(s[t], qa, half2_of_codes(x, 0x4140), half2_of_codes(x, 0x4342));
+            const uint32_t b0 = half2_of_codes(x, 0x4140), b1 = half2_of_codes(x, 0x4342);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) mma16816(s[m][t], qa[m], b0, b1);
           }
         }
       }
 
       // ---- the softmax weights
-      const float kf = ks * factor;
-      float top = -INFINITY;
+      uint4 pa[MT][2];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const float2 both = __fmul2_rn(__fadd2_rn(make_float2(s[t][0], s[t][1]), make_float2(s[t][2], s[t][3])),
-                                       make_float2(kf, kf));
-        s[t][0] = both.x;
-        s[t][1] = both.y;
-      }
-      if (k + TILE > least) {
+      for (int m = 0; m < MT; ++m) {
+        const float kf = ks * factor[m];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const int j = k + 8 * t + 2 * c;
-          if (j >= limit) s[t][0] = -INFINITY;
-          if (j + 1 >= limit) s[t][1] = -INFINITY;
+          const float2 both = __fmul2_rn(__fadd2_rn(make_float2(s[m][t][0], s[m][t][1]), make_float2(s[m][t][2], s[m][t][3])),
+                                         make_float2(kf, kf));
+          s[m][t][0] = both.x;
+          s[m][t][1] = both.y;
         }
-      }
-      if (score_row) {
+        if (k + TILE > least) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) *reinterpret_cast<float2*>(score_row + k + 8 * t) = make_float2(s[t][0], s[t][1]);
-      }
-#pragma unroll
-      for (int t = 0; t < 4; ++t) top = fmaxf(top, fmaxf(s[t][0], s[t][1]));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      if (__any_sync(0xffffffffu, top > ref + MOVE_ABOVE)) {
-        const float now = fmaxf(ref, top);
-        const float f = ref == -INFINITY ? 0.f : exp2_fast(ref - now);
-        l *= f;
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j)
-          sum[j] = __fmul2_rn(sum[j], make_float2(f, f));
-        ref = now;
-      }
-      const float shift = ref == -INFINITY ? 0.f : ref - HEADROOM;
-      uint4 pa[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint32_t hi[2], lo[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float x = exp2_fast(s[2 * j + h][0] - shift), y = exp2_fast(s[2 * j + h][1] - shift);
-          l += x + y;
-          hi[h] = half2_bits(x, y);
-          const float2 f = half2_values(hi[h]);
-          lo[h] = half2_bits(x - f.x, y - f.y);
+          for (int t = 0; t < 4; ++t) {
+            const int j = k + 8 * t + 2 * c;
+            if (j >= limit[m]) s[m][t][0] = -INFINITY;
+            if (j + 1 >= limit[m]) s[m][t][1] = -INFINITY;
+          }
         }
-        pa[j] = make_uint4(hi[0], lo[0], hi[1], lo[1]);
+        if (score_row[m]) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+            *reinterpret_cast<float2*>(score_row[m] + k + 8 * t) = make_float2(s[m][t][0], s[m][t][1]);
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) top = fmaxf(top, fmaxf(s[m][t][0], s[m][t][1]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        if (__any_sync(0xffffffffu, top > ref[m] + MOVE_ABOVE)) {
+          const float now = fmaxf(ref[m], top);
+          const float f = ref[m] == -INFINITY ? 0.f : exp2_fast(ref[m] - now);
+          l[m] *= f;
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j) sum[m][j] = __fmul2_rn(sum[m][j], make_float2(f, f));
+          ref[m] = now;
+        }
+        const float shift = ref[m] == -INFINITY ? 0.f : ref[m] - HEADROOM;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float x = exp2_fast(s[m][2 * j + h][0] - shift), y = exp2_fast(s[m][2 * j + h][1] - shift);
+            l[m] += x + y;
+            hi[h] = half2_bits(x, y);
+            const float2 f = half2_values(hi[h]);
+            lo[h] = half2_bits(x - f.x, y - f.y);
+          }
+          pa[m][j] = make_uint4(hi[0], lo[0], hi[1], lo[1]);
+        }
       }
 
       // ---- their product with the tile's V
       copy_wait<S::SLOTS - 2>();
-      group_sync();
+      __syncwarp();
       send(2 * i + S::SLOTS);
       const uint8_t* vt = ring + (2 * i + 1) % S::SLOTS * S::SLOT;
       constexpr int COLS = D >= 128 ? 16 : 8;  // columns a lane's bytes of a row give
@@ -554,9 +573,11 @@ __global__ void __launch_bounds__(Shape<D, MT>::THREADS, Shape<D, MT>::CTAS) kv8
           }
 #pragma unroll
         for (int w = 0; w < COLS / 4; ++w) {
-          float o[4][4];
+          float o[MT][4][4];
 #pragma unroll
-          for (int t = 0; t < 4; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) o[m][t][0] = o[m][t][1] = o[m][t][2] = o[m][t][3] = 0.f;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             uint32_t x[2][2];  // [rows 2 c, 2 c + 1 or + 8][columns 0, 1 or 2, 3]: the two rows' bytes side by side
@@ -568,136 +589,193 @@ __global__ void __launch_bounds__(Shape<D, MT>::THREADS, Shape<D, MT>::CTAS) kv8
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
               const uint32_t sel = t & 1 ? 0x4342 : 0x4140;
-              mma16816(o[t], pa[j], half2_of_codes(x[0][t / 2], sel), half2_of_codes(x[1][t / 2], sel));
+              const uint32_t b0 = half2_of_codes(x[0][t / 2], sel), b1 = half2_of_codes(x[1][t / 2], sel);
+#pragma unroll
+              for (int m = 0; m < MT; ++m) mma16816(o[m][t], pa[m][j], b0, b1);
             }
           }
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            float2& to = sum[COLS * dc + 4 * w + t];
-            to = __ffma2_rn(make_float2(vs, vs), __fadd2_rn(make_float2(o[t][0], o[t][1]), make_float2(o[t][2], o[t][3])), to);
-          }
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              float2& to = sum[m][COLS * dc + 4 * w + t];
+              to = __ffma2_rn(make_float2(vs, vs),
+                              __fadd2_rn(make_float2(o[m][t][0], o[m][t][1]), make_float2(o[m][t][2], o[m][t][3])), to);
+            }
         }
       }
     }
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
-    group_sync();  // every warp of the group is done with the ring
+    __syncwarp();  // every lane is done with the ring
 
     // ---- the next piece begins while the warps' sums of this one are added up, in order
     const bool whole = u <= first && ue == seg_end;
-    const int done_np = np, done_g = g, done_p0 = p0, done_r0 = span.r0;
+    const int done_np = np, done_g = g, done_p0 = p0;
+    const Kv8Span done = span;
     const size_t slot = (size_t)(2 * blockIdx.x + (u_begin > first ? 0 : 1)) * S::PAIRS;
     u = ue;
     more = begin();
-    auto merge = [&](int w) { return reinterpret_cast<float*>(smem + S::OFF_M + w * S::M_STEP); };  // warp w's [8][D]
-    if (c == 0) s_ml[warp][r] = make_float2(ref == -INFINITY ? -INFINITY : ref - HEADROOM, l);
-    {
-      float* to = merge(warp) + r * D;
+    auto merge = [&](int w, int m) {  // warp w's [8][D] of M tile m
+      return reinterpret_cast<float*>(smem + (m == 0 ? (w * S::SLOTS + S::SLOTS - 1) * S::SLOT : S::OFF_M + w * S::SLOT));
+    };
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      l[m] += __shfl_xor_sync(0xffffffffu, l[m], 1);
+      l[m] += __shfl_xor_sync(0xffffffffu, l[m], 2);
+      if (c == 0) s_ml[warp][8 * m + r] = make_float2(ref[m] == -INFINITY ? -INFINITY : ref[m] - HEADROOM, l[m]);
+      float* to = merge(warp, m) + r * D;
       constexpr int COLS = D >= 128 ? 16 : 8;
 #pragma unroll
       for (int dc = 0; dc < (D + 127) / 128; ++dc)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int i = 0; i < COLS; i += 4)
+          for (int i = 0; i < COLS; i += 4) {
+            const float2* f = sum[m] + COLS * dc + i;
             *reinterpret_cast<float4*>(to + 128 * dc + (2 * c + h) * COLS + i) =
-                h ? make_float4(sum[COLS * dc + i].y, sum[COLS * dc + i + 1].y, sum[COLS * dc + i + 2].y, sum[COLS * dc + i + 3].y)
-                  : make_float4(sum[COLS * dc + i].x, sum[COLS * dc + i + 1].x, sum[COLS * dc + i + 2].x, sum[COLS * dc + i + 3].x);
+                h ? make_float4(f[0].y, f[1].y, f[2].y, f[3].y) : make_float4(f[0].x, f[1].x, f[2].x, f[3].x);
+          }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < done_np * (D / 4); i += THREADS) {
       const int p = i / (D / 4), d = 4 * (i % (D / 4));
       float m = -INFINITY, all = 0.f;
 #pragma unroll
-      for (int w = 0; w < S::GROUPS; ++w) m = fmaxf(m, s_ml[w * MT + p / 8][p % 8].x);
+      for (int w = 0; w < WARPS; ++w) m = fmaxf(m, s_ml[w][p].x);
       if (m == -INFINITY) m = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < S::GROUPS; ++w) {
-        const float2 ml = s_ml[w * MT + p / 8][p % 8];
+      for (int w = 0; w < WARPS; ++w) {
+        const float2 ml = s_ml[w][p];
         const float f = piece_factor(ml, m);
-        const float4 y = *reinterpret_cast<const float4*>(merge(w * MT + p / 8) + (p % 8) * D + d);
+        const float4 y = *reinterpret_cast<const float4*>(merge(w, p / 8) + (p % 8) * D + d);
         all = fmaf(f, ml.y, all);
         o = make_float4(fmaf(f, y.x, o.x), fmaf(f, y.y, o.y), fmaf(f, y.z, o.z), fmaf(f, y.w, o.w));
       }
       if (whole) {
-        finish4(a, done_r0 + (done_p0 + p) / a.group, done_g * a.group + (done_p0 + p) % a.group, D, d, o, m, all);
+        finish4(a, done.r0, done.n, done_g, done_p0 + p, D, d, o, m, all);
       } else {
         if (d == 0) a.part_ml[slot + p] = make_float2(m, all);
         *reinterpret_cast<float4*>(a.part_o + (slot + p) * D + d) = o;
       }
     }
-    // (the fragments are written, and synchronised on, before the last slots are sent into again)
+    // (the next fragments are written, and synchronised on, before these slots are sent into again)
   }
 }
 
-// The pieces of the segments that more than one CTA had. A CTA for each (row,
-// head): D / 4 threads take four dims each of every GROUPS-th piece, so that
-// the loads are under way at once, then add up.
+// Of which CTAs a segment has pieces: c0 and how many from there on. The first
+// wrote its piece as the segment that it began, the others as the one that they
+// continued.
+struct Pieces {
+  int c0, n;
+  __device__ __forceinline__ size_t slot(const AttnArgs& a, int i, int pair) const {
+    return (size_t)(2 * (c0 + i) + (i == 0)) * a.pairs + pair % a.pairs;
+  }
+};
+template <int D>
+__device__ __forceinline__ Pieces pieces_of(const AttnArgs& a, int total, int seq_u0, int su, int g, int pair) {
+  const int u0 = seq_u0 + (pair / a.pairs * a.v.kv_heads + g) * su, ctas = sharing_ctas(a, total);
+  const int c0 = cta_of(u0 + overhead_units(D), ctas, total);
+  return Pieces{c0, cta_of(u0 + su - 1, ctas, total) - c0 + 1};
+}
+
+// The combination's CTAs, blockIdx.x < combine_ctas: one for each (row, head)
+// pair, D / 4 threads take four dims each of every GROUPS-th of its pieces, so
+// that the loads are under way at once, then add up. The weights' CTAs behind
+// them: each 4 positions a thread of a KV head; 8 threads find the maximum and
+// total of a pair from its pieces' anew, 64 pairs at a time, and each thread adds
+// up its positions' weights in the pairs' order.
+constexpr int W_PAIRS = 64;
+
 template <int D, int GROUPS>
-__global__ void __launch_bounds__(D / 4 * GROUPS) kv8_combine_kernel(const __grid_constant__ AttnArgs a) {
-  constexpr int LANES = D / 4;
+__global__ void __launch_bounds__(D / 4 * GROUPS) kv8_finish_kernel(const __grid_constant__ AttnArgs a, int combine_ctas) {
+  constexpr int LANES = D / 4, THREADS = LANES * GROUPS;
   __shared__ float4 s_o[GROUPS][LANES];
-  __shared__ float2 s_ml[GROUPS];
+  __shared__ float2 s_ml[GROUPS > W_PAIRS ? GROUPS : W_PAIRS];
   const Kv8View& v = a.v;
-  const int b = blockIdx.y, g = (int)(blockIdx.x % v.kv_heads), pair = (int)(blockIdx.x / v.kv_heads);
-  const int su = segment_units(a, kv8_len(v, b));
+  const int b = blockIdx.y, len = kv8_len(v, b), su = segment_units(a, len);
   const Kv8Span span = kv8_rows(v, b);
+  const int pairs = span.n * a.group;  // of a KV head
   kv8_ready();
   grid_launch_dependents();
   const int total = a.prefix[v.num_seqs], seq_u0 = a.prefix[b];
-  if (pair >= span.n * a.group) return;
-  const int u0 = seq_u0 + (pair / a.pairs * v.kv_heads + g) * su, ctas = sharing_ctas(a, total);
-  const int c0 = cta_of(u0 + overhead_units(D), ctas, total), n = cta_of(u0 + su - 1, ctas, total) - c0 + 1;
-  if (n == 1) return;
-  const int group = threadIdx.x / LANES, d = 4 * (threadIdx.x % LANES);
-  float m = -INFINITY, all = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto take = [&](float2 ml, const float4& x) {  // the reference follows the largest so far
-    const float now = ml.y > 0.f ? fmaxf(m, ml.x) : m;
-    const float keep = m == now ? 1.f : exp2f(m - now), f = piece_factor(ml, now);
-    m = now;
-    all = fmaf(f, ml.y, all * keep);
-    o = make_float4(fmaf(f, x.x, o.x * keep), fmaf(f, x.y, o.y * keep), fmaf(f, x.z, o.z * keep),
-                    fmaf(f, x.w, o.w * keep));
-  };
-#pragma unroll 8
-  for (int i = group; i < n; i += GROUPS) {
-    // the first CTA wrote it as the segment that it began, the others as the one that they continued
-    const size_t slot = (size_t)(2 * (c0 + i) + (i == 0)) * a.pairs + pair % a.pairs;
-    take(a.part_ml[slot], *reinterpret_cast<const float4*>(a.part_o + slot * D + d));
-  }
-  s_o[group][threadIdx.x % LANES] = o;
-  if (threadIdx.x % LANES == 0) s_ml[group] = make_float2(m, all);
-  __syncthreads();
-  if (group != 0) return;
-#pragma unroll
-  for (int i = 1; i < GROUPS; ++i) take(s_ml[i], s_o[i][threadIdx.x]);
-  finish4(a, span.r0 + pair / a.group, g * a.group + pair % a.group, D, d, o, m == -INFINITY ? 0.f : m, all);
-}
 
-// w_j: a thread for each four positions of a sequence and KV head, its pairs in order.
-__global__ void __launch_bounds__(128) kv8_weights_kernel(const __grid_constant__ AttnArgs a) {
-  const Kv8View& v = a.v;
-  const int g = blockIdx.y, b = blockIdx.z;
-  const int len = kv8_len(v, b);
-  const Kv8Span span = kv8_rows(v, b);
-  kv8_ready();
-  grid_launch_dependents();
-  const long long j = ((long long)blockIdx.x * 128 + threadIdx.x) * 4;
-  if (j >= a.weights_ld || (a.accumulate && j >= len)) return;
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
-  if (j < len) {
-    for (int i = 0; i < span.n; ++i) {
-      const size_t at = (size_t)(span.r0 + i) * a.heads + g * a.group;
+  if ((int)blockIdx.x < combine_ctas) {
+    const int g = (int)(blockIdx.x % v.kv_heads), pair = (int)(blockIdx.x / v.kv_heads);
+    if (pair >= pairs) return;
+    const Pieces pieces = pieces_of<D>(a, total, seq_u0, su, g, pair);
+    if (pieces.n == 1) return;
+    const int group = threadIdx.x / LANES, d = 4 * (threadIdx.x % LANES);
+    float m = -INFINITY, all = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto take = [&](float2 ml, const float4& x) {  // the reference follows the largest so far
+      const float now = ml.y > 0.f ? fmaxf(m, ml.x) : m;
+      const float keep = m == now ? 1.f : exp2f(m - now), f = piece_factor(ml, now);
+      m = now;
+      all = fmaf(f, ml.y, all * keep);
+      o = make_float4(fmaf(f, x.x, o.x * keep), fmaf(f, x.y, o.y * keep), fmaf(f, x.z, o.z * keep),
+                      fmaf(f, x.w, o.w * keep));
+    };
 #pragma unroll 8
-      for (int h = 0; h < a.group; ++h) {
-        const float2 ml = a.final_ml[at + h];
-        const float4 s = __ldcg(reinterpret_cast<const float4*>(a.scores + (at + h) * a.scores_ld + j));
-        sum[0] = fmaf(exp2_fast(s.x - ml.x), ml.y, sum[0]);
-        sum[1] = fmaf(exp2_fast(s.y - ml.x), ml.y, sum[1]);
-        sum[2] = fmaf(exp2_fast(s.z - ml.x), ml.y, sum[2]);
-        sum[3] = fmaf(exp2_fast(s.w - ml.x), ml.y, sum[3]);
+    for (int i = group; i < pieces.n; i += GROUPS) {
+      const size_t slot = pieces.slot(a, i, pair);
+      take(a.part_ml[slot], *reinterpret_cast<const float4*>(a.part_o + slot * D + d));
+    }
+    s_o[group][threadIdx.x % LANES] = o;
+    if (threadIdx.x % LANES == 0) s_ml[group] = make_float2(m, all);
+    __syncthreads();
+    if (group != 0) return;
+#pragma unroll
+    for (int i = 1; i < GROUPS; ++i) take(s_ml[i], s_o[i][threadIdx.x]);
+    finish4(a, span.r0, span.n, g, pair, D, d, o, m == -INFINITY ? 0.f : m, all);
+    return;
+  }
+
+  // ---- w_j
+  const int g = (int)((blockIdx.x - combine_ctas) % v.kv_heads);
+  const long long j0 = (long long)((blockIdx.x - combine_ctas) / v.kv_heads) * (4 * THREADS);
+  if (a.accumulate && j0 >= len) return;
+  const long long j = j0 + 4 * (int)threadIdx.x;
+  const int lane = threadIdx.x & 7;  // of the 8 that look at a pair's pieces
+  const size_t at = pair_at(a, span.r0, span.n, g);
+  const float* scores = a.scores + at * a.scores_ld + j;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  if (j0 < len) {
+    for (int p0 = 0; p0 < pairs; p0 += W_PAIRS) {
+      const int np = min(W_PAIRS, pairs - p0);
+      __syncthreads();
+      for (int p = threadIdx.x / 8; p < (np + 3) / 4 * 4; p += THREADS / 8) {  // (whole warps)
+        const Pieces pieces = pieces_of<D>(a, total, seq_u0, su, g, p0 + min(p, np - 1));
+        float m = -INFINITY, all = 0.f;
+        if (pieces.n > 1) {
+#pragma unroll 4
+          for (int i = lane; i < pieces.n; i += 8) {
+            const float2 ml = a.part_ml[pieces.slot(a, i, p0 + min(p, np - 1))];
+            const float now = ml.y > 0.f ? fmaxf(m, ml.x) : m;
+            all = fmaf(piece_factor(ml, now), ml.y, all * (m == now ? 1.f : exp2f(m - now)));
+            m = now;
+          }
+        }
+        float top = m;
+#pragma unroll
+        for (int x = 4; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        all = m == -INFINITY ? all : all * exp2f(m - top);  // (a lane without pieces: 0, or NaN)
+#pragma unroll
+        for (int x = 4; x > 0; x >>= 1) all += __shfl_xor_sync(0xffffffffu, all, x);
+        if (lane == 0 && p < np)
+          s_ml[p] = pieces.n == 1 ? a.final_ml[at + p0 + p]
+                                  : make_float2(top == -INFINITY ? 0.f : top, all > 0.f || all != all ? 1.f / all : 0.f);
+      }
+      __syncthreads();
+      if (j < len) {
+#pragma unroll 8
+        for (int p = 0; p < np; ++p) {
+          const float2 ml = s_ml[p];
+          const float4 s = __ldcs(reinterpret_cast<const float4*>(scores + (size_t)(p0 + p) * a.scores_ld));
+          sum[0] = fmaf(exp2_fast(s.x - ml.x), ml.y, sum[0]);
+          sum[1] = fmaf(exp2_fast(s.y - ml.x), ml.y, sum[1]);
+          sum[2] = fmaf(exp2_fast(s.z - ml.x), ml.y, sum[2]);
+          sum[3] = fmaf(exp2_fast(s.w - ml.x), ml.y, sum[3]);
+        }
       }
     }
   }
@@ -716,21 +794,13 @@ struct Layout {
   size_t prefix, part_ml, part_o, final_ml, scores, bytes;
 };
 
-// M tiles of 8 pairs that share a key tile's loads: as many as the longest
-// row group of a sequence fills, at most 4.
-int m_tiles(const Kv8View& v, const Kv8Attention& a) {
-  const long long pairs = (long long)v.max_rows * (a.heads / v.kv_heads);
-  return pairs <= 8 ? 1 : (pairs <= 16 ? 2 : 4);
-}
-
-int resident_ctas(int dim, int mt) { return ctas_per_sm(dim, mt) * num_sms(); }
-
 int scores_ld(const Kv8View& v) { return (int)(((long long)v.max_len + TILE - 1) / TILE * TILE); }
 
 Layout layout_of(const Kv8View& v, const Kv8Attention& a) {
   Layout l;
-  l.mt = m_tiles(v, a);
-  const int group = a.heads / v.kv_heads, pairs = 8 * l.mt, most_ctas = resident_ctas(v.dim, l.mt);
+  const int group = a.heads / v.kv_heads;
+  l.mt = m_tiles(v.dim, (long long)v.max_rows * group);
+  const int pairs = 8 * l.mt, most_ctas = ctas_per_sm(v.dim, l.mt) * num_sms();  // those that run at once
   const long long segs = ((long long)v.num_rows * group / pairs + v.num_seqs) * v.kv_heads;  // at most
   const long long most = segs * (v.max_len / UNIT + 1 + overhead_units(v.dim));
   l.ctas = (int)(most < most_ctas ? most : most_ctas);
@@ -749,6 +819,17 @@ Layout layout_of(const Kv8View& v, const Kv8Attention& a) {
   return l;
 }
 
+template <int D, int GROUPS>
+cudaError_t launch_finish(const AttnArgs& a, cudaLaunchConfig_t cfg) {
+  constexpr int N = D / 4 * GROUPS;
+  const long long combine = (long long)a.v.max_rows * a.heads;
+  const long long span = a.weights ? (a.accumulate ? a.v.max_len : a.weights_ld) : 0;
+  cfg.gridDim = dim3((unsigned)(combine + (span + 4 * N - 1) / (4 * N) * a.v.kv_heads), (unsigned)a.v.num_seqs);
+  cfg.blockDim = dim3(N);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, kv8_finish_kernel<D, GROUPS>, a, (int)combine);
+}
+
 template <int D, int MT>
 cudaError_t launch_shape(const AttnArgs& a, cudaStream_t s) {
   using S = Shape<D, MT>;
@@ -763,7 +844,7 @@ cudaError_t launch_shape(const AttnArgs& a, cudaStream_t s) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.ctas);
-  cfg.blockDim = dim3(S::THREADS);
+  cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = S::BYTES;
   cfg.stream = s;
   cudaLaunchAttribute attr[1] = {pdl_attr()};
@@ -771,27 +852,8 @@ cudaError_t launch_shape(const AttnArgs& a, cudaStream_t s) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kv8_attention_kernel<D, MT>, a);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)((long long)a.v.max_rows * a.heads), (unsigned)a.v.num_seqs);
-  cfg.dynamicSmemBytes = 0;
   // few (row, head) pairs have many pieces each; of many pairs most are whole or in two pieces
-  if ((long long)a.v.num_rows * a.heads <= 4 * num_sms()) {
-    cfg.blockDim = dim3(D / 4 * 8);
-    e = cudaLaunchKernelEx(&cfg, kv8_combine_kernel<D, 8>, a);
-  } else {
-    cfg.blockDim = dim3(D / 4 * 2);
-    e = cudaLaunchKernelEx(&cfg, kv8_combine_kernel<D, 2>, a);
-  }
-  if (e != cudaSuccess || !a.weights) return e;
-  const long long span = a.accumulate ? a.v.max_len : a.weights_ld;
-  if (span == 0) return cudaSuccess;
-  cfg.blockDim = dim3(128);
-  cfg.gridDim = dim3((unsigned)((span + 511) / 512), (unsigned)a.v.kv_heads, (unsigned)a.v.num_seqs);
-  return cudaLaunchKernelEx(&cfg, kv8_weights_kernel, a);
-}
-
-template <int D>
-cudaError_t launch_dim(const AttnArgs& a, int mt, cudaStream_t s) {
-  return mt == 1 ? launch_shape<D, 1>(a, s) : (mt == 2 ? launch_shape<D, 2>(a, s) : launch_shape<D, 4>(a, s));
+  return (long long)a.v.num_rows * a.heads <= 4 * num_sms() ? launch_finish<D, 8>(a, cfg) : launch_finish<D, 2>(a, cfg);
 }
 
 }  // namespace
@@ -824,9 +886,9 @@ cudaError_t launch_kv8_attention(const Kv8View& v, const Kv8Attention& in, void*
     a.weights_ld = in.weights_ld;
     a.accumulate = in.accumulate;
   }
-  if (v.dim == 64) return launch_dim<64>(a, l.mt, s);
-  if (v.dim == 128) return launch_dim<128>(a, l.mt, s);
-  return launch_dim<256>(a, l.mt, s);
+  if (v.dim == 256) return launch_shape<256, 1>(a, s);
+  if (v.dim == 128) return l.mt == 1 ? launch_shape<128, 1>(a, s) : launch_shape<128, 2>(a, s);
+  return l.mt == 1 ? launch_shape<64, 1>(a, s) : launch_shape<64, 2>(a, s);
 }
 
 }  // namespace apr

@@ -4,7 +4,7 @@
 // Selection. One cluster of 1 to 8 CTAs per (sequence, KV head), each CTA a
 // contiguous share of the positions, whose weights it reads once: mapped to
 // unsigned keys that order as the numbers do they stay in shared memory (a
-// share of more than 16384 is read again for each pass, from L2). The key of
+// share of more than 40960 is read again for each pass, from L2). The key of
 // the last one kept is found by up to three rounds of histograms over 11, 11
 // and 10 bits of it, each round's counts added up over the cluster through
 // distributed shared memory; a round whose border falls between two bins ends
@@ -31,13 +31,17 @@ constexpr int S_MOST = 8;        // CTAs of a cluster, the portable size
 constexpr int S_THREADS = 1024;
 constexpr int S_WARPS = S_THREADS / 32;
 constexpr int S_BINS = 2048;
-constexpr int S_KEYS = 16384;    // keys that a CTA holds
+constexpr int S_KEYS = 40960;    // keys that a CTA holds
 
 // Unsigned keys in the numbers' order: NaN above all, -0 as 0.
 __device__ __forceinline__ uint32_t order_key(float x) {
   if (x != x) return 0xffffffffu;
   const uint32_t u = __float_as_uint(x + 0.0f);
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ float order_value(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
 }
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(const void* p, int rank) {
@@ -136,7 +140,7 @@ __global__ void __launch_bounds__(S_THREADS) kv8_select_kernel(const __grid_cons
   w += lo;
   const bool held = share <= S_KEYS;
   if (held) {
-#pragma unroll 4
+#pragma unroll 8
     for (int j = threadIdx.x; j < n; j += S_THREADS) s_keys[j] = order_key(w[j]);
   }
   auto key_at = [&](int j) { return held ? s_keys[j] : order_key(w[j]); };
@@ -241,7 +245,7 @@ __global__ void __launch_bounds__(S_THREADS) kv8_select_kernel(const __grid_cons
       if (key[i] > border || (same && eq < take)) {
         const uint32_t o = gt + min(eq, take);
         kept[o] = lo + j + i;
-        wo[o] = w[j + i];
+        wo[o] = order_value(key[i]);
       }
       gt += key[i] > border;
       eq += same;
@@ -277,8 +281,8 @@ __global__ void __launch_bounds__(M_THREADS) kv8_move_kernel(const __grid_consta
   __shared__ long long row_at[M_PAGE];  // offset of a row's codes; -1: none
   __shared__ float row_scale[M_PAGE];
   __shared__ float s_max[M_THREADS / 32];
-  const int b = blockIdx.z, g = (int)(blockIdx.x % v.kv_heads), index = (int)(blockIdx.x / v.kv_heads);
-  const bool is_v = blockIdx.y != 0;
+  const bool is_v = blockIdx.x & 1;  // K and V of a page are neighbours: they look up the same rows
+  const int b = blockIdx.y, g = (int)((blockIdx.x >> 1) % v.kv_heads), index = (int)((blockIdx.x >> 1) / v.kv_heads);
   const int len = kv8_len(v, b);
   const int to = len > a.budget ? a.fresh[(size_t)b * a.fresh_w + index] : -1;
   if (len > a.budget && (to < 0 || to >= v.num_pages) && threadIdx.x == 0) kv8_flag(v);
@@ -343,7 +347,9 @@ cudaError_t launch_kv8_evict(const Kv8View& v, const float* weights, long long w
   const EvictArgs a{weights,   weights_ld, budget,      recent,         fresh_w, fresh,
                     table_out, lens_out,   weights_out, weights_out_ld, kept};
   // As few CTAs of a cluster as hold the keys of the longest sequence: a barrier
-  // of the cluster costs more than a pass over some thousand keys.
+  // of the cluster costs more than a pass over more keys (10 sequences of up to
+  // 33000, 8 heads: 110 us for the whole eviction and read-back with one CTA each,
+  // 116 with two or four).
   int ranks = 1;
   while (ranks < S_MOST && (v.max_len + ranks - 1) / ranks > S_KEYS) ranks *= 2;
   const int share = (v.max_len + ranks - 1) / ranks;
@@ -370,7 +376,7 @@ cudaError_t launch_kv8_evict(const Kv8View& v, const float* weights, long long w
   if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kv8_select_kernel, v, a);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t mcfg = {};
-  mcfg.gridDim = dim3((unsigned)fresh_w * v.kv_heads, 2, (unsigned)v.num_seqs);
+  mcfg.gridDim = dim3(2u * fresh_w * v.kv_heads, (unsigned)v.num_seqs);
   mcfg.blockDim = dim3(M_THREADS);
   mcfg.stream = s;
   mcfg.attrs = attr;

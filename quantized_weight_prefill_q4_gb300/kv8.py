@@ -20,6 +20,8 @@ APR_T_BF16 = 30
 # Every symbol include/apr_kv8.h declares.
 KV8_EXPORTS = ("apr_kv8_append", "apr_kv8_read", "apr_kv8_attention", "apr_kv8_evict")
 
+_I8, _I32, _F32, _Tensor = torch.int8, torch.int32, torch.float32, torch.Tensor
+_raw_stream = torch._C._cuda_getCurrentRawStream
 _TYPES = {torch.float32: APR_T_F32, torch.float16: APR_T_F16, torch.bfloat16: APR_T_BF16}
 
 
@@ -71,7 +73,7 @@ _lib = _bind()
 
 def _array(x, name, dtype, dims):
     """A contiguous CUDA tensor of the type and number of dimensions, checked."""
-    if isinstance(x, torch.Tensor) and x.is_cuda and x.dtype is dtype and x.dim() == dims and x.is_contiguous():
+    if isinstance(x, _Tensor) and x.is_cuda and x.dtype is dtype and x.ndim == dims and x.is_contiguous():
         return x
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name}: expected a CUDA tensor, got {type(x).__name__}")
@@ -84,9 +86,7 @@ def _array(x, name, dtype, dims):
 
 def _stream(stream, device_index):
     """The raw stream: the given one, or torch's current one."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device_index)
-    return capi._stream(stream)
+    return _raw_stream(device_index) if stream is None else capi._stream(stream)
 
 
 class Kv8Cache:
@@ -96,10 +96,10 @@ class Kv8Cache:
     __slots__ = ("K", "V", "k_scale", "v_scale", "kv_heads", "page_tokens", "head_dim", "device_index", "_c")
 
     def __init__(self, K, V, k_scale, v_scale):
-        shape = _array(K, "K", torch.int8, 4).shape
-        if (_array(V, "V", torch.int8, 4).shape != shape
-                or _array(k_scale, "k_scale", torch.float32, 2).shape != shape[:2]
-                or _array(v_scale, "v_scale", torch.float32, 2).shape != shape[:2]):
+        shape = _array(K, "K", _I8, 4).shape
+        scales = shape[:2]
+        if (_array(V, "V", _I8, 4).shape != shape or _array(k_scale, "k_scale", _F32, 2).shape != scales
+                or _array(v_scale, "v_scale", _F32, 2).shape != scales):
             raise ValueError("Kv8Cache: V, k_scale and v_scale must match K's pages, heads, tokens and head_dim")
         self.K, self.V, self.k_scale, self.v_scale = K, V, k_scale, v_scale
         pages, self.kv_heads, self.page_tokens, self.head_dim = shape
@@ -120,30 +120,32 @@ class Kv8Cache:
 
 
 def _rows(page_table, lens, row_start, num_rows, max_rows, max_len):
-    table = _array(page_table, "page_table", torch.int32, 2)
-    n = _array(lens, "lens", torch.int32, 1).numel()
-    if table.shape[0] != n:
-        raise ValueError(f"page_table has {table.shape[0]} rows, lens {n} entries")
+    seqs, width = _array(page_table, "page_table", _I32, 2).shape
+    if _array(lens, "lens", _I32, 1).numel() != seqs:
+        raise ValueError(f"page_table has {seqs} rows, lens {lens.numel()} entries")
     start = None
     if row_start is not None:
-        if _array(row_start, "row_start", torch.int32, 1).numel() != n + 1:
-            raise ValueError(f"row_start: expected {n + 1} entries, got {row_start.numel()}")
+        if _array(row_start, "row_start", _I32, 1).numel() != seqs + 1:
+            raise ValueError(f"row_start: expected {seqs + 1} entries, got {row_start.numel()}")
         start = row_start.data_ptr()
-    return _Rows(table.data_ptr(), table.shape[1], lens.data_ptr(), start, n, num_rows, max_rows, max_len)
+    return _Rows(page_table.data_ptr(), width, lens.data_ptr(), start, seqs, num_rows, max_rows, max_len)
 
 
 def _matrix(x, name, width, like=None):
     """(pointer, rows, elements from row to row) of rows of `width` elements: a
     2-D tensor, or a 3-D one of [rows][heads][head_dim], whose rows are dense."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype not in _TYPES:
+    if not (isinstance(x, _Tensor) and x.is_cuda and x.dtype in _TYPES):
         raise ValueError(f"{name}: expected a float32, float16 or bfloat16 CUDA tensor")
     shape, stride = x.shape, x.stride()
-    rows = shape[0] if shape else 0
-    dense = (len(shape) == 2 and shape[1] == width and stride[1] == 1) or (
-        len(shape) == 3 and shape[1] * shape[2] == width and stride[2] == 1 and (shape[1] == 1 or stride[1] == shape[2]))
+    if len(shape) == 2:
+        dense = shape[1] == width and stride[1] == 1
+    else:
+        dense = (len(shape) == 3 and shape[1] * shape[2] == width and stride[2] == 1
+                 and (shape[1] == 1 or stride[1] == shape[2]))
     if not dense:
         raise ValueError(f"{name}: expected rows of {width} consecutive elements, got shape {tuple(shape)}, "
                          f"strides {tuple(stride)}")
+    rows = shape[0]
     if like is not None and (x.dtype is not like.dtype or rows != like.shape[0]):
         raise ValueError(f"{name}: expected {like.shape[0]} rows of {like.dtype}, got {rows} of {x.dtype}")
     return x.data_ptr(), rows, stride[0] if rows > 1 else width
@@ -187,10 +189,10 @@ def apr_kv8_attention(cache, page_table, lens, q, out, num_heads, *, row_start=N
     rows = _rows(page_table, lens, row_start, n, max_rows, max_len)
     wp, wld = None, 0
     if weights is not None:
-        _array(weights, "weights", torch.float32, 3)
-        if weights.shape[0] != lens.numel() or weights.shape[1] != cache.kv_heads:
-            raise ValueError(f"weights: expected [{lens.numel()}][{cache.kv_heads}][...], got {tuple(weights.shape)}")
-        wp, wld = weights.data_ptr(), weights.shape[2]
+        seqs, heads, wld = _array(weights, "weights", _F32, 3).shape
+        if seqs != rows.num_seqs or heads != cache.kv_heads:
+            raise ValueError(f"weights: expected [{rows.num_seqs}][{cache.kv_heads}][...], got {tuple(weights.shape)}")
+        wp = weights.data_ptr()
     return capi._check(_lib.apr_kv8_attention(cache._c, rows, _TYPES[q.dtype], qp, ldq, op, ldo, num_heads, scale, wp,
                                               wld, int(accumulate), _stream(stream, cache.device_index)))
 
@@ -202,22 +204,25 @@ def apr_kv8_evict(cache, page_table, lens, weights, budget, recent, fresh_pages,
     ([sequences][ceil(budget / page_tokens)]); table_out, lens_out, weights_out
     ([sequences][kv_heads][>= budget]) and kept ([sequences][kv_heads][budget])
     say what the sequences are afterwards."""
-    heads, tokens = cache.kv_heads, cache.page_tokens
     rows = _rows(page_table, lens, None, 0, 0, max_len)
-    n = lens.numel()
-    want = {
-        "weights": (weights, torch.float32, (n, heads, None)),
-        "fresh_pages": (fresh_pages, torch.int32, (n, -(-budget // tokens))),
-        "table_out": (table_out, torch.int32, tuple(page_table.shape)),
-        "lens_out": (lens_out, torch.int32, (n,)),
-        "weights_out": (weights_out, torch.float32, (n, heads, None)),
-        "kept": (kept, torch.int32, (n, heads, budget)),
-    }
-    for name, (x, dtype, shape) in want.items():
-        _array(x, name, dtype, len(shape))
-        if any(w is not None and w != h for w, h in zip(shape, x.shape)):
+    n, heads = rows.num_seqs, cache.kv_heads
+
+    def check(x, name, dtype, shape):
+        if tuple(_array(x, name, dtype, len(shape)).shape) != shape:
             raise ValueError(f"{name}: expected shape {shape}, got {tuple(x.shape)}")
-    return capi._check(_lib.apr_kv8_evict(cache._c, rows, weights.data_ptr(), weights.shape[2], budget, recent,
-                                          fresh_pages.data_ptr(), table_out.data_ptr(), lens_out.data_ptr(),
-                                          weights_out.data_ptr(), weights_out.shape[2], kept.data_ptr(),
+        return x.data_ptr()
+
+    def check_weights(x, name):
+        shape = _array(x, name, _F32, 3).shape
+        if shape[0] != n or shape[1] != heads:
+            raise ValueError(f"{name}: expected [{n}][{heads}][...], got {tuple(shape)}")
+        return x.data_ptr(), shape[2]
+
+    w, w_ld = check_weights(weights, "weights")
+    wo, wo_ld = check_weights(weights_out, "weights_out")
+    fresh = check(fresh_pages, "fresh_pages", _I32, (n, -(-budget // cache.page_tokens)))
+    to = check(table_out, "table_out", _I32, (n, rows.table_ld))
+    lo = check(lens_out, "lens_out", _I32, (n,))
+    ko = check(kept, "kept", _I32, (n, heads, budget))
+    return capi._check(_lib.apr_kv8_evict(cache._c, rows, w, w_ld, budget, recent, fresh, to, lo, wo, wo_ld, ko,
                                           _stream(stream, cache.device_index)))
