@@ -26,15 +26,6 @@ struct Kv8View {
   int table_ld, num_seqs, num_rows, max_rows, max_len;
 };
 
-// Every kernel of the cache is launched before the work ahead of it is done
-// and waits here for it. What it reads before are the index arrays alone (lens,
-// row_start, page_table, fresh_pages): no kernel of the library writes those but the
-// eviction's, which let nothing start before they have ended, and a kernel
-// that lets the next one start early does so after its own wait, so that all
-// work but its own is done by then. Every grid waits somewhere, whatever it
-// finds to do: what is launched behind it relies on that.
-__device__ __forceinline__ void kv8_ready() { grid_dependency_wait(); }
-
 __device__ __forceinline__ void kv8_flag(const Kv8View& v) { atomicOr(v.status, kStatusBadIndex); }
 
 // Tokens of sequence b, within 0 .. max_len whatever the array says.

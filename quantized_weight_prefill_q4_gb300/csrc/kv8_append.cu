@@ -26,6 +26,7 @@ namespace apr {
 namespace {
 
 constexpr int A_THREADS = 128;
+constexpr int A_CTAS = 6;  // on an SM (80 registers; 5 of 96: 36 us where 6 take 33, 8 of 64: 40)
 constexpr int A_WARPS = A_THREADS / 32;
 
 // The largest magnitude; NaN is passed over, an infinity is not (the caller
@@ -79,9 +80,11 @@ __device__ __forceinline__ int pages_touched(const Kv8View& v, int b) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(A_THREADS) kv8_append_kernel(const __grid_constant__ Kv8View v,
+__global__ void __launch_bounds__(A_THREADS, A_CTAS) kv8_append_kernel(const __grid_constant__ Kv8View v,
                                                                const T* __restrict__ k, const T* __restrict__ vv,
                                                                long long ld, int heads_a_cta) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   // the CTAs of a page, K and V and all heads, are neighbours: the rows they read are
   const int parts = 2 * ((v.kv_heads + heads_a_cta - 1) / heads_a_cta);
   const int unit = (int)(blockIdx.x / parts), part = (int)(blockIdx.x % parts);
@@ -128,8 +131,6 @@ __global__ void __launch_bounds__(A_THREADS) kv8_append_kernel(const __grid_cons
   const int first = len - span.n;  // position of row r0; rows of negative positions are skipped
   const int index = (max(first, 0) >> v.page_shift) + slot;
   const int page = span.n == 0 || len == 0 ? -1 : kv8_page(v, b, index);
-  kv8_ready();
-  grid_launch_dependents();
   if (page < 0) return;
 
   const int page0 = index << v.page_shift;
@@ -200,6 +201,8 @@ constexpr int R_THREADS = 256;
 template <typename T, int D, int R_ROWS>
 __global__ void __launch_bounds__(R_THREADS) kv8_read_kernel(const __grid_constant__ Kv8View v, T* __restrict__ k,
                                                              T* __restrict__ vv, long long ld, int heads_a_cta) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   constexpr int N = 16 / sizeof(T);             // values of a 16-byte store
   constexpr int ROW = D / N;                    // stores of a row
   constexpr int STEP = R_THREADS / ROW;         // rows between a thread's stores
@@ -244,8 +247,6 @@ __global__ void __launch_bounds__(R_THREADS) kv8_read_kernel(const __grid_consta
     s_scale[threadIdx.x] = scale;
     s_zero[threadIdx.x] = zero;
   }
-  kv8_ready();
-  grid_launch_dependents();
   __syncthreads();
   const int col = (int)threadIdx.x % ROW * N, r0 = (int)threadIdx.x / ROW;
   T* out = (is_v ? vv : k) + (long long)(row0 + r0) * ld + (size_t)g0 * D + col;

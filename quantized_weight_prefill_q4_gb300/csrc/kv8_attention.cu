@@ -252,9 +252,10 @@ template <int D, int MT>
 __global__ void __launch_bounds__(THREADS, ctas_per_sm(D, MT))
     kv8_attention_kernel(const __grid_constant__ AttnArgs a) {
   using S = Shape<D, MT>;
-  // no early launch of the next kernel: its CTAs would take the places of this
-  // grid's as they free up, and those of the next call's grid would find some
-  // SMs full (48 ragged sequences: 50 us so, 64 us with it)
+  grid_dependency_wait();
+  // (The next kernel is let in late: launched at once, its CTAs took the places of
+  // this grid's as they freed up, and those of the next call's grid found some SMs
+  // full; 48 ragged sequences 64 us, against 50 without.)
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int s_scan[WARPS];
   __shared__ int s_find[2];
@@ -287,10 +288,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(D, MT))
     total += s_scan[w];
   }
   const int ctas = sharing_ctas(a, total);
-  if ((int)blockIdx.x >= ctas) {
-    if (blockIdx.x == 0) kv8_ready();
-    return;
-  }
+  if ((int)blockIdx.x >= ctas) return;
   int u = first_unit(blockIdx.x, ctas, total);
   const int u_begin = u, u_end = first_unit(blockIdx.x + 1, ctas, total);
   if (my_u0 <= u && u < my_u0 + my_units) {
@@ -367,11 +365,9 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(D, MT))
     if (mine > 0) {
       size_t scale_at;
       at_next = tile_of(lane, &scale_at);
-      kv8_ready();
       ks_all = v.k_scale[scale_at];
       vs_all = v.v_scale[scale_at];
     }
-    kv8_ready();
 #pragma unroll
     for (int i = 0; i < QP; ++i) {
       const int p = warp + i * WARPS, pair = p0 + p;
@@ -607,6 +603,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(D, MT))
     }
     __syncwarp();  // every lane is done with the ring
 
+    if (ue == u_end) grid_launch_dependents();
     // ---- the next piece begins while the warps' sums of this one are added up, in order
     const bool whole = u <= first && ue == seg_end;
     const int done_np = np, done_g = g, done_p0 = p0;
@@ -688,6 +685,8 @@ constexpr int W_PAIRS = 64;
 
 template <int D, int GROUPS>
 __global__ void __launch_bounds__(D / 4 * GROUPS) kv8_finish_kernel(const __grid_constant__ AttnArgs a, int combine_ctas) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   constexpr int LANES = D / 4, THREADS = LANES * GROUPS;
   __shared__ float4 s_o[GROUPS][LANES];
   __shared__ float2 s_ml[GROUPS > W_PAIRS ? GROUPS : W_PAIRS];
@@ -695,8 +694,6 @@ __global__ void __launch_bounds__(D / 4 * GROUPS) kv8_finish_kernel(const __grid
   const int b = blockIdx.y, len = kv8_len(v, b), su = segment_units(a, len);
   const Kv8Span span = kv8_rows(v, b);
   const int pairs = span.n * a.group;  // of a KV head
-  kv8_ready();
-  grid_launch_dependents();
   const int total = a.prefix[v.num_seqs], seq_u0 = a.prefix[b];
 
   if ((int)blockIdx.x < combine_ctas) {

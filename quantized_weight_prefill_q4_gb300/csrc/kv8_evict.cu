@@ -96,6 +96,8 @@ struct EvictArgs {
 
 __global__ void __launch_bounds__(S_THREADS) kv8_select_kernel(const __grid_constant__ Kv8View v,
                                                                const __grid_constant__ EvictArgs a) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   extern __shared__ uint32_t s_keys[];
   __shared__ uint32_t hist[S_BINS];
   __shared__ uint32_t chosen[2];  // the round's bin, and how many of it are kept
@@ -103,8 +105,6 @@ __global__ void __launch_bounds__(S_THREADS) kv8_select_kernel(const __grid_cons
   __shared__ uint32_t sums[2][S_WARPS];
   const int ranks = gridDim.x, rank = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
   const int len = kv8_len(v, b);
-  kv8_ready();
-  grid_launch_dependents();  // of the move, which waits for this grid's end and lets nothing start before its own
   const size_t bg = (size_t)b * v.kv_heads + g;
   const float* w = a.weights + bg * a.weights_ld;
   float* wo = a.weights_out + bg * a.weights_out_ld;
@@ -139,9 +139,14 @@ __global__ void __launch_bounds__(S_THREADS) kv8_select_kernel(const __grid_cons
   const int lo = min(rank * share, old), n = min(share, old - lo);
   w += lo;
   const bool held = share <= S_KEYS;
-  if (held) {
+  for (int i = threadIdx.x; i < S_BINS; i += S_THREADS) hist[i] = 0;
+  __syncthreads();
+  // the keys, and the first round's counts
 #pragma unroll 8
-    for (int j = threadIdx.x; j < n; j += S_THREADS) s_keys[j] = order_key(w[j]);
+  for (int j = threadIdx.x; j < n; j += S_THREADS) {
+    const uint32_t key = order_key(w[j]);
+    if (held) s_keys[j] = key;
+    atomicAdd(&hist[key >> 21], 1u);
   }
   auto key_at = [&](int j) { return held ? s_keys[j] : order_key(w[j]); };
 
@@ -150,13 +155,15 @@ __global__ void __launch_bounds__(S_THREADS) kv8_select_kernel(const __grid_cons
 #pragma unroll 1
   for (int round = 0; round < 3; ++round) {
     const int bits = round == 2 ? 10 : 11, shift = round == 0 ? 21 : (round == 1 ? 10 : 0);
-    for (int i = threadIdx.x; i < S_BINS; i += S_THREADS) hist[i] = 0;
-    __syncthreads();
-    const uint32_t above = round == 0 ? 0 : 0xffffffffu << (shift + bits);  // the bits already settled
-#pragma unroll 4
-    for (int j = threadIdx.x; j < n; j += S_THREADS) {
-      const uint32_t key = key_at(j);
-      if ((key & above) == border) atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1)], 1u);
+    if (round > 0) {
+      for (int i = threadIdx.x; i < S_BINS; i += S_THREADS) hist[i] = 0;
+      __syncthreads();
+      const uint32_t above = 0xffffffffu << (shift + bits);  // the bits already settled
+#pragma unroll 8
+      for (int j = threadIdx.x; j < n; j += S_THREADS) {
+        const uint32_t key = key_at(j);
+        if ((key & above) == border) atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1)], 1u);
+      }
     }
     cluster_sync_all(ranks);
     // every CTA adds up all of them: thread t the bins 2 t and 2 t + 1 from the top
@@ -198,7 +205,7 @@ __global__ void __launch_bounds__(S_THREADS) kv8_select_kernel(const __grid_cons
     if (threadIdx.x < 2) counts[threadIdx.x] = 0;
     __syncthreads();
     uint32_t gt = 0, eq = 0;
-#pragma unroll 4
+#pragma unroll 8
     for (int j = threadIdx.x; j < n; j += S_THREADS) {
       const uint32_t key = key_at(j);
       gt += key > border;
@@ -222,14 +229,15 @@ __global__ void __launch_bounds__(S_THREADS) kv8_select_kernel(const __grid_cons
   }
   __syncthreads();
 
-  // ---- the kept positions in order, four neighbours a thread at a time; the
+  // ---- the kept positions in order, some neighbours a thread at a time; the
   // scan counts those above the border in its low half, those equal in its high
+  constexpr int RUN = 8;
   int half = 0;
-  for (int j0 = 0; j0 < n; j0 += 4 * S_THREADS, half ^= 1) {
-    const int j = j0 + 4 * (int)threadIdx.x;
-    uint32_t key[4], mine = 0;
+  for (int j0 = 0; j0 < n; j0 += RUN * S_THREADS, half ^= 1) {
+    const int j = j0 + RUN * (int)threadIdx.x;
+    uint32_t key[RUN], mine = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RUN; ++i) {
       key[i] = j + i < n ? key_at(j + i) : 0u;
       mine += j + i < n ? (key[i] > border ? 1u : (key[i] == border ? 1u << 16 : 0u)) : 0u;
     }
@@ -239,7 +247,7 @@ __global__ void __launch_bounds__(S_THREADS) kv8_select_kernel(const __grid_cons
     gt_before += total & 0xffffu;
     eq_before += total >> 16;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RUN; ++i) {
       if (j + i >= n) break;
       const bool same = key[i] == border;
       if (key[i] > border || (same && eq < take)) {
@@ -278,6 +286,8 @@ __device__ __forceinline__ float amax_of_codes(const uint4& in, float scale) {
 template <int D>
 __global__ void __launch_bounds__(M_THREADS) kv8_move_kernel(const __grid_constant__ Kv8View v,
                                                              const __grid_constant__ EvictArgs a) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   __shared__ long long row_at[M_PAGE];  // offset of a row's codes; -1: none
   __shared__ float row_scale[M_PAGE];
   __shared__ float s_max[M_THREADS / 32];
@@ -286,7 +296,6 @@ __global__ void __launch_bounds__(M_THREADS) kv8_move_kernel(const __grid_consta
   const int len = kv8_len(v, b);
   const int to = len > a.budget ? a.fresh[(size_t)b * a.fresh_w + index] : -1;
   if (len > a.budget && (to < 0 || to >= v.num_pages) && threadIdx.x == 0) kv8_flag(v);
-  kv8_ready();
   if (to < 0 || to >= v.num_pages) return;
   const int* kept = a.kept + ((size_t)b * v.kv_heads + g) * a.budget + ((size_t)index << v.page_shift);
   const int rows = min(1 << v.page_shift, a.budget - (index << v.page_shift));

@@ -93,7 +93,12 @@ class Kv8Cache:
     """The cache's arrays: codes K and V int8 [pages][kv_heads][page_tokens][head_dim],
     scales k_scale and v_scale float32 [pages][kv_heads], all contiguous."""
 
-    __slots__ = ("K", "V", "k_scale", "v_scale", "kv_heads", "page_tokens", "head_dim", "device_index", "_c")
+    __slots__ = ("_arrays", "kv_heads", "page_tokens", "head_dim", "device_index", "_c")
+    # (read-only: the C structure holds their addresses)
+    K = property(lambda self: self._arrays[0])
+    V = property(lambda self: self._arrays[1])
+    k_scale = property(lambda self: self._arrays[2])
+    v_scale = property(lambda self: self._arrays[3])
 
     def __init__(self, K, V, k_scale, v_scale):
         shape = _array(K, "K", _I8, 4).shape
@@ -101,7 +106,7 @@ class Kv8Cache:
         if (_array(V, "V", _I8, 4).shape != shape or _array(k_scale, "k_scale", _F32, 2).shape != scales
                 or _array(v_scale, "v_scale", _F32, 2).shape != scales):
             raise ValueError("Kv8Cache: V, k_scale and v_scale must match K's pages, heads, tokens and head_dim")
-        self.K, self.V, self.k_scale, self.v_scale = K, V, k_scale, v_scale
+        self._arrays = (K, V, k_scale, v_scale)
         pages, self.kv_heads, self.page_tokens, self.head_dim = shape
         self.device_index = K.get_device()
         self._c = _Cache(K.data_ptr(), V.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, self.kv_heads,
