@@ -112,6 +112,11 @@ int apr_kv8_read(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int type,
  *   q, out   [num_rows][ldq], [num_rows][ldo] rows of num_heads * head_dim
  *            elements of `type`
  *   scale    0: 1 / sqrt(head_dim); else finite and positive
+ *   rows     a few for each sequence is what this is for (a decode step, a draft
+ *            of several tokens, the last rows of a prompt that rate its
+ *            positions): each further 8 (row, head) pairs of a KV head cost about
+ *            as much again. Chunks of hundreds of rows: apr_kv8_read, then
+ *            apr_prefill_attention.
  *   weights  NULL, or [num_seqs][num_kv_heads][weights_ld] float32: the weight
  *            that each position received, w_j = sum over the sequence's rows
  *            and the query heads of group g of p_j. accumulate == 0: positions
@@ -126,8 +131,10 @@ int apr_kv8_read(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int type,
  * are within a few 1e-6 of the exact attention of the cache's values. A NaN or
  * an infinity in a query row makes that row and head NaN.
  * out must not overlap q, the cache or weights. Scratch per stream: partial
- * results of 8 to 32 (row, head) pairs for each resident CTA, and, with
- * weights, the scores (4 * num_rows * num_heads * max_len bytes).
+ * results of 8 or 16 (row, head) pairs for each resident CTA (at most 8 MB), and,
+ * with weights, the scores (4 * num_rows * num_heads * max_len bytes, max_len
+ * rounded up to 32: give max_len where the table is much wider than the
+ * sequences).
  * num_heads a multiple of num_kv_heads, at most 65536 in all.
  */
 int apr_kv8_attention(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int type, const void* q, long long ldq,

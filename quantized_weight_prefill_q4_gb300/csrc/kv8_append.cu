@@ -15,6 +15,12 @@
 // time) and one byte a value written; the rounding is five instructions and a
 // byte permute a value (kv8_codes8).
 //
+// Measured (GB300): 13000 rows of 8 heads of 128 in bf16, 9 prompts: 20 us, 80 MB
+// (0.60 of the HBM rate); 50001 of 8 heads of 64 in fp16: 40 us, 154 MB (0.57).
+// What is left is the way of each CTA to its first rows and the barrier between
+// its two passes: rows loaded ahead for the next head (128 registers, 4 CTAs)
+// gained nothing over 6 CTAs.
+//
 // Read. One CTA per 16 or 32 packed rows and some heads, K or V; a thread's
 // 16-byte stores cover neighbouring elements of a row.
 

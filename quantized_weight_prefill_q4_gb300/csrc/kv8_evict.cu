@@ -18,7 +18,14 @@
 // gathered into registers, their largest value gives the scale, and they are
 // written under it, five instructions and a byte permute a value
 // (kv8_requantise16). What a large page has more than the registers hold is
-// gathered again, from L1.
+// gathered again, from L1. Bound by instructions and the way to the rows (kept
+// position, page, scale, codes), which nine CTAs an SM cover for one another: K
+// and V in one CTA, or several pages a CTA with the next one's rows gathered
+// ahead, at 72 to 92 registers a thread, took longer.
+//
+// Measured (GB300): 10 sequences of 3500 to 33000 positions, 8 heads of 128, to
+// 4100: selection 23 us (1.3 MB a head to order; its floor is 3), move 45 us, 151
+// MB (0.50 of the HBM rate).
 
 #include "apr_internal.h"
 #include "host_common.h"
