@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(A_THREADS, A_CTAS) kv8_append_kernel(const __g
   constexpr int HELD = 16 / sizeof(T);  // vectors of 8 values a thread keeps between the passes, 32 registers
   constexpr int ROW = D / 8;            // vectors of a row
   __shared__ float s_max[3][A_WARPS];
-  __shared__ int s_scan[A_WARPS];
+  __shared__ long long s_scan[A_WARPS];
   __shared__ int s_find[2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool is_v = part & 1;
@@ -108,24 +108,24 @@ __global__ void __launch_bounds__(A_THREADS, A_CTAS) kv8_append_kernel(const __g
   if (v.row_start) {
     const int run = (v.num_seqs + A_THREADS - 1) / A_THREADS;
     const int b0 = min((int)threadIdx.x * run, v.num_seqs), b1 = min(b0 + run, v.num_seqs);
-    int mine = 0;
+    long long mine = 0;
     for (int i = b0; i < b1; ++i) mine += pages_touched(v, i);
-    int inc = mine;
+    long long inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
     if (lane == 31) s_scan[warp] = inc;
     if (threadIdx.x == 0) s_find[0] = -1;
     __syncthreads();
-    int at = inc - mine;
+    long long at = inc - mine;
     for (int w = 0; w < warp; ++w) at += s_scan[w];
     if (at <= unit && unit < at + mine) {
       int i = b0;
-      for (int n; at + (n = pages_touched(v, i)) <= unit; ++i) at += n;
+      for (int n; i + 1 < b1 && at + (n = pages_touched(v, i)) <= unit; ++i) at += n;
       s_find[0] = i;
-      s_find[1] = unit - at;
+      s_find[1] = unit - (int)at;
     }
     __syncthreads();
     b = s_find[0];
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(A_THREADS, A_CTAS) kv8_append_kernel(const __g
   const Kv8Span span = b < 0 ? Kv8Span{0, 0} : kv8_rows(v, b);
   const int first = len - span.n;  // position of row r0; rows of negative positions are skipped
   const int index = (max(first, 0) >> v.page_shift) + slot;
-  const int page = span.n == 0 || len == 0 ? -1 : kv8_page(v, b, index);
+  const int page = span.n == 0 || len == 0 || index > (len - 1) >> v.page_shift ? -1 : kv8_page(v, b, index);
   if (page < 0) return;
 
   const int page0 = index << v.page_shift;
@@ -220,6 +220,8 @@ __global__ void __launch_bounds__(R_THREADS) kv8_read_kernel(const __grid_consta
   const int row0 = (int)(blockIdx.x / parts) * R_ROWS;
   const bool is_v = part & 1;
   const int g0 = (part >> 1) * heads_a_cta, g1 = min(g0 + heads_a_cta, v.kv_heads);
+  if (blockIdx.x == 0 && v.row_start)  // every range is looked at, also one that no row is found by
+    for (int b = threadIdx.x; b < v.num_seqs; b += R_THREADS) kv8_rows(v, b);
   if (threadIdx.x < R_ROWS) {
     const int row = row0 + (int)threadIdx.x;
     int b = row;

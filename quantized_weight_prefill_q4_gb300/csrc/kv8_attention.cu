@@ -65,6 +65,7 @@ namespace apr {
 namespace {
 
 constexpr int UNIT = 64;      // positions of a unit of work
+constexpr int MOST_UNITS = 1 << 30;  // of a call, as its arguments are checked for
 constexpr int MIN_SHARE = 2;  // units of a CTA's share, where there are not enough for every CTA
 // Units that a segment counts for besides its positions: what its start (the
 // way from the length over the page table to the codes, the query rows) and
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(D, MT))
   // this grid's as they freed up, and those of the next call's grid found some SMs
   // full; 48 ragged sequences 64 us, against 50 without.)
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ int s_scan[WARPS];
+  __shared__ long long s_scan[WARPS];
   __shared__ int s_find[2];
   __shared__ float s_factor[S::PAIRS];          // score of a pair = factor * (K scale) * sum of products
   __shared__ float2 s_ml[WARPS][S::PAIRS];
@@ -271,29 +272,40 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(D, MT))
   // thread counts the units of `run` neighbouring sequences
   const int run = (v.num_seqs + THREADS - 1) / THREADS;
   const int my_b0 = min((int)threadIdx.x * run, v.num_seqs), my_b1 = min(my_b0 + run, v.num_seqs);
-  int my_units = 0;
+  long long my_units = 0;
   for (int b = my_b0; b < my_b1; ++b) my_units += sequence_units(a, b);
-  int inc = my_units;
+  long long inc = my_units;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
   }
   if (lane == 31) s_scan[warp] = inc;
   __syncthreads();
-  int my_u0 = inc - my_units, total = 0;
+  long long my_u0 = inc - my_units, all_units = 0;
 #pragma unroll
   for (int w = 0; w < WARPS; ++w) {
     if (w < warp) my_u0 += s_scan[w];
-    total += s_scan[w];
+    all_units += s_scan[w];
+  }
+  // more than the host allows for: row ranges that overlap
+  const int total = all_units <= MOST_UNITS ? (int)all_units : 0;
+  if (all_units > MOST_UNITS && threadIdx.x == 0) kv8_flag(v);
+  if (blockIdx.x == 0) {
+    int at = (int)my_u0;
+    for (int b = my_b0; b < my_b1; ++b) {
+      a.prefix[b] = at;
+      at += sequence_units(a, b);
+    }
+    if (threadIdx.x == 0) a.prefix[v.num_seqs] = total;
   }
   const int ctas = sharing_ctas(a, total);
   if ((int)blockIdx.x >= ctas) return;
   int u = first_unit(blockIdx.x, ctas, total);
   const int u_begin = u, u_end = first_unit(blockIdx.x + 1, ctas, total);
   if (my_u0 <= u && u < my_u0 + my_units) {
-    int b = my_b0, at = my_u0;
-    for (int n; at + (n = sequence_units(a, b)) <= u; ++b) at += n;
+    int b = my_b0, at = (int)my_u0;
+    for (int n; b + 1 < my_b1 && at + (n = sequence_units(a, b)) <= u; ++b) at += n;
     s_find[0] = b;
     s_find[1] = at;
   }
@@ -338,7 +350,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(D, MT))
   // the next piece of this CTA's share, if there is one: its first tiles and its query rows under way
   auto begin = [&]() -> bool {
     for (;;) {
-      if (u >= u_end) return false;
+      if (u >= u_end || b >= v.num_seqs) return false;
       len = kv8_len(v, b);
       span = kv8_rows(v, b);
       const int su = segment_units(a, len), nseg = span.n ? segment_count(a, span.n) : 0;
@@ -384,14 +396,6 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(D, MT))
   };
 
   bool more = begin();
-  if (blockIdx.x == 0) {
-    int at = my_u0;
-    for (int b = my_b0; b < my_b1; ++b) {
-      a.prefix[b] = at;
-      at += sequence_units(a, b);
-    }
-    if (threadIdx.x == 0) a.prefix[v.num_seqs] = total;
-  }
   while (more) {
     // ---- the rows as fragments: row r of an M tile its fp16 hi, row r + 8 its lo
 #pragma unroll
@@ -672,7 +676,8 @@ template <int D>
 __device__ __forceinline__ Pieces pieces_of(const AttnArgs& a, int total, int seq_u0, int su, int g, int pair) {
   const int u0 = seq_u0 + (pair / a.pairs * a.v.kv_heads + g) * su, ctas = sharing_ctas(a, total);
   const int c0 = cta_of(u0 + overhead_units(D), ctas, total);
-  return Pieces{c0, cta_of(u0 + su - 1, ctas, total) - c0 + 1};
+  const int n = cta_of(u0 + su - 1, ctas, total) - c0 + 1;
+  return c0 >= 0 && n > 0 && c0 + n <= a.ctas ? Pieces{c0, n} : Pieces{0, 1};  // (lengths that changed meanwhile)
 }
 
 // The combination's CTAs, blockIdx.x < combine_ctas: one for each (row, head)
@@ -693,8 +698,8 @@ __global__ void __launch_bounds__(D / 4 * GROUPS) kv8_finish_kernel(const __grid
   const Kv8View& v = a.v;
   const int b = blockIdx.y, len = kv8_len(v, b), su = segment_units(a, len);
   const Kv8Span span = kv8_rows(v, b);
-  const int pairs = span.n * a.group;  // of a KV head
   const int total = a.prefix[v.num_seqs], seq_u0 = a.prefix[b];
+  const int pairs = total > 0 ? span.n * a.group : 0;  // of a KV head
 
   if ((int)blockIdx.x < combine_ctas) {
     const int g = (int)(blockIdx.x % v.kv_heads), pair = (int)(blockIdx.x / v.kv_heads);

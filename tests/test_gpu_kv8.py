@@ -500,7 +500,7 @@ def bad_index(q):
     q.apr_stream_status()  # cleared
 
 
-@pytest.mark.parametrize("what", ["page", "negative page", "length", "row_start", "row_start past", "max_rows"])
+@pytest.mark.parametrize("what", ["page", "negative page", "length", "row_start", "row_start past", "row_start falls", "max_rows"])
 def test_bad_device_arrays_are_reported_and_touch_nothing(q, what):
     c = Case([100, 70], 1, 64, 32, seed=40, extra_width=0).on_gpu(q)
     rows, more = [3, 2], {}
@@ -515,6 +515,8 @@ def test_bad_device_arrays_are_reported_and_touch_nothing(q, what):
         start[1] = -2
     elif what == "row_start past":
         start[2] = 6
+    elif what == "row_start falls":
+        start[0], start[1] = 5, 0  # the first range ends before it begins, the second is the whole call
     else:
         more = {"max_rows": 2}
     k = torch.ones((5, 64), device="cuda")
