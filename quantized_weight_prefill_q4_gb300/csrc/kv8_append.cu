@@ -15,11 +15,11 @@
 // time) and one byte a value written; the rounding is five instructions and a
 // byte permute a value (kv8_codes8).
 //
-// Measured (GB300): 13000 rows of 8 heads of 128 in bf16, 9 prompts: 20 us, 80 MB
-// (0.60 of the HBM rate); 50001 of 8 heads of 64 in fp16: 40 us, 154 MB (0.57).
-// What is left is the way of each CTA to its first rows and the barrier between
-// its two passes: rows loaded ahead for the next head (128 registers, 4 CTAs)
-// gained nothing over 6 CTAs.
+// Measured (GB300): 13000 rows of 8 heads of 128 in bf16, 9 prompts: 24.6 us, 80 MB
+// (0.49 of the HBM rate); 50001 of 8 heads of 64 in fp16: 35.8 us, 154 MB (0.64).
+// What is left is the way of each CTA to its first rows (loaded while the page
+// table is looked at) and the barrier between its two passes: rows loaded ahead
+// for the next head (128 registers, 4 CTAs) gained nothing over more CTAs.
 //
 // Read. One CTA per 16 or 32 packed rows and some heads, K or V; a thread's
 // 16-byte stores cover neighbouring elements of a row.
@@ -32,7 +32,7 @@ namespace apr {
 namespace {
 
 constexpr int A_THREADS = 128;
-constexpr int A_CTAS = 6;  // on an SM (80 registers; 5 of 96: 36 us where 6 take 33, 8 of 64: 40)
+constexpr int A_CTAS = 5;  // on an SM (102 registers; the 50001 rows 36 us, 39 with 6 of 80, 41 with 7)
 constexpr int A_WARPS = A_THREADS / 32;
 
 // The largest magnitude; NaN is passed over, an infinity is not (the caller
@@ -136,8 +136,8 @@ __global__ void __launch_bounds__(A_THREADS, A_CTAS) kv8_append_kernel(const __g
   const Kv8Span span = b < 0 ? Kv8Span{0, 0} : kv8_rows(v, b);
   const int first = len - span.n;  // position of row r0; rows of negative positions are skipped
   const int index = (max(first, 0) >> v.page_shift) + slot;
-  const int page = span.n == 0 || len == 0 || index > (len - 1) >> v.page_shift ? -1 : kv8_page(v, b, index);
-  if (page < 0) return;
+  if (span.n == 0 || len == 0 || index > (len - 1) >> v.page_shift) return;
+  const int page = v.table[(size_t)b * v.table_ld + index];  // (looked at when the first rows are on their way)
 
   const int page0 = index << v.page_shift;
   const int lo = max(max(first, 0), page0), hi = min(len, page0 + (1 << v.page_shift));
@@ -147,14 +147,21 @@ __global__ void __launch_bounds__(A_THREADS, A_CTAS) kv8_append_kernel(const __g
   const long long step = ld * (A_THREADS / ROW);
   const T* src = (is_v ? vv : k) + (long long)(span.r0 + lo - first + (int)threadIdx.x / ROW) * ld +
                  (int)threadIdx.x % ROW * 8;
-  int8_t* codes = (is_v ? v.V : v.K) + kv8_codes_at(v, page, g0);
-  float* scale = (is_v ? v.v_scale : v.k_scale) + kv8_scale_at(v, page, g0);
   src += (size_t)g0 * D;
-  for (int g = g0; g < g1; ++g, src += D, codes += (size_t)D << v.page_shift, ++scale) {
-    Vec8<T> keep[HELD];
+  Vec8<T> keep[HELD];
+  auto load = [&] {
 #pragma unroll
     for (int j = 0; j < HELD; ++j)
       if ((int)threadIdx.x + j * A_THREADS < nvec) keep[j] = load8(src + j * step);
+  };
+  load();
+  if (page < 0 || page >= v.num_pages) {
+    if (threadIdx.x == 0) kv8_flag(v);
+    return;
+  }
+  int8_t* codes = (is_v ? v.V : v.K) + kv8_codes_at(v, page, g0);
+  float* scale = (is_v ? v.v_scale : v.k_scale) + kv8_scale_at(v, page, g0);
+  for (int g = g0;; codes += (size_t)D << v.page_shift, ++scale) {
     const float s_old = held > 0 ? *scale : 0.f;
     // ---- the largest magnitude
     float m = 0.f;
@@ -197,6 +204,9 @@ __global__ void __launch_bounds__(A_THREADS, A_CTAS) kv8_append_kernel(const __g
 #pragma unroll 2
     for (int i = HELD; (int)threadIdx.x + i * A_THREADS < nvec; ++i)
       dst[i * A_THREADS] = codes_of<T>(load8(src + i * step), s);
+    if (++g == g1) break;
+    src += D;
+    load();
   }
 }
 

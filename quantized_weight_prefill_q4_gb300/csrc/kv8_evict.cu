@@ -4,15 +4,16 @@
 // Selection. One cluster of 1 to 8 CTAs per (sequence, KV head), each CTA a
 // contiguous share of the positions, whose weights it reads once: mapped to
 // unsigned keys that order as the numbers do they stay in shared memory (a
-// share of more than 40960 is read again for each pass, from L2). The key of
+// share of more than 20480 is read again for each pass, from L2). The key of
 // the last one kept is found by up to three rounds of histograms over 11, 11
 // and 10 bits of it, each round's counts added up over the cluster through
 // distributed shared memory; a round whose border falls between two bins ends
 // the search. The kept positions are then written in order: each CTA knows from
 // its peers' counts how many come before its own, and of equal keys the lowest
 // positions are taken. Every count is a whole number, so the result does not
-// depend on the order of the atomics. Bound by latency: barriers and dependent
-// passes of a few hundred cycles each.
+// depend on the order of the atomics. Bound by instructions of the few SMs that
+// it runs on (30700 keys by one: loads and first counts 7 us, rounds 4, the
+// kept positions 7) and, below some thousand keys, by latency.
 //
 // Move. One CTA per (fresh page, KV head), K or V: the kept rows' codes are
 // gathered into registers, their largest value gives the scale, and they are
@@ -38,7 +39,7 @@ constexpr int S_MOST = 8;        // CTAs of a cluster, the portable size
 constexpr int S_THREADS = 1024;
 constexpr int S_WARPS = S_THREADS / 32;
 constexpr int S_BINS = 2048;
-constexpr int S_KEYS = 40960;    // keys that a CTA holds
+constexpr int S_KEYS = 20480;    // keys that a CTA holds
 
 // Unsigned keys in the numbers' order: NaN above all, -0 as 0.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(S_THREADS) kv8_select_kernel(const __grid_cons
                                                                const __grid_constant__ EvictArgs a) {
   grid_dependency_wait();
   grid_launch_dependents();
-  extern __shared__ uint32_t s_keys[];
+  extern __shared__ __align__(16) uint32_t s_keys[];
   __shared__ uint32_t hist[S_BINS];
   __shared__ uint32_t chosen[2];  // the round's bin, and how many of it are kept
   __shared__ uint32_t counts[2];  // this CTA's keys above the border, and equal to it
@@ -148,12 +149,24 @@ __global__ void __launch_bounds__(S_THREADS) kv8_select_kernel(const __grid_cons
   const bool held = share <= S_KEYS;
   for (int i = threadIdx.x; i < S_BINS; i += S_THREADS) hist[i] = 0;
   __syncthreads();
-  // the keys, and the first round's counts
-#pragma unroll 8
-  for (int j = threadIdx.x; j < n; j += S_THREADS) {
-    const uint32_t key = order_key(w[j]);
-    if (held) s_keys[j] = key;
-    atomicAdd(&hist[key >> 21], 1u);
+  // the keys, and the first round's counts; the zeros, often the most, are
+  // counted by the warp instead of one after the other in one bin
+  constexpr uint32_t ZERO = 0x80000000u;
+  constexpr int AT_ONCE = 8;
+  for (int j0 = threadIdx.x; j0 < (n + 31) / 32 * 32; j0 += AT_ONCE * S_THREADS) {  // (whole warps)
+    float x[AT_ONCE];
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) x[i] = j0 + i * S_THREADS < n ? w[j0 + i * S_THREADS] : 1.f;
+    int zeros = 0;
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) {
+      const int j = j0 + i * S_THREADS;
+      const uint32_t key = order_key(x[i]);
+      if (held && j < n) s_keys[j] = key;
+      zeros += __popc(__ballot_sync(0xffffffffu, key == ZERO));
+      if (j < n && key != ZERO) atomicAdd(&hist[key >> 21], 1u);
+    }
+    if ((threadIdx.x & 31) == 0 && zeros) atomicAdd(&hist[ZERO >> 21], (uint32_t)zeros);
   }
   auto key_at = [&](int j) { return held ? s_keys[j] : order_key(w[j]); };
 
@@ -243,9 +256,13 @@ __global__ void __launch_bounds__(S_THREADS) kv8_select_kernel(const __grid_cons
   for (int j0 = 0; j0 < n; j0 += RUN * S_THREADS, half ^= 1) {
     const int j = j0 + RUN * (int)threadIdx.x;
     uint32_t key[RUN], mine = 0;
+    if (held && j < n) {  // (the keys' array ends on a whole run)
+#pragma unroll
+      for (int i = 0; i < RUN; i += 4) *reinterpret_cast<uint4*>(key + i) = *reinterpret_cast<const uint4*>(s_keys + j + i);
+    }
 #pragma unroll
     for (int i = 0; i < RUN; ++i) {
-      key[i] = j + i < n ? key_at(j + i) : 0u;
+      if (!held) key[i] = j + i < n ? order_key(w[j + i]) : 0u;
       mine += j + i < n ? (key[i] > border ? 1u : (key[i] == border ? 1u << 16 : 0u)) : 0u;
     }
     uint32_t total;
@@ -362,17 +379,17 @@ cudaError_t launch_kv8_evict(const Kv8View& v, const float* weights, long long w
   const int page = 1 << v.page_shift, fresh_w = (int)(((long long)budget + page - 1) / page);
   const EvictArgs a{weights,   weights_ld, budget,      recent,         fresh_w, fresh,
                     table_out, lens_out,   weights_out, weights_out_ld, kept};
-  // As few CTAs of a cluster as hold the keys of the longest sequence: a barrier
-  // of the cluster costs more than a pass over more keys (10 sequences of up to
-  // 33000, 8 heads: 110 us for the whole eviction and read-back with one CTA each,
-  // 116 with two or four).
+  // As few CTAs of a cluster as hold the keys of the longest sequence. One SM
+  // takes about 0.6 us per 1000 keys for its passes, a cluster of two or more some
+  // 6 us for its barriers (10 sequences of up to 33000, 8 heads, the eviction and
+  // read-back: 105 us with two CTAs each, 109 with one, 118 with four).
   int ranks = 1;
   while (ranks < S_MOST && (v.max_len + ranks - 1) / ranks > S_KEYS) ranks *= 2;
   const int share = (v.max_len + ranks - 1) / ranks;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ranks, (unsigned)v.kv_heads, (unsigned)v.num_seqs);
   cfg.blockDim = dim3(S_THREADS);
-  cfg.dynamicSmemBytes = (size_t)(share < S_KEYS ? share : S_KEYS) * sizeof(uint32_t);
+  cfg.dynamicSmemBytes = (size_t)(share < S_KEYS ? (share + 7) / 8 * 8 : S_KEYS) * sizeof(uint32_t);  // whole runs
   cfg.stream = s;
   cudaLaunchAttribute attr[2] = {pdl_attr()};
   attr[1].id = cudaLaunchAttributeClusterDimension;

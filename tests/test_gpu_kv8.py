@@ -417,6 +417,15 @@ def test_eviction_of_a_long_sequence(q):
     evict(q, c, w, 6001, 1)
 
 
+def test_eviction_of_more_positions_than_a_cluster_holds(q):
+    # over 8 x 20480 positions: the keys are made from the weights again in each pass
+    c = Case([170001], 1, 64, 256, seed=23, spare=36).on_gpu(q)
+    w = np.exp(2 * c.rng.normal(size=(1, 1, c.table.shape[1] * 256))).astype(np.float32)
+    w[0, 0, ::3] = 0
+    w[0, 0, 5::7] = 9.0
+    evict(q, c, w, 9000, 100)
+
+
 def test_evicted_cache_is_read_and_appended_to(q):
     # the kept positions' attention is the attention over the rows read back, and the next token joins the fresh page
     c = Case([700, 90], 2, 128, 64, seed=22, spare=8).on_gpu(q)
