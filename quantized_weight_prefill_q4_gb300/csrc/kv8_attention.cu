@@ -66,6 +66,12 @@ namespace {
 
 constexpr int UNIT = 64;      // positions of a unit of work
 constexpr int MOST_UNITS = 1 << 30;  // of a call, as its arguments are checked for
+// Where max_len * dim is at most this, segments are not divided among CTAs, which
+// saves the second launch (about 4 us of the host's time where the calls follow one
+// another): one sequence, 8 heads of 128, 200 / 512 / 700 positions 6.8 / 9.0 /
+// 11.3 us on the device, divided 8.0 / 8.4 / 8.5; 64 sequences 16.2 / 24.1 / 30.4
+// and 18.5 / 24.9 / 28.7. At 256 dims the sides meet at half the length.
+constexpr int WHOLE_SIZE = 512 * 128;
 constexpr int MIN_SHARE = 2;  // units of a CTA's share, where there are not enough for every CTA
 // Units that a segment counts for besides its positions: what its start (the
 // way from the length over the page table to the codes, the query rows) and
@@ -85,6 +91,7 @@ struct AttnArgs {
   int pairs;         // (row, head) pairs of a segment
   float scale_log2;  // softmax scale times log2(e)
   int ctas;          // of the grid; no more than there are units share them
+  int whole;         // segments are not divided (WHOLE_SIZE)
   int* prefix;       // [num_seqs + 1] first unit of each sequence, all units (written by CTA 0)
   float2* part_ml;   // [2 ctas][pairs] reference maximum and total of a piece
   float* part_o;     // [2 ctas][pairs][dim]
@@ -365,7 +372,11 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(D, MT))
       np = min(S::PAIRS, span.n * a.group - p0);
       first = seg_u0 + overhead_units(D);  // the segment's first unit of positions
       seg_end = seg_u0 + su;
-      ue = min(u_end, seg_end);
+      if (a.whole && u > seg_u0) {  // of whole segments, those that begin in the share
+        u = seg_end;
+        continue;
+      }
+      ue = a.whole ? seg_end : min(u_end, seg_end);
       if (ue > first) break;
       u = ue;  // nothing but overhead: the next CTA begins the segment
     }
@@ -607,7 +618,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(D, MT))
     }
     __syncwarp();  // every lane is done with the ring
 
-    if (ue == u_end) grid_launch_dependents();
+    if (ue >= u_end) grid_launch_dependents();
     // ---- the next piece begins while the warps' sums of this one are added up, in order
     const bool whole = u <= first && ue == seg_end;
     const int done_np = np, done_g = g, done_p0 = p0;
@@ -674,6 +685,7 @@ struct Pieces {
 };
 template <int D>
 __device__ __forceinline__ Pieces pieces_of(const AttnArgs& a, int total, int seq_u0, int su, int g, int pair) {
+  if (a.whole) return Pieces{0, 1};
   const int u0 = seq_u0 + (pair / a.pairs * a.v.kv_heads + g) * su, ctas = sharing_ctas(a, total);
   const int c0 = cta_of(u0 + overhead_units(D), ctas, total);
   const int n = cta_of(u0 + su - 1, ctas, total) - c0 + 1;
@@ -824,7 +836,7 @@ Layout layout_of(const Kv8View& v, const Kv8Attention& a) {
 template <int D, int GROUPS>
 cudaError_t launch_finish(const AttnArgs& a, cudaLaunchConfig_t cfg) {
   constexpr int N = D / 4 * GROUPS;
-  const long long combine = (long long)a.v.max_rows * a.heads;
+  const long long combine = a.whole ? 0 : (long long)a.v.max_rows * a.heads;
   const long long span = a.weights ? (a.accumulate ? a.v.max_len : a.weights_ld) : 0;
   cfg.gridDim = dim3((unsigned)(combine + (span + 4 * N - 1) / (4 * N) * a.v.kv_heads), (unsigned)a.v.num_seqs);
   cfg.blockDim = dim3(N);
@@ -853,7 +865,7 @@ cudaError_t launch_shape(const AttnArgs& a, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kv8_attention_kernel<D, MT>, a);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || (a.whole && !a.weights)) return e;
   // few (row, head) pairs have many pieces each; of many pairs most are whole or in two pieces
   return (long long)a.v.num_rows * a.heads <= 4 * num_sms() ? launch_finish<D, 8>(a, cfg) : launch_finish<D, 2>(a, cfg);
 }
@@ -877,6 +889,7 @@ cudaError_t launch_kv8_attention(const Kv8View& v, const Kv8Attention& in, void*
   a.pairs = 8 * l.mt;
   a.scale_log2 = in.scale * 1.4426950408889634f;
   a.ctas = l.ctas;
+  a.whole = (long long)v.max_len * v.dim <= WHOLE_SIZE;
   a.prefix = reinterpret_cast<int*>(base + l.prefix);
   a.part_ml = reinterpret_cast<float2*>(base + l.part_ml);
   a.part_o = reinterpret_cast<float*>(base + l.part_o);
