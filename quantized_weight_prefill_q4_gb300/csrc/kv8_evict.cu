@@ -25,7 +25,7 @@
 // ahead, at 72 to 92 registers a thread, took longer.
 //
 // Measured (GB300): 10 sequences of 3500 to 33000 positions, 8 heads of 128, to
-// 4100: selection 23 us (1.3 MB a head to order; its floor is 3), move 45 us, 151
+// 4100: selection 20 us (3.9 MB of weights: instructions, not bytes), move 45 us, 151
 // MB (0.50 of the HBM rate).
 
 #include "apr_internal.h"
