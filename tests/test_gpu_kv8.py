@@ -249,6 +249,31 @@ def test_many_sequences(q):
     assert_attention(c, out, ref)
 
 
+def test_every_operator_over_thousands_of_sequences(q):
+    # more sequences than a CTA has threads: each thread counts several, some without rows, some without positions
+    rng = np.random.default_rng(19)
+    count = 3001
+    lens = rng.integers(0, 70, count)
+    rows = np.minimum(rng.integers(0, 4, count), lens)
+    c = Case(list(lens), 1, 64, 32, seed=19, spare=2 * count).on_gpu(q)
+    n, start = int(rows.sum()), starts(rows)
+    gstart = torch.from_numpy(start).cuda()
+    k, v = (torch.from_numpy(rng.normal(size=(n, 64)).astype(np.float32)).cuda() for _ in range(2))
+    q.apr_kv8_append(c.cache, c.gtable, c.glens, k, v, row_start=gstart, max_rows=3)
+    q.apr_stream_status()
+    c.host = oracle.kv8_append(c.host, c.table, c.lens, start, as_f32(k), as_f32(v))
+    c.assert_cache(c.host)
+    kb, vb = torch.empty_like(k), torch.empty_like(v)
+    q.apr_kv8_read(c.cache, c.gtable, c.glens, kb, vb, row_start=gstart, max_rows=3)
+    wk, wv = oracle.kv8_read(c.host, c.table, c.lens, start, n)
+    np.testing.assert_array_equal(as_f32(kb), wk.reshape(n, -1))
+    np.testing.assert_array_equal(as_f32(vb), wv.reshape(n, -1))
+    out, w, ref = attend(q, c, 2, rows=list(rows), weights=True, max_rows=3)
+    assert_attention(c, out, ref)
+    assert_weights(c, w, ref)
+    evict(q, c, rng.random((count, 1, c.table.shape[1] * 32)).astype(np.float32), 40, 5)
+
+
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_a_dominant_position_and_rising_scores(q, dim):
     # scores that rise from page to page by more than any reference is kept for, one position that takes all, and
