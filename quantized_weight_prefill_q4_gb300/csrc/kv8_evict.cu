@@ -5,8 +5,8 @@
 // contiguous share of the positions, whose weights it reads once: mapped to
 // unsigned keys that order as the numbers do they stay in shared memory (a
 // share of more than 20480 is read again for each pass, from L2). The key of
-// the last one kept is found by up to three rounds of histograms over 11, 11
-// and 10 bits of it, each round's counts added up over the cluster through
+// the last one kept is found by rounds of histograms over 11, 11 and 10 bits of
+// it, in a cluster over 8 bits each time, whose counts every CTA adds up through
 // distributed shared memory; a round whose border falls between two bins ends
 // the search. The kept positions are then written in order: each CTA knows from
 // its peers' counts how many come before its own, and of equal keys the lowest
@@ -79,7 +79,7 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* sums, uint3
   }
   if (lane == 31) sums[warp] = inc;
   __syncthreads();
-  uint32_t w = sums[lane];
+  uint32_t w = lane < S_WARPS ? sums[lane] : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t y = __shfl_up_sync(0xffffffffu, w, o);
@@ -149,6 +149,11 @@ __global__ void __launch_bounds__(S_THREADS) kv8_select_kernel(const __grid_cons
   const bool held = share <= S_KEYS;
   for (int i = threadIdx.x; i < S_BINS; i += S_THREADS) hist[i] = 0;
   __syncthreads();
+  // Bits of a key that a round settles: few bins where every CTA has to read all
+  // the others', fewer rounds where it is alone (the whole call, us, 8 bits against
+  // 11: 8 heads of 131000 positions 62 and 70, of 4 sequences of 60000 61 and 62,
+  // 2 heads of 200000 46 and 52; alone, 4 heads of 4099, 15.4 and 14.3).
+  const int width = ranks == 1 ? 11 : 8, top_shift = 32 - width;
   // the keys, and the first round's counts; the zeros, often the most, are
   // counted by the warp instead of one after the other in one bin
   constexpr uint32_t ZERO = 0x80000000u;
@@ -164,19 +169,20 @@ __global__ void __launch_bounds__(S_THREADS) kv8_select_kernel(const __grid_cons
       const uint32_t key = order_key(x[i]);
       if (held && j < n) s_keys[j] = key;
       zeros += __popc(__ballot_sync(0xffffffffu, key == ZERO));
-      if (j < n && key != ZERO) atomicAdd(&hist[key >> 21], 1u);
+      if (j < n && key != ZERO) atomicAdd(&hist[key >> top_shift], 1u);
     }
-    if ((threadIdx.x & 31) == 0 && zeros) atomicAdd(&hist[ZERO >> 21], (uint32_t)zeros);
+    if ((threadIdx.x & 31) == 0 && zeros) atomicAdd(&hist[ZERO >> top_shift], (uint32_t)zeros);
   }
   auto key_at = [&](int j) { return held ? s_keys[j] : order_key(w[j]); };
 
   // ---- the key of the last position kept: border, of whose equals `take` are kept
   uint32_t border = 0, take = (uint32_t)need;
 #pragma unroll 1
-  for (int round = 0; round < 3; ++round) {
-    const int bits = round == 2 ? 10 : 11, shift = round == 0 ? 21 : (round == 1 ? 10 : 0);
+  for (int round = 0, bits, shift = 32; shift > 0; ++round) {
+    bits = min(width, shift);
+    shift -= bits;
     if (round > 0) {
-      for (int i = threadIdx.x; i < S_BINS; i += S_THREADS) hist[i] = 0;
+      for (int i = threadIdx.x; i < 1 << bits; i += S_THREADS) hist[i] = 0;
       __syncthreads();
       const uint32_t above = 0xffffffffu << (shift + bits);  // the bits already settled
 #pragma unroll 8
@@ -186,28 +192,30 @@ __global__ void __launch_bounds__(S_THREADS) kv8_select_kernel(const __grid_cons
       }
     }
     cluster_sync_all(ranks);
-    // every CTA adds up all of them: thread t the bins 2 t and 2 t + 1 from the top
-    const int bin = S_BINS - 2 - 2 * (int)threadIdx.x;
-    uint32_t hi = 0, low = 0;
-    if (ranks == 1) {
-      hi = hist[bin + 1];
-      low = hist[bin];
-    } else {
+    // every CTA adds up all of them: thread t the bins PER t .. PER t + PER - 1 from the top
+    constexpr int PER = S_BINS / S_THREADS;
+    const int top = (1 << bits) - 1 - PER * (int)threadIdx.x;
+    uint32_t c[PER], sum = 0;
 #pragma unroll
-      for (int r = 0; r < S_MOST; ++r) {
-        if (r < ranks) {
-          hi += ld_cluster_u32(&hist[bin + 1], r);
-          low += ld_cluster_u32(&hist[bin], r);
-        }
-      }
+    for (int i = 0; i < PER; ++i) c[i] = ranks == 1 && top - i >= 0 ? hist[top - i] : 0;
+    if (ranks > 1 && top > 0) {
+#pragma unroll
+      for (int r = 0; r < S_MOST; ++r)
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (r < ranks) c[i] += ld_cluster_u32(&hist[top - i], r);
     }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) sum += c[i];
     uint32_t total;
-    const uint32_t before = block_scan(hi + low, sums[round & 1], &total);
-    const bool in_hi = before < take && take <= before + hi, in_low = before + hi < take && take <= before + hi + low;
-    if (in_hi || in_low) {
-      const uint32_t at = before + (in_hi ? 0 : hi);
-      chosen[0] = ((uint32_t)(in_hi ? bin + 1 : bin) << 1) | (take - at == (in_hi ? hi : low));
-      chosen[1] = take - at;
+    uint32_t before = block_scan(sum, sums[round & 1], &total);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (before < take && take <= before + c[i]) {
+        chosen[0] = ((uint32_t)(top - i) << 1) | (take - before == c[i]);
+        chosen[1] = take - before;
+      }
+      before += c[i];
     }
     cluster_sync_all(ranks);  // chosen is written; every CTA has read the histograms
     border |= (chosen[0] >> 1) << shift;
