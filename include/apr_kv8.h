@@ -120,10 +120,10 @@ int apr_kv8_read(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int type,
  *   weights  NULL, or [num_seqs][num_kv_heads][weights_ld] float32: the weight
  *            that each position received, w_j = sum over the sequence's rows
  *            and the query heads of group g of p_j. accumulate == 0: positions
- *            past the length are set to 0; accumulate != 0: w_j is added to
- *            what the positions before this call's rows hold (the rows' own
- *            positions start at w_j; positions past the length keep what they
- *            hold). weights_ld >= max_len, or >= table_ld * page_tokens where
+ *            past the length, and all of sequences without rows, are set to 0;
+ *            accumulate != 0: w_j is added to what the positions before this
+ *            call's rows hold (the rows' own positions start at w_j; positions
+ *            past the length keep what they hold). weights_ld >= max_len, or >= table_ld * page_tokens where
  *            max_len is 0.
  * A row that sees no position gives zeros. q is split into two fp16 pieces
  * (22 bits of the row's largest magnitude), the softmax weights likewise, the

@@ -40,8 +40,9 @@ size_t span_of(long long count, long long ld, long long width) {
 }
 
 // Checks the cache and the rows, and fills the kernels' view of them. Returns
-// APR_OK, an error, or 1 where there is nothing to do.
-int view_of(const apr_kv8_cache* c, const apr_kv8_rows* r, bool with_rows, Kv8View* v) {
+// APR_OK, an error, or 1 where there is nothing to do: no sequences, or no rows
+// (unless `per_seq`: the call writes something for each sequence all the same).
+int view_of(const apr_kv8_cache* c, const apr_kv8_rows* r, bool with_rows, bool per_seq, Kv8View* v) {
   if (!c || !r) return set_error(APR_E_INVAL, "null cache or rows");
   if (c->num_pages < 1 || c->num_pages > (1 << 27) || c->num_kv_heads < 1 || c->num_kv_heads > 1024)
     return failf(APR_E_INVAL, "bad cache: num_pages=%lld num_kv_heads=%lld", c->num_pages, c->num_kv_heads);
@@ -62,7 +63,7 @@ int view_of(const apr_kv8_cache* c, const apr_kv8_rows* r, bool with_rows, Kv8Vi
     return failf(APR_E_INVAL, "max_len=%lld is not within the table's %lld tokens", r->max_len, cap);
   if (r->max_rows < 0 || (with_rows && r->max_rows > r->num_rows))
     return failf(APR_E_INVAL, "max_rows=%lld is not within num_rows=%lld", r->max_rows, r->num_rows);
-  if (r->num_seqs == 0 || (with_rows && r->num_rows == 0)) return 1;
+  if (r->num_seqs == 0 || (with_rows && !per_seq && r->num_rows == 0)) return 1;
   if (!c->K || !c->V || !c->k_scale || !c->v_scale) return set_error(APR_E_INVAL, "null pointer in the cache");
   if (!r->lens || (!r->page_table && r->table_ld > 0)) return set_error(APR_E_INVAL, "null page_table or lens");
   if (!on16(c->K) || !on16(c->V)) return set_error(APR_E_ALIGN, "the cache's codes are not 16-byte aligned");
@@ -143,7 +144,7 @@ int launched(cudaError_t e, const char* what) {
 int run_append(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int type, const void* k, const void* v,
                long long ld, cudaStream_t s) {
   Kv8View w;
-  int rc = view_of(cache, rows, true, &w);
+  int rc = view_of(cache, rows, true, false, &w);
   if (rc != APR_OK) return rc == 1 ? APR_OK : rc;
   rc = check_rows(w, type, k, v, ld);
   if (rc != APR_OK) return rc;
@@ -165,7 +166,7 @@ int run_append(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int type, c
 int run_read(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int type, void* k, void* v, long long ld,
              cudaStream_t s) {
   Kv8View w;
-  int rc = view_of(cache, rows, true, &w);
+  int rc = view_of(cache, rows, true, false, &w);
   if (rc != APR_OK) return rc == 1 ? APR_OK : rc;
   rc = check_rows(w, type, k, v, ld);
   if (rc != APR_OK) return rc;
@@ -198,7 +199,7 @@ int run_attention(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int type
                   void* out, long long ldo, int num_heads, float scale, float* weights, long long weights_ld,
                   int accumulate, cudaStream_t s) {
   Kv8View w;
-  int rc = view_of(cache, rows, true, &w);
+  int rc = view_of(cache, rows, true, weights && !accumulate, &w);
   if (rc != APR_OK) return rc == 1 ? APR_OK : rc;
   const int size = type_size(type);
   if (!size) return failf(APR_E_INVAL, "unknown element type %lld", type);
@@ -217,7 +218,7 @@ int run_attention(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int type
   if (segs * (w.max_len / 64 + 10) > (1LL << 30) || (long long)w.max_rows * num_heads > (1LL << 30) ||
       (weights_ld / 128 + 1) * w.kv_heads > (1LL << 30))
     return set_error(APR_E_INVAL, "sizes beyond the supported limits");
-  if (!q || !out) return set_error(APR_E_INVAL, "null q or out");
+  if (w.num_rows > 0 && (!q || !out)) return set_error(APR_E_INVAL, "null q or out");
   if (!on16(q) || !on16(out) || ldq * size % 16 != 0 || ldo * size % 16 != 0)
     return failf(APR_E_ALIGN, "the q and out rows (ldq=%lld, ldo=%lld) are not on 16-byte boundaries", ldq, ldo);
   if (!on4(weights)) return set_error(APR_E_ALIGN, "weights are not 4-byte aligned");
@@ -236,6 +237,7 @@ int run_attention(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int type
   if (rc != APR_OK) return rc;
   rc = device_status_word(&w.status);
   if (rc != APR_OK) return rc;
+  if (w.num_rows == 0) return launched(cudaMemsetAsync(weights, 0, wb, s), "attention");  // no row, no weight
   const Kv8Attention a{type,  q,       out,        ldq,       ldo, num_heads, scale > 0.f ? scale : 1.f / std::sqrt((float)w.dim),
                        weights, weights_ld, accumulate != 0};
   void* scratch = nullptr;
@@ -248,7 +250,7 @@ int run_evict(const apr_kv8_cache* cache, const apr_kv8_rows* rows, const float*
               int budget, int recent, const int* fresh_pages, int* table_out, int* lens_out, float* weights_out,
               long long weights_out_ld, int* kept, cudaStream_t s) {
   Kv8View w;
-  int rc = view_of(cache, rows, false, &w);
+  int rc = view_of(cache, rows, false, true, &w);
   if (rc != APR_OK) return rc == 1 ? APR_OK : rc;
   if (budget < 1 || budget > (1 << 30) || recent < 0 || recent > budget)
     return failf(APR_E_INVAL, "budget=%lld must be positive, and recent=%lld within 0 .. budget", budget, recent);

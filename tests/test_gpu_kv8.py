@@ -384,6 +384,21 @@ def test_weights_accumulate_over_steps(q):
         assert (got[b, :, n:] == 5.0).all()
 
 
+@pytest.mark.parametrize("dim", [64, 256])
+def test_weights_of_a_call_without_rows_are_zeros(q, dim):
+    # no sequence has a row: every position received nothing, as where one sequence of several has none
+    c = Case([40, 0, 700], 2, dim, 32, seed=24).on_gpu(q)
+    out, w, ref = attend(q, c, 4, rows=[0, 0, 0], weights=True)
+    assert out.shape[0] == 0 and not w.any() and not ref[1].any()
+    w.fill_(3.0)
+    attend_args = (c.cache, c.gtable, c.glens, out, out.clone(), 4)
+    none = torch.zeros(4, dtype=torch.int32, device="cuda")
+    q.apr_kv8_attention(*attend_args, row_start=none, weights=w, accumulate=True)
+    assert bool((w == 3.0).all())
+    q.apr_kv8_attention(*attend_args, row_start=none)
+    q.apr_stream_status()
+
+
 def test_repeats_are_bitwise_the_same(q):
     c = Case([5000, 40, 1300, 0, 77], 2, 128, 64, seed=17).on_gpu(q)
     qh = c.rng.normal(size=(5, 8 * 128))

@@ -269,6 +269,24 @@ def test_empty_calls_do_nothing(q):
     assert q.library().apr_kv8_append(c, None, *APPEND) == INVAL
 
 
+def test_weights_of_no_rows_are_an_output(q):
+    # zeros to be written, so arguments are checked and the device is needed; with accumulate nothing changes
+    import torch
+
+    lib, none = q.library(), dict(num_rows=0, row_start=7 * A)
+    sets = altered(ATTEND, {1: None, 3: None, 7: 10 * A, 8: 256})
+    c, r = cache_and_rows(q, **none)
+    assert lib.apr_kv8_attention(c, r, *altered(sets, {9: 1})) == 0
+    refused(q, "apr_kv8_attention", INVAL, "weights_ld", none, altered(sets, {8: 255}))
+    refused(q, "apr_kv8_attention", ALIGN, "weights", none, altered(sets, {7: 10 * A + 2}))
+    refused(q, "apr_kv8_attention", ALIAS, "weights overlaps K", none, altered(sets, {7: A + 64}))
+    refused(q, "apr_kv8_attention", INVAL, "null", dict(none, K=None), sets)
+    if not torch.cuda.is_available():
+        refused(q, "apr_kv8_attention", DEVICE, "", none, sets)
+    c, r = cache_and_rows(q, **dict(none, num_seqs=0))
+    assert lib.apr_kv8_attention(c, r, *sets) == 0
+
+
 def test_good_arguments_reach_the_device_check(q):
     import torch
 
