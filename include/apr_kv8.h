@@ -33,7 +33,10 @@
  * row_start that is not within 0 .. num_rows and non-decreasing, or more rows
  * of one sequence than max_rows touch no memory; they set a bit of the device
  * status word, and the next apr_stream_status returns APR_E_INVAL (the call's
- * outputs are then unspecified).
+ * outputs are then unspecified). A sequence whose length is out of range counts
+ * as one of no tokens, one whose rows are as one without rows: nothing of it is
+ * appended or moved, what it holds in the cache stays as it is, and weights that
+ * are added up over calls do not change.
  *
  * All pointers are device pointers, caller owned; codes, rows and outputs on
  * 16-byte boundaries, the other arrays on their element's. Calls are

@@ -28,12 +28,14 @@ struct Kv8View {
 
 __device__ __forceinline__ void kv8_flag(const Kv8View& v) { atomicOr(v.status, kStatusBadIndex); }
 
-// Tokens of sequence b, within 0 .. max_len whatever the array says.
+// Tokens of sequence b, within 0 .. max_len. Any other length counts as 0, not
+// as the nearest one: rows appended behind max_len tokens of a sequence that
+// claims more would overwrite tokens that it holds.
 __device__ __forceinline__ int kv8_len(const Kv8View& v, int b) {
   const int n = v.lens[b];
   if (n >= 0 && n <= v.max_len) return n;
   kv8_flag(v);
-  return n < 0 ? 0 : v.max_len;
+  return 0;
 }
 
 // The call's rows of sequence b: n of them from packed row r0 on, within the
