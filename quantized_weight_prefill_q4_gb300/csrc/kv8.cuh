@@ -51,6 +51,22 @@ __device__ __forceinline__ Kv8Span kv8_rows(const Kv8View& v, int b) {
   return Kv8Span{0, 0};
 }
 
+// The sequence that packed row `row` belongs to, if any: the last one that
+// begins at the row or before it. Found by the whole warp, 32 candidates at a time.
+__device__ __forceinline__ int kv8_sequence_of(const Kv8View& v, int row) {
+  if (!v.row_start) return row;
+  const int lane = threadIdx.x & 31;
+  int lo = 0;
+  for (int n = v.num_seqs; n > 1;) {  // one of lo .. lo + n - 1
+    const int step = (n + 31) / 32;
+    const bool begins = lane * step < n && v.row_start[lo + lane * step] <= row;
+    const int last = max(__popc(__ballot_sync(0xffffffffu, begins)) - 1, 0) * step;  // (within n whatever the array says)
+    lo += last;
+    n = min(step, n - last);
+  }
+  return lo;
+}
+
 // The page of sequence b's tokens `index << page_shift` on, or -1 (flagged)
 // where the table names none.
 __device__ __forceinline__ int kv8_page(const Kv8View& v, int b, int index) {

@@ -215,8 +215,7 @@ int run_attention(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int type
     return failf(APR_E_INVAL, "weights_ld=%lld must be within max_len=%lld and 2^30", weights_ld, w.max_len);
   // units of work of the kernel, counted in 32 bits (64 positions of 8 pairs of row and head)
   const long long segs = ((long long)w.num_rows * (num_heads / w.kv_heads) / 8 + w.num_seqs) * w.kv_heads;
-  if (segs * (w.max_len / 64 + 10) > (1LL << 30) || (long long)w.max_rows * num_heads > (1LL << 30) ||
-      (weights_ld / 128 + 1) * w.kv_heads > (1LL << 30))
+  if (segs * (w.max_len / 64 + 10) > (1LL << 30) || (weights_ld / 128 + 1) * w.kv_heads > (1LL << 30))
     return set_error(APR_E_INVAL, "sizes beyond the supported limits");
   if (w.num_rows > 0 && (!q || !out)) return set_error(APR_E_INVAL, "null q or out");
   if (!on16(q) || !on16(out) || ldq * size % 16 != 0 || ldo * size % 16 != 0)

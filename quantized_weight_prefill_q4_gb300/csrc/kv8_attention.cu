@@ -692,30 +692,37 @@ __device__ __forceinline__ Pieces pieces_of(const AttnArgs& a, int total, int se
   return c0 >= 0 && n > 0 && c0 + n <= a.ctas ? Pieces{c0, n} : Pieces{0, 1};  // (lengths that changed meanwhile)
 }
 
-// The combination's CTAs, blockIdx.x < combine_ctas: one for each (row, head)
-// pair, D / 4 threads take four dims each of every GROUPS-th of its pieces, so
-// that the loads are under way at once, then add up. The weights' CTAs behind
-// them: each 4 positions a thread of a KV head; 8 threads find the maximum and
-// total of a pair from its pieces' anew, 64 pairs at a time, and each thread adds
-// up its positions' weights in the pairs' order.
+// The combination's CTAs, blockIdx.x < combine_x: one for each (row, head) pair
+// of the call, numbered through over the grid's rows, whichever sequence it is of
+// (a grid of the most rows by all sequences has as many times more CTAs as the
+// batch is ragged: 256 sequences of 2 rows and 32 heads with max_rows left out,
+// 4 million for 16384 pairs). D / 4 threads take four dims each of every
+// GROUPS-th of its pieces, so that the loads are under way at once, then add up. The
+// weights' CTAs behind them, for sequence blockIdx.y: each 4 positions a thread of
+// a KV head; 8 threads find the maximum and total of a pair from its pieces' anew,
+// 64 pairs at a time, and each thread adds up its positions' weights in the pairs'
+// order.
 constexpr int W_PAIRS = 64;
 
 template <int D, int GROUPS>
-__global__ void __launch_bounds__(D / 4 * GROUPS) kv8_finish_kernel(const __grid_constant__ AttnArgs a, int combine_ctas) {
+__global__ void __launch_bounds__(D / 4 * GROUPS) kv8_finish_kernel(const __grid_constant__ AttnArgs a, int combine_x) {
   grid_dependency_wait();
   grid_launch_dependents();
   constexpr int LANES = D / 4, THREADS = LANES * GROUPS;
   __shared__ float4 s_o[GROUPS][LANES];
   __shared__ float2 s_ml[GROUPS > W_PAIRS ? GROUPS : W_PAIRS];
   const Kv8View& v = a.v;
-  const int b = blockIdx.y, len = kv8_len(v, b), su = segment_units(a, len);
+  const bool combines = (int)blockIdx.x < combine_x;
+  const int unit = (int)(blockIdx.y * combine_x + blockIdx.x), row = unit / a.heads, head = unit % a.heads;
+  if (combines && row >= v.num_rows) return;
+  const int b = combines ? kv8_sequence_of(v, row) : (int)blockIdx.y, len = kv8_len(v, b), su = segment_units(a, len);
   const Kv8Span span = kv8_rows(v, b);
   const int total = a.prefix[v.num_seqs], seq_u0 = a.prefix[b];
   const int pairs = total > 0 ? span.n * a.group : 0;  // of a KV head
 
-  if ((int)blockIdx.x < combine_ctas) {
-    const int g = (int)(blockIdx.x % v.kv_heads), pair = (int)(blockIdx.x / v.kv_heads);
-    if (pair >= pairs) return;
+  if (combines) {
+    const int g = head / a.group, pair = (row - span.r0) * a.group + head % a.group;
+    if (pair < 0 || pair >= pairs) return;
     const Pieces pieces = pieces_of<D>(a, total, seq_u0, su, g, pair);
     if (pieces.n == 1) return;
     const int group = threadIdx.x / LANES, d = 4 * (threadIdx.x % LANES);
@@ -745,8 +752,8 @@ __global__ void __launch_bounds__(D / 4 * GROUPS) kv8_finish_kernel(const __grid
   }
 
   // ---- w_j
-  const int g = (int)((blockIdx.x - combine_ctas) % v.kv_heads);
-  const long long j0 = (long long)((blockIdx.x - combine_ctas) / v.kv_heads) * (4 * THREADS);
+  const int g = (int)((blockIdx.x - combine_x) % v.kv_heads);
+  const long long j0 = (long long)((blockIdx.x - combine_x) / v.kv_heads) * (4 * THREADS);
   if (a.accumulate && j0 >= len) return;
   const long long j = j0 + 4 * (int)threadIdx.x;
   const int lane = threadIdx.x & 7;  // of the 8 that look at a pair's pieces
@@ -836,7 +843,8 @@ Layout layout_of(const Kv8View& v, const Kv8Attention& a) {
 template <int D, int GROUPS>
 cudaError_t launch_finish(const AttnArgs& a, cudaLaunchConfig_t cfg) {
   constexpr int N = D / 4 * GROUPS;
-  const long long combine = a.whole ? 0 : (long long)a.v.max_rows * a.heads;
+  const long long pairs = (long long)a.v.num_rows * a.heads;  // (below 2^30: the arguments are checked for the units they make)
+  const long long combine = a.whole ? 0 : (pairs + a.v.num_seqs - 1) / a.v.num_seqs;
   const long long span = a.weights ? (a.accumulate ? a.v.max_len : a.weights_ld) : 0;
   cfg.gridDim = dim3((unsigned)(combine + (span + 4 * N - 1) / (4 * N) * a.v.kv_heads), (unsigned)a.v.num_seqs);
   cfg.blockDim = dim3(N);

@@ -47,3 +47,63 @@ def test_a_length_past_max_len_is_not_evicted_and_receives_no_weight(q):
     bad_index(q)
     assert torch.equal(total[0], w[0]) and bool((total[1, :, :89] >= w[1, :, :89]).all())
     np.testing.assert_allclose(float(total[1, 0, :89].sum() - w[1, 0, :89].sum() + total[1, 0, 89]), 2.0, rtol=1e-4)
+
+
+# ---------------------------------------------------------------- ragged batches, max_rows left out
+def us_of(call, calls=5):
+    """The median time of a call on the GPU."""
+    call()
+    times = []
+    for _ in range(calls):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        a.record()
+        call()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b) * 1e3)
+    return sorted(times)[calls // 2]
+
+
+@pytest.mark.parametrize("dim,heads,group,max_rows", [(64, 2, 2, 0), (64, 1, 3, 40), (256, 1, 2, 0), (128, 1, 9, 0)])
+def test_ragged_rows_over_a_wide_table(q, dim, heads, group, max_rows):
+    # segments that are divided, sequences of 0 to 3 rows beside one window of 40, one sequence long enough for every CTA
+    rng = np.random.default_rng(dim + group)
+    lens = rng.integers(0, 90, 150)
+    rows = np.minimum(rng.integers(0, 4, 150), lens)
+    lens[70], rows[70], lens[149], rows[149], rows[:2], rows[100:105] = 1500, 40, 2000, 2, 0, 0
+    c = Case(list(lens), heads, dim, 64, seed=60).on_gpu(q)
+    out, w, ref = attend(q, c, heads * group, rows=list(rows), weights=True, max_rows=max_rows)
+    assert_attention(c, out, ref)
+    assert_weights(c, w, ref)
+    out, _, ref = attend(q, c, heads * group, rows=list(rows), type_="bf16", max_rows=max_rows)
+    assert_attention(c, out, ref, "bf16")
+
+
+def test_thousands_of_sequences_find_their_rows(q):
+    # three rounds of the search by 32, over ranges of rows that begin at the same place
+    rng = np.random.default_rng(61)
+    lens = rng.integers(0, 40, 2100)
+    rows = np.minimum(rng.integers(0, 3, 2100), lens)
+    lens[2050], rows[2050] = 1400, 3
+    rows[500:900] = 0
+    c = Case(list(lens), 1, 64, 32, seed=61).on_gpu(q)
+    out, _, ref = attend(q, c, 1, rows=list(rows))
+    assert_attention(c, out, ref)
+
+
+@pytest.mark.parametrize("rows,max_rows", [([2] * 1024, 0), ([400] + [1] * 600, 400)])
+def test_the_time_does_not_grow_with_the_rows_that_a_sequence_may_have(q, rows, max_rows):
+    # the same pairs as one sequence each take no more than a few times as long however they are spread over sequences: a
+    # grid of the most rows by all sequences would take some 20 ms where the work is 100 us
+    count, total = len(rows), sum(rows)
+    cache = q.Kv8Cache.allocate(20, 4, 64, 64)
+    table = torch.zeros((count, 20), dtype=torch.int32, device="cuda")
+    lens = torch.full((count,), 450, dtype=torch.int32, device="cuda")
+    x = torch.randn((total, 32 * 64), device="cuda")
+    out, start = torch.empty_like(x), torch.from_numpy(starts(rows)).cuda()
+    ragged = us_of(lambda: q.apr_kv8_attention(cache, table, lens, x, out, 32, row_start=start, max_rows=max_rows))
+    table1, lens1 = (t.repeat_interleave(torch.tensor(rows, device="cuda"), 0) for t in (table, lens))
+    single = us_of(lambda: q.apr_kv8_attention(cache, table1, lens1, x, out, 32))
+    q.apr_stream_status()
+    assert ragged <= 4 * single, (ragged, single)
