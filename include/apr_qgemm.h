@@ -85,7 +85,8 @@
  * most), for the exact leg its split copies of X, exponents and, when k is
  * split over CTAs, up to four partial outputs of T*n floats, and, for
  * apr_prefill_attention, the fp16 copies of the K and V cache rows it reads. Calls on one stream share their stream's buffers,
- * which are ordered by the stream. A buffer grows on demand with cudaMalloc (also during a
+ * which are ordered by the stream, from whichever host threads the calls come
+ * (one call's launches are not enqueued between another's). A buffer grows on demand with cudaMalloc (also during a
  * stream capture: the calling thread's capture mode is relaxed for that
  * call) and is never freed while the process runs; a grown buffer replaces
  * the old one for later calls and the old one is kept. A graph captured from
@@ -298,8 +299,8 @@ int apr_qgemm_f16_in(int qtype, const void* W, const void* Wu, int n, int k, con
  *     call; once it has succeeded it is kept for the process.
  *   - Every call shares the one array, which keeps the last call's contents
  *     (each call overwrites the T*k values it reads, so nothing needs
- *     clearing). Calls whose work overlaps on the GPU (on different streams,
- *     or from different threads) race on it: order them on one stream.
+ *     clearing). Calls whose work overlaps on the GPU (on different streams)
+ *     race on it: order them on one stream.
  * Other arguments, errors and the status word as for apr_qgemm.
  */
 #define APR_NOALLOC_MAX_TK (8 * 1024 * 1024)

@@ -84,7 +84,8 @@ int device_state(DeviceState** out) {
 // GEMV. Calls on one stream are ordered by it, and every kernel touches
 // scratch only after waiting for the kernel before it (griddepcontrol.wait),
 // so one buffer serves every call on the stream and successive kernels still
-// overlap (no allocation between them). A buffer only grows: a larger one
+// overlap (no allocation between them). A call of several launches holds the
+// stream's StreamOrder over them. A buffer only grows: a larger one
 // replaces it and the old one is kept, so graphs captured with it stay valid.
 // Growth uses cudaMalloc with the calling thread's capture mode relaxed for
 // the call, so that it also works while the stream is being captured. A graph
@@ -246,6 +247,7 @@ int run(const Problem& p) {
   rc = device_state(&st);
   if (rc != APR_OK) return rc;
 
+  const StreamOrder order(p.s);
   int path = p.path;
   if (path == APR_PATH_AUTO) path = p.T <= APR_AUTO_GEMV_MAX_T ? APR_PATH_GEMV : APR_PATH_GEMM;
   // The exact leg's tensor-core GEMM beats the CUDA-core GEMVs (their FFMA
@@ -355,6 +357,7 @@ int run_ffn(const apr_ffn_args& a) {
   int rc = device_state(&st);
   if (rc != APR_OK) return rc;
   const cudaStream_t s = (cudaStream_t)a.stream;
+  const StreamOrder order(s);
   const int chunk = a.T < APR_FFN_CHUNK_ROWS ? a.T : APR_FFN_CHUNK_ROWS;
   // h: the normed rows, fp32, or fp16 padded to kMinXRows rows
   const size_t h_bytes = align256(std::max((size_t)chunk * a.hidden * 4, (size_t)padded_x_rows(chunk) * a.hidden * 2));
@@ -411,6 +414,7 @@ int run_normed(const Problem& p, const float* w, float eps) {
   DeviceState* st = nullptr;
   rc = device_state(&st);
   if (rc != APR_OK) return rc;
+  const StreamOrder order(p.s);
   int path = p.path;
   if (path == APR_PATH_AUTO) path = p.T <= APR_AUTO_GEMV_MAX_T ? APR_PATH_GEMV : APR_PATH_GEMM;
   const bool tc = p.leg == APR_LEG_F16 && path == APR_PATH_GEMM && p.k % 256 == 0;
@@ -488,6 +492,7 @@ int run_layer(const apr_layer_args& a) {
   int rc = device_state(&st);
   if (rc != APR_OK) return rc;
   const cudaStream_t s = (cudaStream_t)a.stream;
+  const StreamOrder order(s);
   const int chunk = a.chunk > 0 ? a.chunk : 512;
   const int rmax = a.T < chunk ? a.T : chunk;
   // the chunk's normed rows (fp32 at most), q and the attention output
@@ -569,6 +574,12 @@ int run_layer(const apr_layer_args& a) {
 }  // namespace
 
 namespace apr {
+
+namespace {
+std::recursive_mutex g_order[64];
+}  // namespace
+
+StreamOrder::StreamOrder(cudaStream_t s) : lock_(g_order[((uintptr_t)s >> 4 ^ (uintptr_t)s >> 10) % 64]) {}
 
 int set_error(int code, const char* msg) {
   snprintf(t_msg, sizeof t_msg, "%s", msg);
@@ -718,6 +729,7 @@ int apr_prefill_attention(const float* Q, const float* K_cache, const float* V_c
   int rc = device_state(&st);
   if (rc != APR_OK) return rc;
   // the stream's scratch holds the fp16 copies of K and of V transposed
+  const StreamOrder order((cudaStream_t)stream);
   void* scratch = nullptr;
   rc = stream_scratch(st->dev, (cudaStream_t)stream, kScratchAttn,
                       prefill_attention_scratch_bytes(T, pos0, num_kv_heads), &scratch);

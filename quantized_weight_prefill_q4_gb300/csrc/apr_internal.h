@@ -4,6 +4,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <mutex>
 #include <cuda_runtime.h>
 
 namespace apr {
@@ -176,6 +177,18 @@ int launch_gemm_xs(int qtype, const void* W, const void* Wu, int n, int k, const
 int set_error(int code, const char* msg);
 int check_gemm_args(int qtype, const void* W, int n, int k, const float* X, int T, const float* Y, const float* R);
 unsigned* status_word_address();
+
+// Held by a call from the lookup of its stream's scratch until its last launch.
+// What one of its launches leaves in scratch for a later one is ordered by the
+// stream only if no call of another host thread on that stream is enqueued
+// between them. Taken again by the calls that a call is made of; streams may
+// share a mutex.
+struct StreamOrder {
+  explicit StreamOrder(cudaStream_t s);
+
+ private:
+  std::unique_lock<std::recursive_mutex> lock_;
+};
 
 // Shared with the 8-bit cache's entry points (kv8_api.cu): checks the current
 // device and gives its status word; the stream's scratch buffer of those

@@ -97,6 +97,7 @@ extern "C" int apr_qgemm_noalloc(int qtype, const void* W, int n, int k, const f
   rc = setup(&st);
   if (rc != APR_OK) return rc;
   const cudaStream_t s = (cudaStream_t)stream;
+  const StreamOrder order(s);
   cudaError_t e = launch_x_to_f16(X, st->scratch, (size_t)T * (size_t)k, s);
   if (e != cudaSuccess) return set_error(APR_E_LAUNCH, cudaGetErrorString(e));
   char msg[256] = "";

@@ -107,3 +107,104 @@ def test_the_time_does_not_grow_with_the_rows_that_a_sequence_may_have(q, rows, 
     single = us_of(lambda: q.apr_kv8_attention(cache, table1, lens1, x, out, 32))
     q.apr_stream_status()
     assert ragged <= 4 * single, (ragged, single)
+
+
+# ---------------------------------------------------------------- host threads that share a stream
+def both_at_once(calls, times):
+    """Two threads make their calls `times` times, both on one stream: the outputs of each."""
+    import threading
+
+    ready, outs, failed = threading.Barrier(2), [[], []], []
+
+    def work(i):
+        try:
+            ready.wait()
+            for k in range(times):
+                calls[i](outs[i][k])
+        except Exception as e:  # (an assertion of the main thread's)
+            failed.append(e)
+
+    for i, call in enumerate(calls):
+        outs[i] = [call(None) for _ in range(times)]
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+    return outs
+
+
+def test_two_threads_attend_on_one_stream(q):
+    # each call's second launch reads what its first left in the stream's scratch
+    stream = torch.cuda.Stream()
+    cases = [Case([3000, 33], 2, 128, 64, seed=70).on_gpu(q), Case([40, 1700, 900], 2, 128, 64, seed=71).on_gpu(q)]
+    rows = [torch.from_numpy(c.rng.normal(size=(len(c.lens), 8 * 128)).astype(np.float32)).cuda() for c in cases]
+
+    def call(i):
+        c, x = cases[i], rows[i]
+
+        def run(out):
+            if out is None:
+                return torch.full_like(x, 9.0), torch.full((len(c.lens), 2, c.table.shape[1] * 64), 9.0, device="cuda")
+            q.apr_kv8_attention(c.cache, c.gtable, c.glens, x, out[0], 8, weights=out[1], stream=stream)
+
+        return run
+
+    outs = both_at_once([call(0), call(1)], 200)
+    q.apr_stream_status(stream)
+    for i, c in enumerate(cases):
+        ref = oracle.kv8_attention(c.host, c.table, c.lens, None, as_f32(rows[i]), 8)
+        assert_attention(c, outs[i][0][0], ref)
+        assert_weights(c, outs[i][0][1], ref)
+        for out, w in outs[i][1:]:
+            assert torch.equal(out, outs[i][0][0]) and torch.equal(w, outs[i][0][1])
+
+
+def test_two_threads_multiply_on_one_stream(q):
+    # the GEMM's fp16 copy of its rows, the FFN sublayer's normed rows and activations
+    import synth
+    from gpu_util import assert_f16_leg, dev
+
+    stream = torch.cuda.Stream()
+    cases = [synth.make_case(synth.Q4_0, 1024, 2048, T, seed=72 + T) for T in (64, 200)]
+    ins = [(dev(c["W"]), dev(c["X"])) for c in cases]
+
+    def call(i):
+        W, X = ins[i]
+
+        def run(out):
+            if out is None:
+                return torch.full((X.shape[0], 1024), 9.0, device="cuda")
+            q.apr_qgemm(synth.Q4_0, W, 1024, 2048, X, X.shape[0], out, stream=stream)
+
+        return run
+
+    outs = both_at_once([call(0), call(1)], 200)
+    q.apr_stream_status(stream)
+    for c, ys in zip(cases, outs):
+        assert_f16_leg(ys[0].cpu().numpy(), oracle.qgemm_f64(synth.Q4_0, c["W"], 1024, 2048, c["X"]))
+        assert all(torch.equal(y, ys[0]) for y in ys[1:])
+    layers = []
+    for i in range(2):
+        ws = [dev(synth.quantize(synth.Q4_0, synth.weight_f32(n, k, 80 + 3 * i + j))) for j, (n, k) in enumerate(((1024, 512), (1024, 512), (512, 1024)))]
+        layers.append((ws, torch.ones(512, device="cuda"), dev(synth.activations(40 + 60 * i, 512, 90 + i))))
+
+    def sublayer(i):
+        ws, norm, X = layers[i]
+
+        def run(out):
+            if out is None:
+                return X.clone()
+            q.apr_ffn_sublayer(synth.Q4_0, *ws, 512, 1024, out.shape[0], norm, 1e-6, out, stream=stream)
+
+        return run
+
+    outs = both_at_once([sublayer(0), sublayer(1)], 100)
+    q.apr_stream_status(stream)
+    for i, ys in enumerate(outs):
+        alone = layers[i][2].clone()
+        q.apr_ffn_sublayer(synth.Q4_0, *layers[i][0], 512, 1024, alone.shape[0], layers[i][1], 1e-6, alone)
+        assert all(torch.equal(y, alone) for y in ys)
