@@ -2,7 +2,9 @@
 
 Like :mod:`.capi` it only marshals: tensors become device pointers, sizes are
 checked against the tensors so that no call can address past an allocation,
-and a nonzero status raises :class:`~.capi.AprError`.
+and a nonzero status raises :class:`~.capi.AprError`. The library works on the
+calling thread's current device: tensors on another than the cache's, and a
+cache on another than that, are refused.
 """
 
 from __future__ import annotations
@@ -22,6 +24,7 @@ KV8_EXPORTS = ("apr_kv8_append", "apr_kv8_read", "apr_kv8_attention", "apr_kv8_e
 
 _I8, _I32, _F32, _Tensor = torch.int8, torch.int32, torch.float32, torch.Tensor
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 _TYPES = {torch.float32: APR_T_F32, torch.float16: APR_T_F16, torch.bfloat16: APR_T_BF16}
 
 
@@ -71,21 +74,28 @@ def _bind():
 _lib = _bind()
 
 
-def _array(x, name, dtype, dims):
-    """A contiguous CUDA tensor of the type and number of dimensions, checked."""
-    if isinstance(x, _Tensor) and x.is_cuda and x.dtype is dtype and x.ndim == dims and x.is_contiguous():
-        return x
+def _array(x, name, dtype, dims, device=None):
+    """A contiguous CUDA tensor of the type and number of dimensions on the
+    device (an index), checked."""
+    if isinstance(x, _Tensor) and x.get_device() == device and x.dtype is dtype and x.ndim == dims and x.is_contiguous():
+        return x  # (a tensor that is not on a GPU has no device index)
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name}: expected a CUDA tensor, got {type(x).__name__}")
     if not x.is_cuda:
         raise ValueError(f"{name}: tensor is on {x.device}, the library takes device memory")
     if x.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype}, got {x.dtype}")
+    if x.get_device() != device:
+        raise ValueError(f"{name}: tensor is on device {x.get_device()}, the cache on {device}")
     raise ValueError(f"{name}: expected a contiguous tensor of {dims} dimensions, got shape {tuple(x.shape)}")
 
 
 def _stream(stream, device_index):
-    """The raw stream: the given one, or torch's current one."""
+    """The raw stream: the given one, or torch's current one. The library takes
+    scratch and status word, and launches, on the current device."""
+    device = _current_device()
+    if device != device_index:
+        raise ValueError(f"the cache is on device {device_index}, the current device is {device}")
     return _raw_stream(device_index) if stream is None else capi._stream(stream)
 
 
@@ -101,14 +111,15 @@ class Kv8Cache:
     v_scale = property(lambda self: self._arrays[3])
 
     def __init__(self, K, V, k_scale, v_scale):
-        shape = _array(K, "K", _I8, 4).shape
+        device = K.get_device() if isinstance(K, _Tensor) else None
+        shape = _array(K, "K", _I8, 4, device).shape
         scales = shape[:2]
-        if (_array(V, "V", _I8, 4).shape != shape or _array(k_scale, "k_scale", _F32, 2).shape != scales
-                or _array(v_scale, "v_scale", _F32, 2).shape != scales):
+        if (_array(V, "V", _I8, 4, device).shape != shape or _array(k_scale, "k_scale", _F32, 2, device).shape != scales
+                or _array(v_scale, "v_scale", _F32, 2, device).shape != scales):
             raise ValueError("Kv8Cache: V, k_scale and v_scale must match K's pages, heads, tokens and head_dim")
         self._arrays = (K, V, k_scale, v_scale)
         pages, self.kv_heads, self.page_tokens, self.head_dim = shape
-        self.device_index = K.get_device()
+        self.device_index = device
         self._c = _Cache(K.data_ptr(), V.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, self.kv_heads,
                          self.page_tokens, self.head_dim)
 
@@ -124,23 +135,26 @@ class Kv8Cache:
                    torch.zeros(codes[:2], dtype=torch.float32, device=device))
 
 
-def _rows(page_table, lens, row_start, num_rows, max_rows, max_len):
-    seqs, width = _array(page_table, "page_table", _I32, 2).shape
-    if _array(lens, "lens", _I32, 1).numel() != seqs:
+def _rows(cache, page_table, lens, row_start, num_rows, max_rows, max_len):
+    device = cache.device_index
+    seqs, width = _array(page_table, "page_table", _I32, 2, device).shape
+    if _array(lens, "lens", _I32, 1, device).numel() != seqs:
         raise ValueError(f"page_table has {seqs} rows, lens {lens.numel()} entries")
     start = None
     if row_start is not None:
-        if _array(row_start, "row_start", _I32, 1).numel() != seqs + 1:
+        if _array(row_start, "row_start", _I32, 1, device).numel() != seqs + 1:
             raise ValueError(f"row_start: expected {seqs + 1} entries, got {row_start.numel()}")
         start = row_start.data_ptr()
     return _Rows(page_table.data_ptr(), width, lens.data_ptr(), start, seqs, num_rows, max_rows, max_len)
 
 
-def _matrix(x, name, width, like=None):
+def _matrix(x, name, width, device=None, like=None):
     """(pointer, rows, elements from row to row) of rows of `width` elements: a
     2-D tensor, or a 3-D one of [rows][heads][head_dim], whose rows are dense."""
-    if not (isinstance(x, _Tensor) and x.is_cuda and x.dtype in _TYPES):
-        raise ValueError(f"{name}: expected a float32, float16 or bfloat16 CUDA tensor")
+    if not (isinstance(x, _Tensor) and x.get_device() == device and x.dtype in _TYPES):
+        if not (isinstance(x, _Tensor) and x.is_cuda and x.dtype in _TYPES):
+            raise ValueError(f"{name}: expected a float32, float16 or bfloat16 CUDA tensor")
+        raise ValueError(f"{name}: tensor is on device {x.get_device()}, the cache on {device}")
     shape, stride = x.shape, x.stride()
     if len(shape) == 2:
         dense = shape[1] == width and stride[1] == 1
@@ -158,8 +172,8 @@ def _matrix(x, name, width, like=None):
 
 def _k_and_v(cache, k, v):
     width = cache.kv_heads * cache.head_dim
-    kp, rows, ld = _matrix(k, "k", width)
-    vp, _, vld = _matrix(v, "v", width, like=k)
+    kp, rows, ld = _matrix(k, "k", width, cache.device_index)
+    vp, _, vld = _matrix(v, "v", width, cache.device_index, like=k)
     if vld != ld and rows > 1:
         raise ValueError(f"k and v must have the same row stride, got {ld} and {vld}")
     return kp, vp, rows, ld
@@ -170,7 +184,7 @@ def apr_kv8_append(cache, page_table, lens, k, v, *, row_start=None, max_rows=0,
     rows allowed) into the cache, as the last positions of their sequences:
     lens counts them already. row_start None: one row a sequence."""
     kp, vp, n, ld = _k_and_v(cache, k, v)
-    rows = _rows(page_table, lens, row_start, n, max_rows, 0)
+    rows = _rows(cache, page_table, lens, row_start, n, max_rows, 0)
     return capi._check(_lib.apr_kv8_append(cache._c, rows, _TYPES[k.dtype], kp, vp, ld, _stream(stream, cache.device_index)))
 
 
@@ -178,7 +192,7 @@ def apr_kv8_read(cache, page_table, lens, k, v, *, row_start=None, max_rows=0, s
     """Writes the values of each sequence's last rows to k and v (their types
     and strides as for the append)."""
     kp, vp, n, ld = _k_and_v(cache, k, v)
-    rows = _rows(page_table, lens, row_start, n, max_rows, 0)
+    rows = _rows(cache, page_table, lens, row_start, n, max_rows, 0)
     return capi._check(_lib.apr_kv8_read(cache._c, rows, _TYPES[k.dtype], kp, vp, ld, _stream(stream, cache.device_index)))
 
 
@@ -189,12 +203,12 @@ def apr_kv8_attention(cache, page_table, lens, q, out, num_heads, *, row_start=N
     ([sequences][kv_heads][>= max_len] float32) receives, or with accumulate
     adds, the weight of each position. max_len bounds lens (0: the table)."""
     width = num_heads * cache.head_dim
-    qp, n, ldq = _matrix(q, "q", width)
-    op, _, ldo = _matrix(out, "out", width, like=q)
-    rows = _rows(page_table, lens, row_start, n, max_rows, max_len)
+    qp, n, ldq = _matrix(q, "q", width, cache.device_index)
+    op, _, ldo = _matrix(out, "out", width, cache.device_index, like=q)
+    rows = _rows(cache, page_table, lens, row_start, n, max_rows, max_len)
     wp, wld = None, 0
     if weights is not None:
-        seqs, heads, wld = _array(weights, "weights", _F32, 3).shape
+        seqs, heads, wld = _array(weights, "weights", _F32, 3, cache.device_index).shape
         if seqs != rows.num_seqs or heads != cache.kv_heads:
             raise ValueError(f"weights: expected [{rows.num_seqs}][{cache.kv_heads}][...], got {tuple(weights.shape)}")
         wp = weights.data_ptr()
@@ -209,16 +223,16 @@ def apr_kv8_evict(cache, page_table, lens, weights, budget, recent, fresh_pages,
     ([sequences][ceil(budget / page_tokens)]); table_out, lens_out, weights_out
     ([sequences][kv_heads][>= budget]) and kept ([sequences][kv_heads][budget])
     say what the sequences are afterwards."""
-    rows = _rows(page_table, lens, None, 0, 0, max_len)
-    n, heads = rows.num_seqs, cache.kv_heads
+    rows = _rows(cache, page_table, lens, None, 0, 0, max_len)
+    n, heads, device = rows.num_seqs, cache.kv_heads, cache.device_index
 
     def check(x, name, dtype, shape):
-        if tuple(_array(x, name, dtype, len(shape)).shape) != shape:
+        if tuple(_array(x, name, dtype, len(shape), device).shape) != shape:
             raise ValueError(f"{name}: expected shape {shape}, got {tuple(x.shape)}")
         return x.data_ptr()
 
     def check_weights(x, name):
-        shape = _array(x, name, _F32, 3).shape
+        shape = _array(x, name, _F32, 3, device).shape
         if shape[0] != n or shape[1] != heads:
             raise ValueError(f"{name}: expected [{n}][{heads}][...], got {tuple(shape)}")
         return x.data_ptr(), shape[2]
