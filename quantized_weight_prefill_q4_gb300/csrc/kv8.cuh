@@ -33,7 +33,7 @@ __device__ __forceinline__ void kv8_flag(const Kv8View& v) { atomicOr(v.status, 
 // claims more would overwrite tokens that it holds.
 __device__ __forceinline__ int kv8_len(const Kv8View& v, int b) {
   const int n = v.lens[b];
-  if (n >= 0 && n <= v.max_len) return n;
+  if ((unsigned)n <= (unsigned)v.max_len) return n;
   kv8_flag(v);
   return 0;
 }
