@@ -706,14 +706,14 @@ constexpr int W_PAIRS = 64;
 
 template <int D, int GROUPS>
 __global__ void __launch_bounds__(D / 4 * GROUPS) kv8_finish_kernel(const __grid_constant__ AttnArgs a, int combine_x) {
-  grid_dependency_wait();
-  grid_launch_dependents();
   constexpr int LANES = D / 4, THREADS = LANES * GROUPS;
   __shared__ float4 s_o[GROUPS][LANES];
   __shared__ float2 s_ml[GROUPS > W_PAIRS ? GROUPS : W_PAIRS];
   const Kv8View& v = a.v;
   const bool combines = (int)blockIdx.x < combine_x;
   const int unit = (int)(blockIdx.y * combine_x + blockIdx.x), row = unit / a.heads, head = unit % a.heads;
+  grid_dependency_wait();
+  grid_launch_dependents();
   if (combines && row >= v.num_rows) return;
   const int b = combines ? kv8_sequence_of(v, row) : (int)blockIdx.y, len = kv8_len(v, b), su = segment_units(a, len);
   const Kv8Span span = kv8_rows(v, b);
@@ -782,9 +782,14 @@ __global__ void __launch_bounds__(D / 4 * GROUPS) kv8_finish_kernel(const __grid
         all = m == -INFINITY ? all : all * exp2f(m - top);  // (a lane without pieces: 0, or NaN)
 #pragma unroll
         for (int x = 4; x > 0; x >>= 1) all += __shfl_xor_sync(0xffffffffu, all, x);
-        if (lane == 0 && p < np)
-          s_ml[p] = pieces.n == 1 ? a.final_ml[at + p0 + p]
-                                  : make_float2(top == -INFINITY ? 0.f : top, all > 0.f || all != all ? 1.f / all : 0.f);
+        if (lane == 0 && p < np) {
+          const float2 ml = pieces.n == 1 ? a.final_ml[at + p0 + p]
+                                          : make_float2(top == -INFINITY ? 0.f : top, all > 0.f || all != all ? 1.f / all : 0.f);
+          // Where the total is NaN, a reference that leaves a NaN score NaN and turns that of
+          // a position behind the row, minus infinity, into the weight 0 (minus infinity less
+          // NaN would be NaN).
+          s_ml[p] = ml.y != ml.y ? make_float2(INFINITY, 1.f) : ml;
+        }
       }
       __syncthreads();
       if (j < len) {

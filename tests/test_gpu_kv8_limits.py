@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import oracle
-from test_gpu_kv8 import Case, as_f32, assert_attention, assert_weights, attend, bad_index, starts
+from test_gpu_kv8 import Case, as_f32, assert_attention, assert_weights, attend, bad_index, rows_tensor, starts
 
 pytestmark = pytest.mark.gpu
 
@@ -208,3 +208,26 @@ def test_two_threads_multiply_on_one_stream(q):
         alone = layers[i][2].clone()
         q.apr_ffn_sublayer(synth.Q4_0, *layers[i][0], 512, 1024, alone.shape[0], layers[i][1], 1e-6, alone)
         assert all(torch.equal(y, alone) for y in ys)
+
+
+# ---------------------------------------------------------------- values out of the ordinary
+@pytest.mark.parametrize("lens", [[70, 33], [70, 1700], [2100, 1]])  # whole and divided segments
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+def test_a_bad_row_gives_no_weight_to_positions_behind_it(q, bad, lens):
+    c = Case(lens, 2, 64, 64, seed=80, extra_width=0).on_gpu(q)
+    rows = [min(5, n) for n in lens]
+    qh = c.rng.normal(size=(sum(rows), 4 * 64))
+    qh[1, 70] = bad  # the second row's head 1, of the first KV head: it does not see the last three positions
+    qt, out = rows_tensor(qh, torch.float32), torch.empty((sum(rows), 4 * 64), device="cuda")
+    w = torch.full((2, 2, c.table.shape[1] * 64), 3.0, device="cuda")
+    q.apr_kv8_attention(c.cache, c.gtable, c.glens, qt, out, 4, row_start=torch.from_numpy(starts(rows)).cuda(), weights=w)
+    q.apr_stream_status()
+    sees = lens[0] - 3
+    finite = np.where(np.isfinite(qh), as_f32(qt), 0.0)  # (whatever the row gives, it gives to the first `sees` positions)
+    _, want, reach = oracle.kv8_attention(c.host, c.table, c.lens, starts(rows), finite, 4)
+    want[0, 0, :sees] = np.nan
+    got = w.cpu().numpy()
+    tol = (4 * 64 * 2.0 ** -24 * float(reach.max()) + 2.0 ** -20) * max(1.0, float(np.nanmax(want)))
+    for b, n in enumerate(lens):
+        np.testing.assert_allclose(got[b, :, :n], want[b, :, :n], rtol=0, atol=tol)
+        assert not got[b, :, n:].any()
