@@ -81,6 +81,10 @@ __host__ __device__ constexpr int overhead_units(int dim) { return 512 / dim; }
 constexpr int TILE = 32;      // positions of a tile, within one page
 constexpr float HEADROOM = 10.f;  // weights are kept times 2^10
 constexpr float MOVE_ABOVE = 4.f;  // the reference moves when the maximum is more than this above it
+// V's scales enter times 2^-24, which the end takes back: of unnormalised weights,
+// 2^10 and more each, the sum over 1000 values of 2^108 would pass float32's
+// range (exact for scales from 2^-102 on, below which a value's last bits go).
+constexpr float V_DOWN = 0x1p-24f, V_UP = 0x1p24f;
 
 struct AttnArgs {
   Kv8View v;
@@ -219,7 +223,8 @@ __device__ __forceinline__ void finish4(const AttnArgs& a, int r0, int n, int g,
                                         const float4& o, float m, float total) {
   const float inv = total > 0.f || total != total ? 1.f / total : 0.f;  // no position seen: zeros
   const size_t row = r0 + pair / a.group, head = g * a.group + pair % a.group;
-  store4_any(a.out, a.type, row * a.ldo + head * dim + d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+  const float up = inv * V_UP;
+  store4_any(a.out, a.type, row * a.ldo + head * dim + d, make_float4(o.x * up, o.y * up, o.z * up, o.w * up));
   if (a.final_ml && d == 0) a.final_ml[pair_at(a, r0, n, g) + pair] = make_float2(m, inv);
 }
 
@@ -472,7 +477,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(D, MT))
         ks_all = v.k_scale[scale_at];
         vs_all = v.v_scale[scale_at];
       }
-      const float ks = __shfl_sync(0xffffffffu, ks_all, i & 31), vs = __shfl_sync(0xffffffffu, vs_all, i & 31);
+      const float ks = __shfl_sync(0xffffffffu, ks_all, i & 31), vs = __shfl_sync(0xffffffffu, vs_all, i & 31) * V_DOWN;
       const int k = k0 + (warp + i * WARPS) * TILE;
 
       // ---- scores of the tile's 32 positions: 4 columns of 8

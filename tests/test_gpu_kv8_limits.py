@@ -231,3 +231,15 @@ def test_a_bad_row_gives_no_weight_to_positions_behind_it(q, bad, lens):
     for b, n in enumerate(lens):
         np.testing.assert_allclose(got[b, :, :n], want[b, :, :n], rtol=0, atol=tol)
         assert not got[b, :, n:].any()
+
+
+@pytest.mark.parametrize("dim,type_,lens", [(64, "f32", [300, 2500]), (256, "bf16", [70, 600]), (128, "f32", [400, 33])])
+@pytest.mark.parametrize("exponent", [105, 115, -90])
+def test_values_at_the_ends_of_the_range(q, dim, type_, lens, exponent):
+    # values of 10^33 and 10^36, all of one sign, whose sums over a few hundred positions no float32 holds; and of 10^-26
+    c = Case(lens, 1, dim, 64, seed=81)
+    c.host["v_scale"][:] *= np.float32(2.0 ** exponent) / c.host["v_scale"].mean()
+    c.host["V"][:] = np.abs(c.host["V"]) // 2 + 60
+    c.on_gpu(q)
+    out, _, ref = attend(q, c, 2, type_=type_)
+    assert_attention(c, out, ref, type_)
