@@ -72,6 +72,15 @@ constexpr int MOST_UNITS = 1 << 30;  // of a call, as its arguments are checked 
 // 11.3 us on the device, divided 8.0 / 8.4 / 8.5; 64 sequences 16.2 / 24.1 / 30.4
 // and 18.5 / 24.9 / 28.7. At 256 dims the sides meet at half the length.
 constexpr int WHOLE_SIZE = 512 * 128;
+// With weights there is a second launch either way, and what stays undivided saves
+// only its combination. Where a KV head's pairs are one segment, dividing pays from
+// less on: 1 / 8 / 64 sequences of 500 positions, one row, 8 heads of 128, 12.3 / 15.0
+// / 29.7 us whole, 9.7 / 12.9 / 26.9 divided; of 1000, 64 dims, 13.3 / 16.2 / 29.9 and
+// 8.9 / 12.2 / 27.7; of 200, 128 dims, 10.1 / 13.1 / 20.1 and 9.4 / 12.4 / 20.7; of 100,
+// 9.4 / 10.1 / 17.1 and 9.6 / 11.9 / 17.9. With more segments the pieces cost more
+// (32 rows, 500 positions of 128: 34.7 / 54.5 whole, 42.3 / 68.2 divided), at 256
+// dims too (64 of 256, 17.7 and 22.5).
+constexpr int WHOLE_SIZE_WEIGHTED = 192 * 128;
 constexpr int MIN_SHARE = 2;  // units of a CTA's share, where there are not enough for every CTA
 // Units that a segment counts for besides its positions: what its start (the
 // way from the length over the page table to the codes, the query rows) and
@@ -907,7 +916,8 @@ cudaError_t launch_kv8_attention(const Kv8View& v, const Kv8Attention& in, void*
   a.pairs = 8 * l.mt;
   a.scale_log2 = in.scale * 1.4426950408889634f;
   a.ctas = l.ctas;
-  a.whole = (long long)v.max_len * v.dim <= WHOLE_SIZE;
+  const bool one_segment = (long long)v.max_rows * a.group <= a.pairs;  // of a KV head
+  a.whole = (long long)v.max_len * v.dim <= (in.weights && one_segment && v.dim < 256 ? WHOLE_SIZE_WEIGHTED : WHOLE_SIZE);
   a.prefix = reinterpret_cast<int*>(base + l.prefix);
   a.part_ml = reinterpret_cast<float2*>(base + l.part_ml);
   a.part_o = reinterpret_cast<float*>(base + l.part_o);

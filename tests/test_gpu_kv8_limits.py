@@ -243,3 +243,16 @@ def test_values_at_the_ends_of_the_range(q, dim, type_, lens, exponent):
     c.on_gpu(q)
     out, _, ref = attend(q, c, 2, type_=type_)
     assert_attention(c, out, ref, type_)
+
+
+@pytest.mark.parametrize("dim,heads,group,rows", [(64, 2, 4, 1), (128, 1, 8, 2), (128, 2, 3, 6), (256, 1, 4, 2)])
+def test_weights_around_the_length_from_which_segments_are_divided(q, dim, heads, group, rows):
+    # one segment a KV head (up to 16 pairs) and more, at lengths on either side of 192 and 512 x 128 codes
+    lens = [512 * 128 // dim, 512 * 128 // dim - 1, 192 * 128 // dim + 1, 192 * 128 // dim, 7]
+    c = Case(lens, heads, dim, 32, seed=90).on_gpu(q)
+    for longest in (192 * 128 // dim, 192 * 128 // dim + 1, 512 * 128 // dim):
+        c.lens[:] = np.minimum(lens, longest)
+        c.glens.copy_(torch.from_numpy(c.lens))
+        out, w, ref = attend(q, c, heads * group, rows=[rows] * 5, weights=True, max_rows=rows, max_len=longest)
+        assert_attention(c, out, ref)
+        assert_weights(c, w, ref)
