@@ -256,3 +256,39 @@ def test_weights_around_the_length_from_which_segments_are_divided(q, dim, heads
         out, w, ref = attend(q, c, heads * group, rows=[rows] * 5, weights=True, max_rows=rows, max_len=longest)
         assert_attention(c, out, ref)
         assert_weights(c, w, ref)
+
+
+# ---------------------------------------------------------------- places past 2^32
+def test_every_operator_on_pages_past_4_gib(q):
+    # the same steps on the last pages of two arrays of 4.3e9 codes and on the first of two small ones: the same bits
+    pages, heads, tokens, dim, n = 8200, 8, 256, 256, 700
+    assert (pages - 8) * heads * tokens * dim >= 1 << 32
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("not enough memory")
+    gen = torch.Generator("cuda").manual_seed(91)
+    k, v, x = (torch.randn((rows, heads * dim), generator=gen, device="cuda") for rows in (n, n, 2))
+    weights = torch.rand((1, heads, 3 * tokens), generator=gen, device="cuda")
+    ints = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    results = []
+    for count in (pages, 8):
+        first = count - 8
+        cache = q.Kv8Cache.allocate(count, heads, dim, tokens)
+        table, lens = ints([[first + 7, first + 2, first + 5]]), ints([n])
+        q.apr_kv8_append(cache, table, lens, k, v, row_start=ints([0, n]))
+        q.apr_kv8_append(cache, table, lens, 2 * k[n - 40:], 2 * v[n - 40:], row_start=ints([0, 40]))  # raises the last page's scales
+        kb, vb, out, w = torch.empty_like(k), torch.empty_like(v), torch.empty_like(x), torch.empty_like(weights)
+        q.apr_kv8_read(cache, table, lens, kb, vb, row_start=ints([0, n]))
+        q.apr_kv8_attention(cache, table, lens, x, out, heads, row_start=ints([0, 2]), weights=w)
+        table_out, lens_out = torch.empty_like(table), torch.empty_like(lens)
+        kept, wo = torch.empty((1, heads, 300), dtype=torch.int32, device="cuda"), torch.empty((1, heads, 300), device="cuda")
+        q.apr_kv8_evict(cache, table, lens, weights, 300, 20, ints([[first + 6, first + 3]]), table_out, lens_out, wo, kept)
+        q.apr_stream_status()
+        ends = [a[first:].clone() for a in (cache.K, cache.V, cache.k_scale, cache.v_scale)]
+        results.append(ends + [kb, vb, out, w, kept, wo, lens_out, table_out - first * (table_out >= 0).int()])
+        assert all(bool(e[p].any()) for e in ends for p in (2, 3, 5, 6, 7))
+        if first:  # nothing went anywhere else
+            for a in (cache.K, cache.V):
+                assert not any(bool(a[i:min(i + 512, first)].view(torch.int64).any()) for i in range(0, first, 512))
+            assert not cache.k_scale[:first].any() and not cache.v_scale[:first].any()
+    for big, small in zip(*results):
+        assert torch.equal(big, small)
