@@ -29,14 +29,17 @@
  * kernels run, so a captured step can be replayed as they change.
  *
  * What the device arrays say is checked where it is used: a page id outside
- * 0 .. num_pages - 1, a length past table_ld * page_tokens or max_len, a
+ * 0 .. num_pages - 1, a length below 0 or past table_ld * page_tokens or max_len, a
  * row_start that is not within 0 .. num_rows and non-decreasing, or more rows
- * of one sequence than max_rows touch no memory; they set a bit of the device
- * status word, and the next apr_stream_status returns APR_E_INVAL (the call's
- * outputs are then unspecified). A sequence whose length is out of range counts
- * as one of no tokens, one whose rows are as one without rows: nothing of it is
- * appended or moved, what it holds in the cache stays as it is, and weights that
- * are added up over calls do not change.
+ * of one sequence than max_rows make no access outside the call's arrays; they
+ * set a bit of the device status word, and the next apr_stream_status returns
+ * APR_E_INVAL (the call's outputs are then unspecified). Where a page id is out
+ * of range, the append writes none of that page's rows, the read none of its
+ * values, the eviction takes them for zeros or writes no such page, and the
+ * attention reads page 0 in its place. A sequence whose length is out of range
+ * counts as one of no tokens, one whose rows are as one without rows: nothing of
+ * it is appended or moved, what it holds in the cache stays as it is, and weights
+ * that are added up over calls do not change.
  *
  * All pointers are device pointers, caller owned; codes, rows and outputs on
  * 16-byte boundaries, the other arrays on their element's. Calls are
@@ -130,9 +133,14 @@ int apr_kv8_read(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int type,
  *            max_len is 0.
  * A row that sees no position gives zeros. q is split into two fp16 pieces
  * (22 bits of the row's largest magnitude), the softmax weights likewise, the
- * codes enter the products exactly, and every sum is float32: float32 results
- * are within a few 1e-6 of the exact attention of the cache's values. A NaN or
- * an infinity in a query row makes that row and head NaN.
+ * codes enter the products exactly, and every sum is float32: of rows of about
+ * unit variance float32 results are within a few 1e-6 of the exact attention of
+ * the cache's values. What limits them is a score's error, some 2^-22 of the sum of
+ * |scale q K|, and that weights below 2^-34 of the row's largest are left out of
+ * its outputs (but not of its total): at most 2^-34 of V's largest value for each
+ * such position, 2^-14 for a million of them beside one that takes all. A NaN or an
+ * infinity in a query row makes that row and head NaN, and the weights of the
+ * positions that the row sees.
  * out must not overlap q, the cache or weights. Scratch per stream: partial
  * results of 8 or 16 (row, head) pairs for each resident CTA (at most 8 MB), and,
  * with weights, the scores (4 * num_rows * num_heads * max_len bytes, max_len
