@@ -7,16 +7,16 @@
 // raised, and writes the new codes. A CTA takes several heads of the page one
 // after the other, K or V: the way from the lengths over the table to the page
 // is gone once, and the next head's rows are under way while one is rounded.
-// The pages that a call touches are numbered through (each CTA adds up the
-// sequences before its own), so that prompts of different lengths leave no CTA
-// without work.
+// The pages that a call may touch are numbered through, so that prompts of
+// different lengths leave at most two CTAs a sequence (of each head) without work.
 // Bound by memory: a row is read once (up to 32 registers a thread hold it
 // between the two passes; what a larger page has more comes from L1 the second
 // time) and one byte a value written; the rounding is five instructions and a
 // byte permute a value (kv8_codes8).
 //
-// Measured (GB300): 13000 rows of 8 heads of 128 in bf16, 9 prompts: 24.6 us, 80 MB
-// (0.49 of the HBM rate); 50001 of 8 heads of 64 in fp16: 35.8 us, 154 MB (0.64).
+// Measured (GB300): 13000 rows of 8 heads of 128 in bf16, 9 prompts: 22.8 us, 80 MB
+// (0.52 of the HBM rate); 50001 of 8 heads of 64 in fp16: 34.1 us, 154 MB (0.67); the 13000
+// rows of 4 heads of 256 in float32: 32.4 us, 133 MB (0.61).
 // What is left is the way of each CTA to its first rows (loaded while the page
 // table is looked at) and the barrier between its two passes: rows loaded ahead
 // for the next head (128 registers, 4 CTAs) gained nothing over more CTAs.
@@ -32,7 +32,9 @@ namespace apr {
 namespace {
 
 constexpr int A_THREADS = 128;
-constexpr int A_CTAS = 5;  // on an SM (102 registers; the 50001 rows 36 us, 39 with 6 of 80, 41 with 7)
+// On an SM (96 registers; the three shapes above with 4 / 6 / 7: 24.0 / 24.2 / 24.9, 36.5 / 37.8 / 40.0,
+// 30.1 / 31.6 / 33.5 us).
+constexpr int A_CTAS = 5;
 constexpr int A_WARPS = A_THREADS / 32;
 
 // The largest magnitude; NaN is passed over, an infinity is not (the caller
@@ -79,10 +81,12 @@ __device__ __forceinline__ float block_max(float m, float* warp_max) {
   return m;
 }
 
-// Pages that the rows of sequence b go to.
-__device__ __forceinline__ int pages_touched(const Kv8View& v, int b) {
-  const int len = kv8_len(v, b), n = kv8_rows(v, b).n;
-  return n == 0 || len == 0 ? 0 : ((len - 1) >> v.page_shift) - (max(len - n, 0) >> v.page_shift) + 1;
+// The first of a sequence's units, one for each page that its rows may go to: n
+// rows touch at most n / page_tokens + 2 pages, so this many further on begins the next
+// one's, and a CTA finds its sequence by a search instead of adding up all of them
+// (2 rows of each of 16384 sequences: 0.6 ms, 10.8 when every CTA did).
+__device__ __forceinline__ int first_append_unit(const Kv8View& v, int b) {
+  return (v.row_start[b] >> v.page_shift) + 2 * b;
 }
 
 template <typename T, int D>
@@ -97,46 +101,22 @@ __global__ void __launch_bounds__(A_THREADS, A_CTAS) kv8_append_kernel(const __g
   constexpr int HELD = 16 / sizeof(T);  // vectors of 8 values a thread keeps between the passes, 32 registers
   constexpr int ROW = D / 8;            // vectors of a row
   __shared__ float s_max[3][A_WARPS];
-  __shared__ long long s_scan[A_WARPS];
-  __shared__ int s_find[2];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool is_v = part & 1;
   const int g0 = (part >> 1) * heads_a_cta, g1 = min(g0 + heads_a_cta, v.kv_heads);
 
-  // ---- which page: the unit-th of those that the sequences touch
+  // ---- which page: the slot-th that the sequence's rows go to, if it has so many
   int b = unit, slot = 0;
   if (v.row_start) {
-    const int run = (v.num_seqs + A_THREADS - 1) / A_THREADS;
-    const int b0 = min((int)threadIdx.x * run, v.num_seqs), b1 = min(b0 + run, v.num_seqs);
-    long long mine = 0;
-    for (int i = b0; i < b1; ++i) mine += pages_touched(v, i);
-    long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    if (lane == 31) s_scan[warp] = inc;
-    if (threadIdx.x == 0) s_find[0] = -1;
-    __syncthreads();
-    long long at = inc - mine;
-    for (int w = 0; w < warp; ++w) at += s_scan[w];
-    if (at <= unit && unit < at + mine) {
-      int i = b0;
-      for (int n; i + 1 < b1 && at + (n = pages_touched(v, i)) <= unit; ++i) at += n;
-      s_find[0] = i;
-      s_find[1] = unit - (int)at;
-    }
-    __syncthreads();
-    b = s_find[0];
-    slot = s_find[1];
+    b = kv8_last_sequence(v, [&](int i) { return first_append_unit(v, i) <= unit; });
+    slot = unit - first_append_unit(v, b);
+    // every length and range is looked at, also one that no unit is found by
+    if (part == 0 && unit < v.num_seqs && threadIdx.x == 0) kv8_len(v, unit), kv8_rows(v, unit);
   }
-  // (the grid is for the most pages that the rows can touch: there may be none)
-  const int len = b < 0 ? 0 : kv8_len(v, b);
-  const Kv8Span span = b < 0 ? Kv8Span{0, 0} : kv8_rows(v, b);
+  const int len = kv8_len(v, b);
+  const Kv8Span span = kv8_rows(v, b);
   const int first = len - span.n;  // position of row r0; rows of negative positions are skipped
   const int index = (max(first, 0) >> v.page_shift) + slot;
-  if (span.n == 0 || len == 0 || index > (len - 1) >> v.page_shift) return;
+  if (slot < 0 || span.n == 0 || len == 0 || index > (len - 1) >> v.page_shift) return;
   const int page = v.table[(size_t)b * v.table_ld + index];  // (looked at when the first rows are on their way)
 
   const int page0 = index << v.page_shift;
@@ -323,7 +303,7 @@ int heads_a_cta(long long units, int kv_heads, int most) {
 
 template <typename T, int D>
 cudaError_t append_shape(const Kv8View& v, const void* k, const void* vv, long long ld, cudaStream_t s) {
-  // the most pages that the rows can touch
+  // the most pages that the rows can touch (first_append_unit)
   const long long pages = v.row_start ? (v.num_rows >> v.page_shift) + 2ll * v.num_seqs : v.num_seqs;
   const int heads = heads_a_cta(pages, v.kv_heads, 12);
   cudaLaunchConfig_t cfg = {};

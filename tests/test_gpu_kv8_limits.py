@@ -292,3 +292,48 @@ def test_every_operator_on_pages_past_4_gib(q):
             assert not cache.k_scale[:first].any() and not cache.v_scale[:first].any()
     for big, small in zip(*results):
         assert torch.equal(big, small)
+
+
+# ---------------------------------------------------------------- appends to many sequences
+@pytest.mark.parametrize("tokens,before", [(32, 0), (64, 3), (32, 100)])
+def test_append_to_many_ragged_sequences(q, tokens, before):
+    # rows over up to four pages, sequences without rows or positions, packed rows ahead of the first sequence's
+    rng = np.random.default_rng(tokens + before)
+    lens = rng.integers(0, 200, 1500)
+    rows = np.where(rng.random(1500) < 0.3, 0, np.minimum(rng.integers(0, 100, 1500), lens))
+    rows[7] = lens[7] + 5  # more rows than positions
+    c = Case(list(lens), 1, 64, tokens, seed=100).on_gpu(q)
+    start = starts(rows) + np.int32(before)
+    x = [c.rng.normal(size=(int(start[-1]) + 9, 64)).astype(np.float32) for _ in range(2)]
+    q.apr_kv8_append(c.cache, c.gtable, c.glens, *(torch.from_numpy(a).cuda() for a in x), row_start=torch.from_numpy(start).cuda())
+    q.apr_stream_status()
+    c.assert_cache(oracle.kv8_append(c.host, c.table, c.lens, start, *x))
+
+
+def test_the_time_of_an_append_does_not_grow_with_the_square_of_the_sequences(q):
+    # 2 rows of each of 8000 sequences take no more than twice as long as one of each of 16000: 6 times where each CTA looks at all
+    cache = q.Kv8Cache.allocate(16000, 8, 64, 32)
+    table = torch.arange(16000, dtype=torch.int32, device="cuda").view(16000, 1)
+    lens = torch.full((16000,), 20, dtype=torch.int32, device="cuda")
+    x = torch.randn((16000, 8 * 64), device="cuda")
+    start = torch.arange(0, 16001, 2, dtype=torch.int32, device="cuda")
+    two = us_of(lambda: q.apr_kv8_append(cache, table[:8000], lens[:8000], x, x, row_start=start))
+    one = us_of(lambda: q.apr_kv8_append(cache, table, lens, x, x))
+    q.apr_stream_status()
+    assert two <= 2 * one, (two, one)
+
+
+@pytest.mark.parametrize("what", ["length", "row_start", "max_rows"])
+def test_append_looks_at_every_sequence(q, what):
+    # the last of 300 sequences, one without rows, says something that cannot be
+    c = Case([10] * 300, 1, 64, 32, seed=101).on_gpu(q)
+    start, more = torch.from_numpy(starts([2] * 299 + [0])).cuda(), {}
+    if what == "length":
+        c.glens[299] = 1 << 20
+    elif what == "row_start":
+        start[300] = 597
+    else:
+        more = {"max_rows": 1}
+    x = torch.ones((598, 64), device="cuda")
+    q.apr_kv8_append(c.cache, c.gtable, c.glens, x, x, row_start=start, **more)
+    bad_index(q)
