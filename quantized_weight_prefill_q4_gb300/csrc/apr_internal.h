@@ -213,6 +213,7 @@ struct Kv8Attention {
   float* weights;  // nullptr: not wanted
   long long weights_ld;
   int accumulate;
+  int tile_rows;  // rows of a sequence that the tiles are chosen for: the most, or about as many where that is not known
 };
 size_t kv8_attention_scratch(const Kv8View& v, const Kv8Attention& a);
 cudaError_t launch_kv8_attention(const Kv8View& v, const Kv8Attention& a, void* scratch, cudaStream_t s);

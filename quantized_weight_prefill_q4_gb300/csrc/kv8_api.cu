@@ -238,7 +238,8 @@ int run_attention(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int type
   if (rc != APR_OK) return rc;
   if (w.num_rows == 0) return launched(cudaMemsetAsync(weights, 0, wb, s), "attention");  // no row, no weight
   const Kv8Attention a{type,  q,       out,        ldq,       ldo, num_heads, scale > 0.f ? scale : 1.f / std::sqrt((float)w.dim),
-                       weights, weights_ld, accumulate != 0};
+                       weights, weights_ld, accumulate != 0,
+                       rows->row_start && !rows->max_rows ? (w.num_rows + w.num_seqs - 1) / w.num_seqs : w.max_rows};
   const StreamOrder order(s);
   void* scratch = nullptr;
   rc = kv8_scratch(s, kv8_attention_scratch(w, a), &scratch);

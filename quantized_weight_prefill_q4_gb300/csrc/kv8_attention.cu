@@ -242,14 +242,16 @@ __device__ __forceinline__ void finish4(const AttnArgs& a, int r0, int n, int g,
 // so that a segment of two costs about 1.5 of one (16 pairs over 4 x 60000
 // positions of 128 dims: 112 us, 140 as two segments; 18 pairs over 4 x 8000 of
 // 64: 32 us, 29 as three). Only up to 128 dims, where the registers hold the sums
-// of 16 pairs. (The warps of a CTA sharing tiles between them, 8 pairs each, took
-// longer than more segments for any number of pairs: 152 us for the 16.)
+// of 16 pairs. Where max_rows is left out the mean of the rows decides, not all of
+// the call's (48 ragged sequences of one row: 46 us, 65 with two tiles). (The warps
+// of a CTA sharing tiles between them, 8 pairs each, took longer than more segments
+// for any number of pairs: 152 us for the 16.)
 __host__ __device__ constexpr int m_tiles(int dim, long long pairs) {
   return dim <= 128 && (pairs + 15) / 16 * 3 < (pairs + 7) / 8 * 2 ? 2 : 1;
 }
 
-// CTAs of 4 warps on an SM, as registers (168 a thread, 255) and shared memory
-// allow. (At 128 dims 16 warps of 128 registers took 96 us for 4 sequences of
+// CTAs of 4 warps on an SM, as registers (168 a thread, 255; 16 to 68 bytes of them
+// spilled, but for 64 dims and one M tile) and shared memory allow. (At 128 dims 16 warps of 128 registers took 96 us for 4 sequences of
 // 60000 where 12 take 83.)
 constexpr int WARPS = 4;
 constexpr int THREADS = 32 * WARPS;
@@ -839,7 +841,7 @@ int scores_ld(const Kv8View& v) { return (int)(((long long)v.max_len + TILE - 1)
 Layout layout_of(const Kv8View& v, const Kv8Attention& a) {
   Layout l;
   const int group = a.heads / v.kv_heads;
-  l.mt = m_tiles(v.dim, (long long)v.max_rows * group);
+  l.mt = m_tiles(v.dim, (long long)a.tile_rows * group);
   const int pairs = 8 * l.mt, most_ctas = ctas_per_sm(v.dim, l.mt) * num_sms();  // those that run at once
   const long long segs = ((long long)v.num_rows * group / pairs + v.num_seqs) * v.kv_heads;  // at most
   const long long most = segs * (v.max_len / UNIT + 1 + overhead_units(v.dim));
@@ -916,7 +918,7 @@ cudaError_t launch_kv8_attention(const Kv8View& v, const Kv8Attention& in, void*
   a.pairs = 8 * l.mt;
   a.scale_log2 = in.scale * 1.4426950408889634f;
   a.ctas = l.ctas;
-  const bool one_segment = (long long)v.max_rows * a.group <= a.pairs;  // of a KV head
+  const bool one_segment = (long long)in.tile_rows * a.group <= a.pairs;  // of a KV head
   a.whole = (long long)v.max_len * v.dim <= (in.weights && one_segment && v.dim < 256 ? WHOLE_SIZE_WEIGHTED : WHOLE_SIZE);
   a.prefix = reinterpret_cast<int*>(base + l.prefix);
   a.part_ml = reinterpret_cast<float2*>(base + l.part_ml);

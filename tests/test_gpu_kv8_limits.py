@@ -337,3 +337,20 @@ def test_append_looks_at_every_sequence(q, what):
     x = torch.ones((598, 64), device="cuda")
     q.apr_kv8_append(c.cache, c.gtable, c.glens, x, x, row_start=start, **more)
     bad_index(q)
+
+
+@pytest.mark.parametrize("heads,group,dim,rows", [(8, 4, 128, 1), (8, 2, 64, 3)])
+def test_max_rows_left_out_costs_no_time(q, heads, group, dim, rows):
+    # the same rows of each sequence: the tiles are those that max_rows gives (1.3 times as long with those for all rows)
+    count, tokens = 48, 6000
+    cache = q.Kv8Cache.allocate(count * 94, heads, dim, 64)
+    table = torch.arange(count * 94, dtype=torch.int32, device="cuda").view(count, 94)
+    lens = torch.full((count,), tokens, dtype=torch.int32, device="cuda")
+    x = torch.randn((rows * count, heads * group * dim), device="cuda")
+    start = torch.arange(0, rows * count + 1, rows, dtype=torch.int32, device="cuda")
+    outs = [torch.empty_like(x) for _ in range(2)]
+    given, left_out = (us_of(lambda: q.apr_kv8_attention(cache, table, lens, x, o, heads * group, row_start=start, max_rows=m), 15)
+                       for o, m in zip(outs, (rows, 0)))
+    q.apr_stream_status()
+    assert left_out <= 1.15 * given, (left_out, given)
+    assert torch.equal(*outs)
