@@ -49,10 +49,10 @@
 // The softmax works in base 2.
 //
 // Measured (GB300, back to back in a graph): 48 sequences of 130 to 9000 tokens,
-// 32 heads over 8 of 128: 43.5 us, 207 MB (0.71 of the HBM rate); 3 of 100000 to
-// 131000, 16 over 4 of 256: 116 us (0.90); one of 700: 8.5 us; with weights 16 of
-// 2000 to 12000, 32 over 4 of 128: 30 us, and 9 rows of each of 4 of 5000 to 8200,
-// 16 over 8 of 64: 26.5 us. Of the 43.5 us the tiles stream at 6.3 TB/s for 33;
+// 32 heads over 8 of 128: 45 us, 207 MB (0.69 of the HBM rate); 3 of 100000 to
+// 131000, 16 over 4 of 256: 119 us (0.88), one of 700: 10.7 us; with weights 16 of
+// 2000 to 12000, 32 over 4 of 128: 31 us, and 9 rows of each of 4 of 5000 to 8200,
+// 16 over 8 of 64: 28 us. Of the 45 us the tiles stream at 6.3 TB/s for 33;
 // the rest is the way to the first codes (length, table, codes: 3 us), CTAs of
 // equal shares that end up to 5 us apart, and the combination (3 us). The 9 rows
 // (18 pairs) are bound by the warps' instructions, 330 a tile and 8 pairs.
