@@ -867,7 +867,9 @@ cudaError_t launch_finish(const AttnArgs& a, cudaLaunchConfig_t cfg) {
   const long long pairs = (long long)a.v.num_rows * a.heads;  // (below 2^30: the arguments are checked for the units they make)
   const long long combine = a.whole ? 0 : (pairs + a.v.num_seqs - 1) / a.v.num_seqs;
   const long long span = a.weights ? (a.accumulate ? a.v.max_len : a.weights_ld) : 0;
-  cfg.gridDim = dim3((unsigned)(combine + (span + 4 * N - 1) / (4 * N) * a.v.kv_heads), (unsigned)a.v.num_seqs);
+  const long long ctas = combine + (span + 4 * N - 1) / (4 * N) * a.v.kv_heads;
+  if (ctas == 0) return cudaSuccess;  // weights added up over tables of no pages
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)a.v.num_seqs);
   cfg.blockDim = dim3(N);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, kv8_finish_kernel<D, GROUPS>, a, (int)combine);

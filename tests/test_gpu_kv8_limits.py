@@ -81,7 +81,7 @@ def test_ragged_rows_over_a_wide_table(q, dim, heads, group, max_rows):
 
 
 def test_thousands_of_sequences_find_their_rows(q):
-    # three rounds of the search by 32, over ranges of rows that begin at the same place
+    # more sequences than one round of the search looks at, ranges of rows that begin at the same place
     rng = np.random.default_rng(61)
     lens = rng.integers(0, 40, 2100)
     rows = np.minimum(rng.integers(0, 3, 2100), lens)
@@ -354,3 +354,21 @@ def test_max_rows_left_out_costs_no_time(q, heads, group, dim, rows):
     q.apr_stream_status()
     assert left_out <= 1.15 * given, (left_out, given)
     assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_tables_of_no_pages(q, accumulate):
+    # two slots that hold nothing yet: every operator runs, rows read as zeros, weights stay or are zeros
+    cache = q.Kv8Cache.allocate(4, 2, 64, 32)
+    table, lens = torch.empty((2, 0), dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    k, v, x = (torch.ones((2, n * 64), device="cuda") for n in (2, 2, 4))
+    out, kb, vb, w = torch.ones_like(x), torch.ones_like(k), torch.ones_like(v), torch.full((2, 2, 7), 3.0, device="cuda")
+    q.apr_kv8_append(cache, table, lens, k, v)
+    q.apr_kv8_read(cache, table, lens, kb, vb)
+    q.apr_kv8_attention(cache, table, lens, x, out, 4, weights=w, accumulate=accumulate)
+    table_out, lens_out = torch.empty_like(table), torch.ones_like(lens)
+    kept, wo = torch.ones((2, 2, 5), dtype=torch.int32, device="cuda"), torch.ones((2, 2, 5), device="cuda")
+    q.apr_kv8_evict(cache, table, lens, w, 5, 2, torch.zeros((2, 1), dtype=torch.int32, device="cuda"), table_out, lens_out, wo, kept)
+    q.apr_stream_status()
+    assert not any(bool(t.any()) for t in (out, kb, vb, lens_out, wo, cache.K, cache.V, cache.k_scale, cache.v_scale))
+    assert bool((kept == -1).all()) and bool((w == (3.0 if accumulate else 0.0)).all())
