@@ -7,6 +7,8 @@
  *   apr_kv8_read       gives rows of the cache back as numbers
  *   apr_kv8_attention  causal attention of each sequence's last rows over its
  *                      cache, and the weight that each position received
+ *   apr_kv8_prefill_attention
+ *                      the same attention (no weights) of chunks of rows
  *   apr_kv8_evict      keeps the positions of the largest weights and the most
  *                      recent ones, in fresh pages
  *
@@ -121,8 +123,7 @@ int apr_kv8_read(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int type,
  *   rows     a few for each sequence is what this is for (a decode step, a draft
  *            of several tokens, the last rows of a prompt that rate its
  *            positions): each further 8 (row, head) pairs of a KV head cost about
- *            as much again. Chunks of hundreds of rows: apr_kv8_read, then
- *            apr_prefill_attention.
+ *            as much again. Chunks of more rows: apr_kv8_prefill_attention.
  *   weights  NULL, or [num_seqs][num_kv_heads][weights_ld] float32: the weight
  *            that each position received, w_j = sum over the sequence's rows
  *            and the query heads of group g of p_j. accumulate == 0: positions
@@ -151,6 +152,25 @@ int apr_kv8_read(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int type,
 int apr_kv8_attention(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int type, const void* q, long long ldq,
                       void* out, long long ldo, int num_heads, float scale, float* weights, long long weights_ld,
                       int accumulate, apr_stream_t stream);
+
+/*
+ * Attention of chunks of rows over their sequences' caches (which hold the rows'
+ * own k and v already): what apr_kv8_attention says of out, q, scale, rows that see no
+ * position and rows with a NaN or an infinity, for prompts read in
+ * chunks and batches of chunks and single tokens, any number of rows of each
+ * sequence. The (row, head) pairs of a KV head are the 128 rows of a tensor-core
+ * tile, the codes enter the products exactly (fp16), every sum is float32.
+ *   float32 rows  q is split into two fp16 pieces (22 bits of the row's largest
+ *                 magnitude), the softmax weights likewise
+ *   fp16, bf16    q enters as one fp16 row (scaled by a power of two: all bits
+ *                 of values within 2^-14 of the row's largest), the softmax weights rounded
+ *                 to fp16
+ * out must not overlap q or the cache. Scratch per stream: partial results of
+ * the tiles that several CTAs share (at most 86 MB).
+ */
+int apr_kv8_prefill_attention(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int type, const void* q,
+                              long long ldq, void* out, long long ldo, int num_heads, float scale,
+                              apr_stream_t stream);
 
 /*
  * Eviction. A sequence of more than `budget` positions is cut to budget, for

@@ -43,3 +43,7 @@ from .kv8ref import (  # noqa: F401
     kv8_scale,
     kv8_values,
 )
+from .roperef import (  # noqa: F401
+    rope_rows,
+    rope_table,
+)

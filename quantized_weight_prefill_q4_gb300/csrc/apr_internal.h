@@ -217,8 +217,22 @@ struct Kv8Attention {
 };
 size_t kv8_attention_scratch(const Kv8View& v, const Kv8Attention& a);
 cudaError_t launch_kv8_attention(const Kv8View& v, const Kv8Attention& a, void* scratch, cudaStream_t s);
+// Chunks of rows (kv8_prefill.cu); its scratch: kv8_prefill_scratch.
+size_t kv8_prefill_scratch(const Kv8View& v, int type, int heads);
+cudaError_t launch_kv8_prefill(const Kv8View& v, int type, const void* q, long long ldq, void* out, long long ldo,
+                               int heads, float scale, void* scratch, cudaStream_t s);
 cudaError_t launch_kv8_evict(const Kv8View& v, const float* weights, long long weights_ld, int budget, int recent,
                              const int* fresh, int* table_out, int* lens_out, float* weights_out,
                              long long weights_out_ld, int* kept, cudaStream_t s);
+
+// Rotations by position (rope.cu, rope_append.cu): include/apr_rope.h; launched as
+// the cache's kernels are.
+struct RopeView;
+struct RopeRows;
+cudaError_t launch_rope_table(const float* inv_freq, int pairs, long long first, long long positions, double scale,
+                              float* table, cudaStream_t s);
+cudaError_t launch_rope_rows(const RopeView& r, const RopeRows& a, int type, cudaStream_t s);
+cudaError_t launch_rope_kv8_append(const Kv8View& v, const RopeView& r, int type, const void* k, const void* vv,
+                                   long long ld, const float* k_norm, float eps, const RopeRows& q, cudaStream_t s);
 
 }  // namespace apr

@@ -1,5 +1,5 @@
-// C ABI of the 8-bit paged KV cache (include/apr_kv8.h): argument checks,
-// scratch, launches.
+// C ABI of the 8-bit paged KV cache (include/apr_kv8.h) and of the rotations by
+// position (include/apr_rope.h): argument checks, scratch, launches.
 
 #include <cmath>
 #include <cstdint>
@@ -8,7 +8,9 @@
 
 #include "apr_internal.h"
 #include "apr_kv8.h"
+#include "apr_rope.h"
 #include "kv8.cuh"
+#include "rope.cuh"
 
 using namespace apr;
 
@@ -37,6 +39,16 @@ struct Range {
 // Elements of `count` rows of `width` every `ld`.
 size_t span_of(long long count, long long ld, long long width) {
   return count > 0 ? (size_t)(count - 1) * (size_t)ld + (size_t)width : 0;
+}
+
+// Whether `count` rows of wa bytes every lda from a and as many of wb bytes every ldb from b meet. Of one distance
+// they may be slices of one buffer, rows that interleave; of two, their whole ranges count.
+bool rows_meet(const void* a, size_t lda, size_t wa, const void* b, size_t ldb, size_t wb, long long count) {
+  if (!meet(a, span_of(count, lda, wa), b, span_of(count, ldb, wb))) return false;
+  if (lda != ldb) return true;
+  const bool a_first = (uintptr_t)a <= (uintptr_t)b;
+  const size_t off = (a_first ? (uintptr_t)b - (uintptr_t)a : (uintptr_t)a - (uintptr_t)b) % lda;
+  return off < (a_first ? wa : wb) || lda - off < (a_first ? wb : wa);
 }
 
 // Checks the cache and the rows, and fills the kernels' view of them. Returns
@@ -133,6 +145,25 @@ int check_rows(const Kv8View& v, int type, const void* k, const void* vv, long l
   return APR_OK;
 }
 
+// The q rows and outputs of the attentions.
+int check_heads(const Kv8View& w, int type, const void* q, long long ldq, const void* out, long long ldo, int num_heads,
+                float scale) {
+  const int size = type_size(type);
+  if (!size) return failf(APR_E_INVAL, "unknown element type %lld", type);
+  if (num_heads <= 0 || num_heads > 65536 || num_heads % w.kv_heads != 0)
+    return failf(APR_E_INVAL, "num_heads (%lld) must be a multiple of num_kv_heads (%lld), at most 65536", num_heads,
+                 w.kv_heads);
+  const long long width = (long long)num_heads * w.dim;
+  if (ldq < width || ldo < width || ldq > (1LL << 28) || ldo > (1LL << 28))
+    return failf(APR_E_INVAL, "ldq=%lld and ldo=%lld must be within num_heads * head_dim=%lld and 2^28", ldq, ldo,
+                 width);
+  if (!(scale >= 0.f) || !std::isfinite(scale)) return set_error(APR_E_INVAL, "scale must be finite and not negative");
+  if (w.num_rows > 0 && (!q || !out)) return set_error(APR_E_INVAL, "null q or out");
+  if (!on16(q) || !on16(out) || ldq * size % 16 != 0 || ldo * size % 16 != 0)
+    return failf(APR_E_ALIGN, "the q and out rows (ldq=%lld, ldo=%lld) are not on 16-byte boundaries", ldq, ldo);
+  return APR_OK;
+}
+
 int launched(cudaError_t e, const char* what) {
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e == cudaSuccess) return APR_OK;
@@ -172,10 +203,7 @@ int run_read(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int type, voi
   if (rc != APR_OK) return rc;
   const size_t width = (size_t)w.kv_heads * w.dim, size = type_size(type);
   const size_t bytes = span_of(w.num_rows, ld, width) * size;
-  // k and v may be slices of one buffer: rows that interleave, apart by less than ld
-  const ptrdiff_t apart = (const char*)v - (const char*)k;
-  const size_t gap = (size_t)(apart < 0 ? -apart : apart);
-  if (gap < bytes && (gap % (ld * size) < width * size || ld * size - gap % (ld * size) < width * size))
+  if (rows_meet(k, ld * size, width * size, v, ld * size, width * size, w.num_rows))
     return set_error(APR_E_ALIAS, "k overlaps v");
   const size_t cb = code_bytes(w), sb = scale_bytes(w);
   const Range ins[] = {{w.K, cb, "K"},
@@ -201,25 +229,16 @@ int run_attention(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int type
   Kv8View w;
   int rc = view_of(cache, rows, true, weights && !accumulate, &w);
   if (rc != APR_OK) return rc == 1 ? APR_OK : rc;
+  rc = check_heads(w, type, q, ldq, out, ldo, num_heads, scale);
+  if (rc != APR_OK) return rc;
   const int size = type_size(type);
-  if (!size) return failf(APR_E_INVAL, "unknown element type %lld", type);
-  if (num_heads <= 0 || num_heads > 65536 || num_heads % w.kv_heads != 0)
-    return failf(APR_E_INVAL, "num_heads (%lld) must be a multiple of num_kv_heads (%lld), at most 65536", num_heads,
-                 w.kv_heads);
   const long long width = (long long)num_heads * w.dim;
-  if (ldq < width || ldo < width || ldq > (1LL << 28) || ldo > (1LL << 28))
-    return failf(APR_E_INVAL, "ldq=%lld and ldo=%lld must be within num_heads * head_dim=%lld and 2^28", ldq, ldo,
-                 width);
-  if (!(scale >= 0.f) || !std::isfinite(scale)) return set_error(APR_E_INVAL, "scale must be finite and not negative");
   if (weights && (weights_ld < w.max_len || weights_ld > (1LL << 30)))
     return failf(APR_E_INVAL, "weights_ld=%lld must be within max_len=%lld and 2^30", weights_ld, w.max_len);
   // units of work of the kernel, counted in 32 bits (64 positions of 8 pairs of row and head)
   const long long segs = ((long long)w.num_rows * (num_heads / w.kv_heads) / 8 + w.num_seqs) * w.kv_heads;
   if (segs * (w.max_len / 64 + 10) > (1LL << 30) || (weights_ld / 128 + 1) * w.kv_heads > (1LL << 30))
     return set_error(APR_E_INVAL, "sizes beyond the supported limits");
-  if (w.num_rows > 0 && (!q || !out)) return set_error(APR_E_INVAL, "null q or out");
-  if (!on16(q) || !on16(out) || ldq * size % 16 != 0 || ldo * size % 16 != 0)
-    return failf(APR_E_ALIGN, "the q and out rows (ldq=%lld, ldo=%lld) are not on 16-byte boundaries", ldq, ldo);
   if (!on4(weights)) return set_error(APR_E_ALIGN, "weights are not 4-byte aligned");
   const size_t cb = code_bytes(w), sb = scale_bytes(w);
   const size_t wb = weights ? ((size_t)w.num_seqs * w.kv_heads * weights_ld) * 4 : 0;
@@ -245,6 +264,184 @@ int run_attention(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int type
   rc = kv8_scratch(s, kv8_attention_scratch(w, a), &scratch);
   if (rc != APR_OK) return rc;
   return launched(launch_kv8_attention(w, a, scratch, s), "attention");
+}
+
+int run_prefill_attention(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int type, const void* q, long long ldq,
+                          void* out, long long ldo, int num_heads, float scale, cudaStream_t s) {
+  Kv8View w;
+  int rc = view_of(cache, rows, true, false, &w);
+  if (rc != APR_OK) return rc == 1 ? APR_OK : rc;
+  rc = check_heads(w, type, q, ldq, out, ldo, num_heads, scale);
+  if (rc != APR_OK) return rc;
+  // what the tiles are worth is counted in 64 bits
+  if ((double)w.num_rows * num_heads * ((double)w.max_len + 4096.) > 0x1p60 || (long long)w.num_rows * num_heads > (1LL << 32))
+    return set_error(APR_E_INVAL, "sizes beyond the supported limits");
+  const size_t size = type_size(type), width = (size_t)num_heads * w.dim, cb = code_bytes(w), sb = scale_bytes(w);
+  const Range outs[] = {{out, span_of(w.num_rows, ldo, width) * size, "out"}};
+  const Range ins[] = {{q, span_of(w.num_rows, ldq, width) * size, "q"},
+                       {w.K, cb, "K"},
+                       {w.V, cb, "V"},
+                       {w.k_scale, sb, "k_scale"},
+                       {w.v_scale, sb, "v_scale"},
+                       {w.table, table_bytes(w), "page_table"},
+                       {w.lens, (size_t)w.num_seqs * 4, "lens"},
+                       {w.row_start, start_bytes(w), "row_start"}};
+  rc = check_overlap(outs, ins);
+  if (rc != APR_OK) return rc;
+  rc = device_status_word(&w.status);
+  if (rc != APR_OK) return rc;
+  const StreamOrder order(s);
+  void* scratch = nullptr;
+  rc = kv8_scratch(s, kv8_prefill_scratch(w, type, num_heads), &scratch);
+  if (rc != APR_OK) return rc;
+  return launched(launch_kv8_prefill(w, type, q, ldq, out, ldo, num_heads, scale > 0.f ? scale : 1.f / std::sqrt((float)w.dim),
+                                     scratch, s),
+                  "prefill attention");
+}
+
+// ---------------------------------------------------------------- rotations
+// Checks a rotation for `rows` rows of heads of `dim`, and fills the kernels' view of it.
+int rope_view(const apr_rope* r, int dim, int rows, bool needs_positions, RopeView* w) {
+  if (!r) return set_error(APR_E_INVAL, "null rope");
+  if (r->rot_dim < 8 || r->rot_dim % 8 != 0 || r->rot_dim > dim)
+    return failf(APR_E_INVAL, "rot_dim=%lld must be a multiple of 8 within the head's %lld dims", r->rot_dim, dim);
+  if (r->num_positions < 1 || r->num_positions > (1 << 30))
+    return failf(APR_E_INVAL, "num_positions=%lld must be within 1 and 2^30", r->num_positions);
+  if (r->num_axes < 1 || r->num_axes > 16 || (r->num_axes > 1 && !r->pair_axis))
+    return failf(APR_E_INVAL, "num_axes=%lld must be within 1 and 16, and 1 without pair_axis", r->num_axes);
+  if (r->positions_ld != 0 && r->positions_ld < rows)
+    return failf(APR_E_INVAL, "positions_ld=%lld is less than the call's %lld rows", r->positions_ld, rows);
+  if (!r->table) return set_error(APR_E_INVAL, "null table");
+  if (!r->positions && (needs_positions || r->num_axes > 1))
+    return set_error(APR_E_INVAL, "null positions");
+  if (!on16(r->table)) return set_error(APR_E_ALIGN, "the table is not 16-byte aligned");
+  if (!on4(r->positions) || !on4(r->pair_axis))
+    return set_error(APR_E_ALIGN, "positions or pair_axis are not 4-byte aligned");
+  *w = RopeView{reinterpret_cast<const float2*>(r->table), r->pair_axis, r->positions, r->positions_ld ? r->positions_ld : rows,
+                nullptr, r->num_positions, r->rot_dim / 2, r->num_axes, r->interleaved != 0};
+  return APR_OK;
+}
+size_t rope_table_bytes(const RopeView& w) { return (size_t)w.num_positions * w.pairs * 8; }
+size_t rope_positions_bytes(const RopeView& w, int rows) {
+  return w.positions ? span_of(w.num_axes, w.positions_ld, rows) * 4 : 0;
+}
+
+// The rows x and out of heads that are rotated: sizes, alignment, and that out is x itself or does not meet it.
+int check_rope_rows(int size, const void* x, long long ldx, const void* out, long long ldo, int rows, long long width,
+                    const char* what) {
+  if (ldx < width || ldo < width || ldx > (1LL << 28) || ldo > (1LL << 28))
+    return failf(APR_E_INVAL, "row strides %lld and %lld must be within the rows' %lld elements and 2^28", ldx, ldo, width);
+  if (!x || !out) return set_error(APR_E_INVAL, "null rows");
+  if (!on16(x) || !on16(out) || ldx * size % 16 != 0 || ldo * size % 16 != 0)
+    return failf(APR_E_ALIGN, "the rows (strides %lld, %lld) are not on 16-byte boundaries", ldx, ldo);
+  if (!(x == out && (ldx == ldo || rows <= 1)) && rows_meet(x, ldx * size, width * size, out, ldo * size, width * size, rows))
+    return set_error(APR_E_ALIAS, what);
+  return APR_OK;
+}
+int check_norm(const float* norm, float eps) {
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return set_error(APR_E_INVAL, "eps must be finite and not negative");
+  if (!on16(norm)) return set_error(APR_E_ALIGN, "the norm's weights are not 16-byte aligned");
+  return APR_OK;
+}
+
+int run_rope_table(const float* inv_freq, int pairs, long long first, long long positions, double scale, float* table,
+                   cudaStream_t s) {
+  if (pairs < 1 || pairs > 256) return failf(APR_E_INVAL, "pairs=%lld must be within 1 and 256", pairs);
+  if (first < 0 || positions < 0 || first > (1LL << 30) || positions > (1LL << 30) - first || positions * pairs > (1LL << 32))
+    return failf(APR_E_INVAL, "positions %lld and %lld more are beyond 2^30, or 2^32 values", first, positions);
+  if (!std::isfinite(scale)) return set_error(APR_E_INVAL, "scale must be finite");
+  if (positions == 0) return APR_OK;
+  if (!inv_freq || !table) return set_error(APR_E_INVAL, "null inv_freq or table");
+  if (!on16(table) || !on4(inv_freq)) return set_error(APR_E_ALIGN, "the table is not 16-byte, or inv_freq not 4-byte aligned");
+  if (meet(inv_freq, (size_t)pairs * 4, table, (size_t)positions * pairs * 8))
+    return set_error(APR_E_ALIAS, "table overlaps inv_freq");
+  unsigned* status;
+  const int rc = device_status_word(&status);
+  if (rc != APR_OK) return rc;
+  return launched(launch_rope_table(inv_freq, pairs, first, positions, scale, table, s), "rope table");
+}
+
+int run_rope_rows(const apr_rope* rope, int type, const void* x, long long ldx, void* out, long long ldo, int num_rows,
+                  int num_heads, int head_dim, const float* norm, float eps, cudaStream_t s) {
+  const int size = type_size(type);
+  if (!size) return failf(APR_E_INVAL, "unknown element type %lld", type);
+  if (num_rows < 0 || num_rows > (1 << 24) || num_heads < 1 || num_heads > 65536 || (long long)num_rows * num_heads > (1LL << 32))
+    return failf(APR_E_INVAL, "bad sizes: num_rows=%lld num_heads=%lld", num_rows, num_heads);
+  if (head_dim < 8 || head_dim > 512 || head_dim % 8 != 0)
+    return failf(APR_E_INVAL, "head_dim=%lld must be a multiple of 8 within 8 and 512", head_dim);
+  RopeView w;
+  if (num_rows == 0) return APR_OK;
+  int rc = rope_view(rope, head_dim, num_rows, true, &w);
+  if (rc != APR_OK) return rc;
+  rc = check_norm(norm, eps);
+  if (rc != APR_OK) return rc;
+  const long long width = (long long)num_heads * head_dim;
+  rc = check_rope_rows(size, x, ldx, out, ldo, num_rows, width, "out overlaps x without being it");
+  if (rc != APR_OK) return rc;
+  const Range outs[] = {{out, span_of(num_rows, ldo, width) * size, "out"}};
+  const Range ins[] = {{w.table, rope_table_bytes(w), "table"},
+                       {w.axis, w.axis ? (size_t)w.pairs : 0, "pair_axis"},
+                       {w.positions, rope_positions_bytes(w, num_rows), "positions"},
+                       {norm, norm ? (size_t)head_dim * 4 : 0, "norm"}};
+  rc = check_overlap(outs, ins);
+  if (rc != APR_OK) return rc;
+  rc = device_status_word(&w.status);
+  if (rc != APR_OK) return rc;
+  return launched(launch_rope_rows(w, RopeRows{x, out, ldx, ldo, norm, eps, num_rows, num_heads, head_dim, 0}, type, s), "rope rows");
+}
+
+int run_rope_append(const apr_kv8_cache* cache, const apr_kv8_rows* rows, const apr_rope* rope, int type, const void* k,
+                    const void* v, long long ld, const float* k_norm, const void* q, long long ldq, void* q_out,
+                    long long ldqo, int num_heads, const float* q_norm, float eps, cudaStream_t s) {
+  Kv8View w;
+  int rc = view_of(cache, rows, true, false, &w);
+  if (rc != APR_OK) return rc == 1 ? APR_OK : rc;
+  rc = check_rows(w, type, k, v, ld);
+  if (rc != APR_OK) return rc;
+  RopeView r;
+  rc = rope_view(rope, w.dim, w.num_rows, false, &r);
+  if (rc != APR_OK) return rc;
+  rc = check_norm(k_norm, eps);
+  if (rc == APR_OK) rc = check_norm(q_norm, eps);
+  if (rc != APR_OK) return rc;
+  const size_t size = type_size(type), kv_width = (size_t)w.kv_heads * w.dim;
+  if (!q != !q_out) return set_error(APR_E_INVAL, "q without q_out, or q_out without q");
+  size_t q_width = 0;
+  if (q) {
+    if (num_heads < 1 || num_heads > 65536 || (long long)w.num_rows * num_heads > (1LL << 32))
+      return failf(APR_E_INVAL, "bad num_heads=%lld", num_heads);
+    q_width = (size_t)num_heads * w.dim;
+    rc = check_rope_rows((int)size, q, ldq, q_out, ldqo, w.num_rows, (long long)q_width, "q_out overlaps q without being it");
+    if (rc != APR_OK) return rc;
+    for (const void* p : {k, v})
+      if (rows_meet(q_out, ldqo * size, q_width * size, p, ld * size, kv_width * size, w.num_rows))
+        return set_error(APR_E_ALIAS, "q_out overlaps k or v");
+  }
+  const size_t bytes = span_of(w.num_rows, ld, kv_width) * size, cb = code_bytes(w), sb = scale_bytes(w);
+  const Range outs[] = {{w.K, cb, "K"}, {w.V, cb, "V"}, {w.k_scale, sb, "k_scale"}, {w.v_scale, sb, "v_scale"},
+                        {q_out, q ? span_of(w.num_rows, ldqo, q_width) * size : 0, "q_out"}};
+  const Range ins[] = {{w.table, table_bytes(w), "page_table"},
+                       {w.lens, (size_t)w.num_seqs * 4, "lens"},
+                       {w.row_start, start_bytes(w), "row_start"},
+                       {r.table, rope_table_bytes(r), "table"},
+                       {r.axis, r.axis ? (size_t)r.pairs : 0, "pair_axis"},
+                       {r.positions, rope_positions_bytes(r, w.num_rows), "positions"},
+                       {k_norm, k_norm ? (size_t)w.dim * 4 : 0, "k_norm"},
+                       {q_norm, q_norm ? (size_t)w.dim * 4 : 0, "q_norm"}};
+  rc = check_overlap(outs, ins);
+  if (rc != APR_OK) return rc;
+  for (const Range in : {Range{k, bytes, "k"}, Range{v, bytes, "v"}, Range{q, q ? span_of(w.num_rows, ldq, q_width) * size : 0, "q"}})
+    for (int i = 0; i < 4; ++i) {  // (q_out has been looked at: rows that interleave)
+      const Range one[] = {outs[i]}, in1[] = {in};
+      rc = check_overlap(one, in1);
+      if (rc != APR_OK) return rc;
+    }
+  rc = device_status_word(&w.status);
+  if (rc != APR_OK) return rc;
+  r.status = w.status;
+  return launched(launch_rope_kv8_append(w, r, type, k, v, ld, k_norm, eps,
+                                         RopeRows{q, q_out, ldq, ldqo, q_norm, eps, w.num_rows, q ? num_heads : 0, w.dim, 0}, s),
+                  "rotating append");
 }
 
 int run_evict(const apr_kv8_cache* cache, const apr_kv8_rows* rows, const float* weights, long long weights_ld,
@@ -321,6 +518,36 @@ int apr_kv8_attention(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int 
   return guarded([&] {
     return run_attention(cache, rows, type, q, ldq, out, ldo, num_heads, scale, weights, weights_ld, accumulate,
                          (cudaStream_t)stream);
+  });
+}
+
+int apr_kv8_prefill_attention(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int type, const void* q,
+                              long long ldq, void* out, long long ldo, int num_heads, float scale,
+                              apr_stream_t stream) {
+  return guarded([&] {
+    return run_prefill_attention(cache, rows, type, q, ldq, out, ldo, num_heads, scale, (cudaStream_t)stream);
+  });
+}
+
+int apr_rope_table(const float* inv_freq, int pairs, long long first, long long positions, double scale, float* table,
+                   apr_stream_t stream) {
+  return guarded([&] { return run_rope_table(inv_freq, pairs, first, positions, scale, table, (cudaStream_t)stream); });
+}
+
+int apr_rope_rows(const apr_rope* rope, int type, const void* x, long long ldx, void* out, long long ldo, int num_rows,
+                  int num_heads, int head_dim, const float* norm, float eps, apr_stream_t stream) {
+  return guarded([&] {
+    return run_rope_rows(rope, type, x, ldx, out, ldo, num_rows, num_heads, head_dim, norm, eps, (cudaStream_t)stream);
+  });
+}
+
+int apr_rope_kv8_append(const apr_kv8_cache* cache, const apr_kv8_rows* rows, const apr_rope* rope, int type,
+                        const void* k, const void* v, long long ld, const float* k_norm, const void* q, long long ldq,
+                        void* q_out, long long ldqo, int num_heads, const float* q_norm, float eps,
+                        apr_stream_t stream) {
+  return guarded([&] {
+    return run_rope_append(cache, rows, rope, type, k, v, ld, k_norm, q, ldq, q_out, ldqo, num_heads, q_norm, eps,
+                           (cudaStream_t)stream);
   });
 }
 

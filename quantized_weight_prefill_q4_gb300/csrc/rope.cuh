@@ -1,0 +1,240 @@
+// Rotations by position (include/apr_rope.h) as the kernels see them.
+//
+// A head is cut into units of eight dims, one for each lane of a group of lanes: the
+// units below rot / 8 are four pairs (dims 4 u .. and rot / 2 + 4 u .., or 8 u .. in
+// the interleaved order), the others eight dims that pass. A lane keeps its unit over
+// rows and heads, so which table columns, axes and norm weights are its own is settled once.
+#pragma once
+
+#include "kv8.cuh"
+
+namespace apr {
+
+struct RopeView {
+  const float2* table;
+  const uint8_t* axis;    // nullptr: axis 0
+  const int* positions;   // nullptr: the row's position in its sequence
+  long long positions_ld;
+  unsigned* status;
+  int num_positions, pairs, num_axes, interleaved;
+};
+
+// The norm of the heads, and rows into rows.
+struct RopeRows {
+  const void* x;
+  void* out;
+  long long ldx, ldo;
+  const float* norm;  // nullptr: none
+  float eps;
+  int num_rows, heads, dim;
+  int heads_a_group;  // that a group of lanes does of one row
+};
+
+// Unit u of a head: dims d0 .. d0 + 3 and d1 .. d1 + 3.
+struct RopeUnit {
+  int d0, d1, pair;  // its first pair; -1: the dims pass
+  uint32_t axes;     // of its four pairs, a byte each
+};
+__device__ __forceinline__ RopeUnit rope_unit(const RopeView& r, int u) {
+  const bool turned = 4 * u < r.pairs;
+  RopeUnit w;
+  w.pair = turned ? 4 * u : -1;
+  w.d0 = turned && !r.interleaved ? 4 * u : 8 * u;
+  w.d1 = turned && !r.interleaved ? r.pairs + 4 * u : 8 * u + 4;
+  w.axes = turned && r.axis ? *reinterpret_cast<const uint32_t*>(r.axis + 4 * u) : 0;
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    if ((int)(w.axes >> i & 255) >= r.num_axes) {
+      atomicOr(r.status, kStatusBadIndex);
+      w.axes &= ~(255u << i);
+    }
+  return w;
+}
+
+// The cosines and sines of a unit's pairs for packed row `row`, whose position in
+// its sequence is `own` (what counts where no positions are given).
+struct RopeTurn {
+  float2 t[4];
+};
+__device__ __forceinline__ int rope_position(const RopeView& r, int axis, int row, int own) {
+  const int p = r.positions ? r.positions[axis * r.positions_ld + row] : max(own, 0);
+  if ((unsigned)p < (unsigned)r.num_positions) return p;
+  atomicOr(r.status, kStatusBadIndex);
+  return 0;
+}
+__device__ __forceinline__ RopeTurn rope_turn(const RopeView& r, const RopeUnit& u, int row, int own) {
+  RopeTurn w;
+  if (u.pair < 0) return w;
+  const int a = (int)(u.axes & 255);
+  const float2* at = r.table + (size_t)rope_position(r, a, row, own) * r.pairs + u.pair;
+  if (u.axes == a * 0x01010101u) {
+    const float4 x = reinterpret_cast<const float4*>(at)[0], y = reinterpret_cast<const float4*>(at)[1];
+    w.t[0] = make_float2(x.x, x.y), w.t[1] = make_float2(x.z, x.w);
+    w.t[2] = make_float2(y.x, y.y), w.t[3] = make_float2(y.z, y.w);
+  } else {
+    w.t[0] = at[0];
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+      w.t[i] = r.table[(size_t)rope_position(r, (int)(u.axes >> 8 * i & 255), row, own) * r.pairs + u.pair + i];
+  }
+  return w;
+}
+
+// Every product, sum and difference rounded by itself, whatever the compiler would join.
+__device__ __forceinline__ void rope_pair(float& x, float& y, float2 t) {
+  const float a = __fsub_rn(__fmul_rn(x, t.x), __fmul_rn(y, t.y));
+  y = __fadd_rn(__fmul_rn(y, t.x), __fmul_rn(x, t.y));
+  x = a;
+}
+__device__ __forceinline__ void rope_rotate(const RopeView& r, const RopeUnit& u, const RopeTurn& w, float (&x)[8]) {
+  if (u.pair < 0) return;
+  if (r.interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) rope_pair(x[2 * i], x[2 * i + 1], w.t[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) rope_pair(x[i], x[4 + i], w.t[i]);
+  }
+}
+
+// ---------------------------------------------------------------- the norm
+// A number as the sum of two float32 ones, the second within half a step of the first
+// (Dekker 1971, Knuth's two-sum): some 45 bits.
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return Two{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Two two_add(const Two& a, const Two& b) {
+  const Two s = two_sum(a.hi, b.hi);
+  return Two{s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo))};
+}
+__device__ __forceinline__ Two two_add_square(const Two& a, float x) {
+  const float p = __fmul_rn(x, x);
+  return two_add(a, Two{p, __fmaf_rn(x, x, -p)});
+}
+// f32(1 / sqrt(sum / n + eps)): one step of Newton's from the approximation's 22
+// bits, its residual by fma.
+__device__ __forceinline__ float rope_inverse_rms(const Two& sum, float n, float eps) {
+  const float q = __fdiv_rn(sum.hi, n);
+  const Two m = two_add(Two{q, __fdiv_rn(__fadd_rn(__fmaf_rn(-q, n, sum.hi), sum.lo), n)}, Two{eps, 0.f});
+  const float s = __fadd_rn(m.hi, m.lo), low = __fadd_rn(__fsub_rn(m.hi, s), m.lo);
+  const float y = rsqrtf(s), p = __fmul_rn(y, y), e = __fmaf_rn(y, y, -p);
+  const float t = __fmaf_rn(-s, e, __fmaf_rn(-s, p, 1.f)) - low * p;
+  return __fmaf_rn(__fmul_rn(y, 0.5f), t, y);
+}
+// The sum over a group of LANES neighbouring lanes, for all of them.
+template <int LANES>
+__device__ __forceinline__ Two two_group_sum(Two s) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1)
+    s = two_add(s, Two{__shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o)});
+  return s;
+}
+
+// ---------------------------------------------------------------- elements
+__device__ __forceinline__ Vec8<float> load44(const float* p, int d0, int d1) {
+  return Vec8<float>{*reinterpret_cast<const float4*>(p + d0), *reinterpret_cast<const float4*>(p + d1)};
+}
+template <typename T>
+__device__ __forceinline__ Vec8<T> load44(const T* p, int d0, int d1) {
+  const uint2 a = *reinterpret_cast<const uint2*>(p + d0), b = *reinterpret_cast<const uint2*>(p + d1);
+  return Vec8<T>{make_uint4(a.x, a.y, b.x, b.y)};
+}
+__device__ __forceinline__ void store44(float* p, int d0, int d1, const Vec8<float>& e) {
+  *reinterpret_cast<float4*>(p + d0) = e.a;
+  *reinterpret_cast<float4*>(p + d1) = e.b;
+}
+template <typename T>
+__device__ __forceinline__ void store44(T* p, int d0, int d1, const Vec8<T>& e) {
+  *reinterpret_cast<uint2*>(p + d0) = make_uint2(e.a.x, e.a.y);
+  *reinterpret_cast<uint2*>(p + d1) = make_uint2(e.a.z, e.a.w);
+}
+template <typename T>
+__device__ __forceinline__ Vec8<T> vec8_of(const float (&x)[8]) {
+  if constexpr (sizeof(T) == 4)
+    return Vec8<T>{make_float4(x[0], x[1], x[2], x[3]), make_float4(x[4], x[5], x[6], x[7])};
+  else
+    return Vec8<T>{make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]))};
+}
+
+// Norm and rotation of a unit's values, w its norm weights.
+__device__ __forceinline__ void rope_norm(float (&x)[8], float inv, const float (&w)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], inv), w[i]);
+}
+
+// ---------------------------------------------------------------- rows into rows
+// The row of group `group`, which may be past the last one.
+__device__ __forceinline__ long long rope_row_of(const RopeRows& a, long long group) {
+  return group / ((a.heads + a.heads_a_group - 1) / a.heads_a_group);
+}
+// Group `group` of LANES lanes does heads_a_group heads of one row, EACH units a
+// lane; `lane` within the group; nothing of a row that is not `live`. All lanes of the warp call it.
+template <typename T, int LANES, int EACH>
+__device__ __forceinline__ void rope_rows_group(const RopeView& r, const RopeRows& a, long long group, int lane,
+                                                int own, bool live) {
+  constexpr int BATCH = EACH == 1 ? 4 : 2;  // heads whose values are on their way together
+  const int per_row = (a.heads + a.heads_a_group - 1) / a.heads_a_group;
+  live = live && group / per_row < a.num_rows;
+  const long long row = live ? group / per_row : 0;
+  const int h0 = (int)(group % per_row) * a.heads_a_group, h1 = live ? min(h0 + a.heads_a_group, a.heads) : h0;
+  RopeUnit unit[EACH];
+  RopeTurn turn[EACH];
+  float w[EACH][8];
+  bool mine[EACH];
+#pragma unroll
+  for (int e = 0; e < EACH; ++e) {
+    mine[e] = (lane + e * LANES) * 8 < a.dim && h0 < h1;
+    unit[e] = rope_unit(r, mine[e] ? lane + e * LANES : 0);
+    if (mine[e]) turn[e] = rope_turn(r, unit[e], (int)row, own);
+    if (mine[e] && a.norm) {
+      const Vec8<float> v = load44(a.norm, unit[e].d0, unit[e].d1);
+      values8(v, w[e]);
+    }
+  }
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  T* out = static_cast<T*>(a.out) + row * a.ldo;
+  for (int i = 0; i < a.heads_a_group; i += BATCH) {
+    Vec8<T> v[BATCH][EACH];
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j)
+#pragma unroll
+      for (int e = 0; e < EACH; ++e)
+        if (mine[e] && h0 + i + j < h1) v[j][e] = load44(x + (size_t)(h0 + i + j) * a.dim, unit[e].d0, unit[e].d1);
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) {
+      const int h = h0 + i + j;
+      float y[EACH][8];
+#pragma unroll
+      for (int e = 0; e < EACH; ++e) {
+        if (mine[e] && h < h1) {
+          values8(v[j][e], y[e]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) y[e][k] = 0.f;
+        }
+      }
+      if (a.norm) {
+        Two s = {0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < EACH; ++e)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) s = two_add_square(s, y[e][k]);
+        const float inv = rope_inverse_rms(two_group_sum<LANES>(s), (float)a.dim, a.eps);
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) rope_norm(y[e], inv, w[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < EACH; ++e)
+        if (mine[e] && h < h1) {
+          rope_rotate(r, unit[e], turn[e], y[e]);
+          store44(out + (size_t)h * a.dim, unit[e].d0, unit[e].d1, vec8_of<T>(y[e]));
+        }
+    }
+  }
+}
+
+}  // namespace apr

@@ -20,7 +20,7 @@ APR_T_F16 = 1
 APR_T_BF16 = 30
 
 # Every symbol include/apr_kv8.h declares.
-KV8_EXPORTS = ("apr_kv8_append", "apr_kv8_read", "apr_kv8_attention", "apr_kv8_evict")
+KV8_EXPORTS = ("apr_kv8_append", "apr_kv8_read", "apr_kv8_attention", "apr_kv8_prefill_attention", "apr_kv8_evict")
 
 _I8, _I32, _F32, _Tensor = torch.int8, torch.int32, torch.float32, torch.Tensor
 _raw_stream = torch._C._cuda_getCurrentRawStream
@@ -62,6 +62,7 @@ def _bind():
         "apr_kv8_append": [cache, rows, ci, vp, vp, ll, vp],
         "apr_kv8_read": [cache, rows, ci, vp, vp, ll, vp],
         "apr_kv8_attention": [cache, rows, ci, vp, ll, vp, ll, ci, ctypes.c_float, vp, ll, ci, vp],
+        "apr_kv8_prefill_attention": [cache, rows, ci, vp, ll, vp, ll, ci, ctypes.c_float, vp],
         "apr_kv8_evict": [cache, rows, vp, ll, ci, ci, vp, vp, vp, vp, ll, vp, vp],
     }
     for name, args in sig.items():
@@ -214,6 +215,17 @@ def apr_kv8_attention(cache, page_table, lens, q, out, num_heads, *, row_start=N
         wp = weights.data_ptr()
     return capi._check(_lib.apr_kv8_attention(cache._c, rows, _TYPES[q.dtype], qp, ldq, op, ldo, num_heads, scale, wp,
                                               wld, int(accumulate), _stream(stream, cache.device_index)))
+
+
+def apr_kv8_prefill_attention(cache, page_table, lens, q, out, num_heads, *, row_start=None, max_rows=0, max_len=0,
+                              scale=0.0, stream=None) -> int:
+    """apr_kv8_attention without weights for chunks of rows: any number of packed rows q of each sequence."""
+    width = num_heads * cache.head_dim
+    qp, n, ldq = _matrix(q, "q", width, cache.device_index)
+    op, _, ldo = _matrix(out, "out", width, cache.device_index, like=q)
+    rows = _rows(cache, page_table, lens, row_start, n, max_rows, max_len)
+    return capi._check(_lib.apr_kv8_prefill_attention(cache._c, rows, _TYPES[q.dtype], qp, ldq, op, ldo, num_heads, scale,
+                                                      _stream(stream, cache.device_index)))
 
 
 def apr_kv8_evict(cache, page_table, lens, weights, budget, recent, fresh_pages, table_out, lens_out, weights_out, kept,
