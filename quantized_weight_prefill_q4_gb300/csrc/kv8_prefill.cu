@@ -44,8 +44,7 @@ constexpr int START = 256;       // positions that a segment's start and end are
 constexpr int MIN_TILES = 2;     // of a CTA's share
 constexpr float MOVE = 8.f;
 constexpr int FOLD = 512;        // positions
-constexpr int SOFT_WARPS = 8, CONV_WARPS = 4, MMA_WARP = SOFT_WARPS + CONV_WARPS;  // (one M tile: 4 and 8)
-constexpr int THREADS = 32 * (MMA_WARP + 1);
+constexpr int MMA_WARP = 12, PIECE_WARP = 13, COPY_WARP = 14, THREADS = 512;  // (the last warp has nothing to do)
 
 struct PrefillArgs {
   Kv8View v;
@@ -73,10 +72,17 @@ struct Shape {
   static constexpr int PANEL = KT * 128;                   // bytes of 64 dims of a tile
   static constexpr int SLOT = KT * D * 2;
   static constexpr int Q_BYTES = MT * PIECES * 128 * D * 2;
-  static constexpr int SLOTS_FIT = (226 * 1024 - Q_BYTES) / SLOT;
-  static constexpr int SLOTS = SLOTS_FIT < 6 ? SLOTS_FIT : 6;
-  static constexpr int SMEM = Q_BYTES + SLOTS * SLOT + 1024;
+  // fp16 slots and slots of codes as they lie in memory
+  static constexpr int RAW = KT * D;
+  static constexpr int LEFT = 226 * 1024 - Q_BYTES;
+  static constexpr int SLOTS = LEFT >= 4 * (SLOT + RAW) ? (LEFT / (SLOT + RAW) < 6 ? LEFT / (SLOT + RAW) : 6) : (LEFT >= 3 * (SLOT + RAW) ? 3 : 2);
+  static constexpr int RAWS_FIT = (LEFT - SLOTS * SLOT) / RAW;
+  static constexpr int RAWS = RAWS_FIT < 6 ? RAWS_FIT : 6;
+  static constexpr int SMEM = Q_BYTES + SLOTS * SLOT + RAWS * RAW + 1024;
   static constexpr int SOFT = 4 * MT, CONV = MMA_WARP - SOFT;  // warps
+  // registers a thread of each role; as launched: 128
+  static constexpr int SOFT_REGS = MT == 2 ? 200 : 208, CONV_REGS = MT == 2 ? 56 : 88, MMA_REGS = MT == 2 ? 56 : 128;
+  static_assert(32 * (SOFT * SOFT_REGS + CONV * CONV_REGS + 4 * MMA_REGS) <= THREADS * 128, "registers");
   static constexpr int EACH = KT * D / 16 / (32 * CONV);   // 16-byte pieces of a chunk that a converter thread has
   // tensor memory columns: O of each M tile, then two buffers of scores, then (where there is room) two of weights
   static constexpr int COL_S = MT * D;
@@ -85,7 +91,7 @@ struct Shape {
   static constexpr int COL_P = OWN_P ? COL_S + 2 * KT : COL_S;
   static constexpr int P_STEP = OWN_P ? P_COLS : KT;
   static_assert(COL_S + 2 * KT <= 512 && (OWN_P || !TWO), "tensor memory");
-  static_assert(SLOTS >= 3 && SMEM + 2048 <= 232448, "shared memory");
+  static_assert(SLOTS >= 2 && RAWS >= 2 && SMEM + 1024 <= 232448, "shared memory");
   static_assert(EACH >= 1 && KT * D / 16 % (32 * CONV) == 0, "converters");
   static constexpr int FOLD_TILES = FOLD / KT;
 };
@@ -140,13 +146,13 @@ __device__ __forceinline__ long long share_begin(int c, int ctas, long long tota
   return (long long)((unsigned long long)total / ctas) * c + (long long)((unsigned long long)total % ctas) * c / ctas;
 }
 
+// A piece, as the roles see it: key tiles k0 .. k1 - 1 of the `tiles` of a segment (k1 == 0: no more pieces).
 struct Piece {
-  Work w;
-  int b, g, t;
+  int b, g;          // sequence and KV head
+  int len, first, r0;
+  int k0, k1, tiles;
+  int np;            // pairs of the segment, from p0 of the sequence's on
   long long p0;
-  int np;            // pairs of the segment
-  int k0, k1;        // its key tiles k0 .. k1 - 1
-  int tiles;         // of the segment
 };
 
 // The pieces of a CTA's share, one after the other; a whole warp calls it.
@@ -155,11 +161,12 @@ struct Pieces {
   int b, ctas;
   long long u, end, seq_u0, total;
 
-  __device__ __forceinline__ bool next(const PrefillArgs& a, Piece& p) {
+  // The next piece, and of how many pieces its segment is made where the piece begins it (by CTA c).
+  __device__ bool next(const PrefillArgs& a, int c, Piece& p, int& t, int& made_of) {
     const int lane = threadIdx.x & 31;
     while (u < end && b < a.v.num_seqs) {
-      p.w = work_of<S>(a, b);
-      const long long all = cost_all<S>(a, p.w);
+      const Work w = work_of<S>(a, b);
+      const long long all = cost_all<S>(a, w);
       if (u >= seq_u0 + all) {  // the next sequence that has rows
         seq_u0 += all;
         ++b;
@@ -177,39 +184,36 @@ struct Pieces {
         continue;
       }
       const long long at = u - seq_u0;
-      int lo = 0, hi = p.w.segments;  // the last segment that begins at or before it
+      int lo = 0, hi = w.segments;  // the last segment that begins at or before it
       while (hi - lo > 1) {
         const int mid = lo + (hi - lo) / 2;
-        if (a.v.kv_heads * cost_before<S>(p.w, mid) <= at)
+        if (a.v.kv_heads * cost_before<S>(w, mid) <= at)
           lo = mid;
         else
           hi = mid;
       }
-      const long long before = a.v.kv_heads * cost_before<S>(p.w, lo), one = cost<S>(p.w, lo);
+      const long long before = a.v.kv_heads * cost_before<S>(w, lo), one = cost<S>(w, lo);
+      t = lo;
       p.b = b;
-      p.t = lo;
       p.g = (int)min((at - before) / one, (long long)a.v.kv_heads - 1);
       const long long seg_u0 = seq_u0 + before + p.g * one, seg_end = seg_u0 + one;
-      p.tiles = key_tiles<S>(a, p.w, lo);
+      p.tiles = key_tiles<S>(a, w, lo);
       p.k0 = u == seg_u0 ? 0 : tile_at<S>(a, u - seg_u0, p.tiles);
       p.k1 = end >= seg_end ? p.tiles : tile_at<S>(a, end - seg_u0, p.tiles);
       u = min(end, seg_end);
       if (p.k0 >= p.k1) continue;
+      p.len = w.len, p.first = w.first, p.r0 = w.r0;
       p.p0 = (long long)lo * S::PAIRS;
-      p.np = (int)min((long long)S::PAIRS, p.w.pairs - p.p0);
+      p.np = (int)min((long long)S::PAIRS, w.pairs - p.p0);
+      made_of = 1;
+      if (p.k0 == 0 && p.k1 < p.tiles)
+        for (++c; c < ctas; ++c, ++made_of) {
+          const long long x = share_begin(c, ctas, total);
+          if (x >= seg_end || tile_at<S>(a, x - seg_u0, p.tiles) >= p.tiles) break;
+        }
       return true;
     }
     return false;
-  }
-  // Pieces of the segment that p begins (k0 == 0), this CTA the c-th.
-  __device__ __forceinline__ int count(const PrefillArgs& a, const Piece& p, int c) const {
-    const long long one = cost<S>(p.w, p.t), seg_u0 = seq_u0 + a.v.kv_heads * cost_before<S>(p.w, p.t) + p.g * one;
-    int n = 1;
-    for (++c; c < ctas; ++c, ++n) {
-      const long long at = share_begin(c, ctas, total);
-      if (at >= seg_u0 + one || tile_at<S>(a, at - seg_u0, p.tiles) >= p.tiles) break;
-    }
-    return n;
   }
 };
 
@@ -235,15 +239,20 @@ struct Window {
 
 // Where the codes of a group of 32 positions lie, in groups (page ids out of range read page 0, flagged).
 __device__ __forceinline__ uint32_t group_at(const PrefillArgs& a, const Piece& p, int group) {
-  if (group * 32ll >= p.w.len) return 0;
+  if (group * 32ll >= p.len) return 0;
   const int pos = group * 32, page = max(kv8_page(a.v, p.b, pos >> a.v.page_shift), 0);
   return (uint32_t)(kv8_scale_at(a.v, page, p.g) << (a.v.page_shift - 5)) +
          (uint32_t)((pos >> 5) & ((1 << (a.v.page_shift - 5)) - 1));
 }
-__device__ __forceinline__ float2 group_scales(const PrefillArgs& a, const Piece& p, int group) {
-  if (group * 32ll >= p.w.len) return make_float2(0.f, 0.f);
+// The scales of a group of 32 positions, V's as a logarithm too.
+struct GroupScales {
+  float k, v, log2_v;
+};
+__device__ __forceinline__ GroupScales group_scales(const PrefillArgs& a, const Piece& p, int group) {
+  if (group * 32ll >= p.len) return GroupScales{0.f, 0.f, 0.f};
   const size_t at = kv8_scale_at(a.v, max(kv8_page(a.v, p.b, group * 32 >> a.v.page_shift), 0), p.g);
-  return make_float2(a.v.k_scale[at], a.v.v_scale[at]);
+  const float x = a.v.v_scale[at];
+  return GroupScales{a.v.k_scale[at], x, log2f(x)};
 }
 
 // ---------------------------------------------------------------- tensor core operands
@@ -262,6 +271,16 @@ __device__ __forceinline__ uint64_t smem_desc_n_major(const void* tile, uint32_t
 }
 constexpr uint32_t N_MAJOR_B = 1u << 16;
 
+// Registers of a warpgroup's threads from here on (a rise waits for those that others give up).
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // 32 lanes x 16 columns, from v[0 .. 15].
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
@@ -273,6 +292,18 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
 }
 
 // ---------------------------------------------------------------- rows
+// The exponent of a row's largest magnitude (kept to 2^+-120: beyond, the row enters scaled less, its products still in range).
+__device__ __forceinline__ int q_exponent(float top) {
+  return top <= FLT_MAX ? min(max((int)(__float_as_uint(top) >> 23) - 127, -120), 120) : 0;
+}
+// The elements of 16 bytes of a row.
+template <typename T, int N>
+__device__ __forceinline__ void values_of(const uint4& w, float (&x)[N]) {
+  if constexpr (N == 4)
+    x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y), x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
+  else
+    values8(Vec8<T>{w}, x);
+}
 template <typename T>
 __device__ __forceinline__ void store4(T* p, const float4& x) {
   if constexpr (sizeof(T) == 4)
@@ -289,10 +320,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQ = smem;
   uint8_t* ring = smem + S::Q_BYTES;
-  __shared__ uint64_t full[S::SLOTS], empty[S::SLOTS], q_full[2], s_full[2], p_full[2], o_done[2], o_last[2], drain;
+  uint8_t* raw = ring + S::SLOTS * S::SLOT;
+  __shared__ uint64_t raw_full[S::RAWS], raw_empty[S::RAWS], full[S::SLOTS], empty[S::SLOTS], q_full[2], s_full[2], p_full[2], o_done[2], o_last[2], piece_full[2],
+      piece_empty[2], drain;
+  __shared__ Piece s_piece[2];
   __shared__ uint32_t tmem_holder;
   __shared__ int abort_words[2];  // the second is never set: the drain's wait ignores the abort
-  __shared__ long long s_scan[MMA_WARP + 1], s_found[1];
+  __shared__ long long s_scan[THREADS / 32], s_found[1];
   __shared__ int s_found_b;
   volatile int* abort_flag = abort_words;
   const Kv8View& v = a.v;
@@ -315,12 +349,18 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
       mbar_init(&full[i], S::CONV);
       mbar_init(&empty[i], 1);
     }
+    for (int i = 0; i < S::RAWS; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], S::CONV);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 4);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&o_done[i], 1);
       mbar_init(&o_last[i], 1);
+      mbar_init(&piece_full[i], 1);
+      mbar_init(&piece_empty[i], MMA_WARP + 2);
     }
     mbar_init(&drain, 1);
     abort_words[0] = abort_words[1] = 0;
@@ -335,93 +375,126 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
   const uint32_t tmem = tmem_holder;
   long long my_u0 = inc - mine, total = 0;
 #pragma unroll
-  for (int w = 0; w <= MMA_WARP; ++w) {
+  for (int w = 0; w < THREADS / 32; ++w) {
     if (w < warp) my_u0 += s_scan[w];
     total += s_scan[w];
   }
-  Pieces<S> pieces;
-  pieces.total = total;
-  pieces.ctas = (int)max(1ll, min((long long)a.ctas, total / ((long long)MIN_TILES * S::KT * a.group)));
-  const bool idle = (int)blockIdx.x >= pieces.ctas || total <= 0;
-  pieces.u = idle ? 0 : share_begin(blockIdx.x, pieces.ctas, total);
-  pieces.end = idle ? 0 : share_begin(blockIdx.x + 1, pieces.ctas, total);
-  if (!idle && my_u0 <= pieces.u && pieces.u < my_u0 + mine) {
+  const int ctas = (int)max(1ll, min((long long)a.ctas, total / ((long long)MIN_TILES * S::KT * a.group)));
+  const bool idle = (int)blockIdx.x >= ctas || total <= 0;
+  const long long u = idle ? 0 : share_begin(blockIdx.x, ctas, total);
+  if (!idle && my_u0 <= u && u < my_u0 + mine) {
     int b = my_b0;
     long long at = my_u0;
-    for (long long n; b + 1 < my_b1 && at + (n = cost_all<S>(a, work_of<S>(a, b))) <= pieces.u; ++b) at += n;
+    for (long long n; b + 1 < my_b1 && at + (n = cost_all<S>(a, work_of<S>(a, b))) <= u; ++b) at += n;
     s_found_b = b;
     s_found[0] = at;
   }
   __syncthreads();
-  pieces.b = s_found_b;
-  pieces.seq_u0 = s_found[0];
-  Piece p;
+  int ok = 1;
+  auto wait = [&](uint64_t* bar, int phase) {
+    ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)(phase & 1), abort_flag, v.status));
+    return ok;
+  };
+  // the i-th piece, once it is known; and no longer looked at
+  auto piece_is = [&](int i) { return wait(&piece_full[i & 1], i >> 1) && s_piece[i & 1].k1 > 0; };
+  auto piece_done = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&piece_empty[i & 1]);
+  };
 
   if (warp < S::SOFT) {
     // ------------------------------------------------ softmax
+    more_registers<S::SOFT_REGS>();
     const int m = warp / 4, r = (int)threadIdx.x & 127;
     const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16), o_col = lanes + m * D;
     const T* q = static_cast<const T*>(a.q);
     T* out = static_cast<T*>(a.out);
-    int cnt = 0, npiece = 0;  // key tiles and pieces so far
-    bool ok = true, begun = false;
-    auto wait = [&](uint64_t* bar, int phase) {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)(phase & 1), abort_flag, v.status));
-      return ok;
-    };
-    auto scales_of = [&](int group) { return group_scales(a, p, group); };
-    Window<float2, decltype(scales_of)> scales;
-    while (ok && pieces.next(a, p)) {
+    int cnt = 0, mine_so_far = 0;  // key tiles, and pieces with pairs of this M tile, so far
+    for (int ip = 0; piece_is(ip); piece_done(ip), ++ip) {
+      const Piece& p = s_piece[ip & 1];
       if (128 * m >= p.np) continue;
-      // ---- the row: fp16 pieces times a power of two that brings the largest magnitude into [1, 2)
+      auto scales_of = [&](int group) { return group_scales(a, p, group); };
+      Window<GroupScales, decltype(scales_of)> scales;
       scales.begin(p.k0 * S::GROUPS, scales_of);
       const bool live = 128 * m + r < p.np;
       const long long pair = p.p0 + 128 * m + (live ? r : 0);
       const int i = (int)(pair / a.group);
       const size_t head = (size_t)p.g * a.group + (size_t)(pair % a.group);
-      const T* qr = q + (long long)(p.w.r0 + i) * a.ldq + head * D;
-      float top = 0.f;
-      bool odd = false;
-#pragma unroll 8
-      for (int d = 0; d < D; d += 8) {
-        float x[8];
-        values8(load8(qr + d), x);
+      // ---- the warp's 32 rows, some lanes a row: fp16 pieces times a power of two that brings a row's largest
+      // magnitude into [1, 2); a row with a NaN or an infinity as zeros, its scores' factor NaN
+      const long long q_at = (long long)(p.r0 + i) * a.ldq + (long long)(head * D);
+      float top = 0.f;  // of this thread's row
+      {
+        constexpr int N = 16 / sizeof(T), VECS = D / N, LR = VECS < 32 ? VECS : 32, V = VECS / LR;  // elements of 16 bytes; a row's lanes, and what a lane has of it
+        constexpr int RS = 32 / LR, BATCH = V == 1 ? 16 : 8;
+        const int in_row = lane % LR;
+        uint8_t* rows = sQ + m * S::PIECES * 128 * D * 2;
+#pragma unroll 1
+        for (int b0 = 0; b0 < 32 / RS; b0 += BATCH) {
+          uint4 x[BATCH][V];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e])), odd |= x[e] != x[e];
-      }
-      const int e2 = top <= FLT_MAX ? min(max((int)(__float_as_uint(top) >> 23) - 127, -120), 120) : 0;
-      const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
-      // (a NaN or an infinity: every score of the row NaN, its products finite)
-      const bool bad = odd || !(top <= FLT_MAX);
-      const float factor = bad ? __int_as_float(0x7fffffff) : a.scale_log2 * __uint_as_float((uint32_t)(127 + e2) << 23);
-      uint8_t* sq = sQ + m * S::PIECES * 128 * D * 2 + r * 128;
-#pragma unroll 4
-      for (int d = 0; d < D; d += 8) {
-        float x[8];
-        values8(load8(qr + d), x);
-        uint32_t h[4], l[4];
+          for (int k = 0; k < BATCH; ++k) {
+            const int owner = (b0 + k) * RS + lane / LR;
+            const T* from = q + __shfl_sync(0xffffffffu, q_at, owner & 31);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float y0 = live && !bad ? x[2 * e] * down : 0.f, y1 = live && !bad ? x[2 * e + 1] * down : 0.f;
-          h[e] = half2_bits(y0, y1);
-          const float2 f = half2_values(h[e]);
-          l[e] = half2_bits(y0 - f.x, y1 - f.y);
+            for (int e = 0; e < V; ++e)
+              if (owner < 32) x[k][e] = *reinterpret_cast<const uint4*>(from + (e * LR + in_row) * N);
+          }
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) {
+            if ((b0 + k) * RS >= 32) break;
+            const int owner = (b0 + k) * RS + lane / LR, R = warp % 4 * 32 + owner;
+            float y[V][N];
+            float most = 0.f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              values_of<T>(x[k][e], y[e]);
+#pragma unroll
+              for (int h = 0; h < N; ++h) most = fmaxf(most, y[e][h] == y[e][h] ? fabsf(y[e][h]) : INFINITY);
+            }
+#pragma unroll
+            for (int o = LR / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+            const float mine = __shfl_sync(0xffffffffu, most, (lane - (b0 + k) * RS) * LR & 31);
+            if (lane / RS == b0 + k) top = mine;
+            const int counts = __shfl_sync(0xffffffffu, (int)live, owner);
+            const bool zero = !(most <= FLT_MAX) || !counts;
+            const float down = __uint_as_float((uint32_t)(127 - q_exponent(most)) << 23);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              uint32_t hi[N / 2], lo[N / 2];
+#pragma unroll
+              for (int h = 0; h < N / 2; ++h) {
+                const float y0 = zero ? 0.f : y[e][2 * h] * down, y1 = zero ? 0.f : y[e][2 * h + 1] * down;
+                hi[h] = half2_bits(y0, y1);
+                const float2 f = half2_values(hi[h]);
+                lo[h] = half2_bits(y0 - f.x, y1 - f.y);
+              }
+              const int d = (e * LR + in_row) * N;
+              uint8_t* to = rows + (d / 64) * 128 * 128 + R * 128 + (((d / 8 % 8) ^ (R & 7)) << 4) + d % 8 * 2;
+              if constexpr (N == 8) {
+                *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              } else {
+                *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2*>(to + 128 * D * 2) = make_uint2(lo[0], lo[1]);
+              }
+            }
+          }
         }
-        uint8_t* to = sq + (d / 64) * 128 * 128 + (((d / 8 % 8) ^ (r & 7)) << 4);
-        *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
-        if constexpr (S::TWO) *reinterpret_cast<uint4*>(to + 128 * D * 2) = make_uint4(l[0], l[1], l[2], l[3]);
       }
+      const float factor = !(top <= FLT_MAX) ? __int_as_float(0x7fffffff)
+                                             : a.scale_log2 * __uint_as_float((uint32_t)(127 + q_exponent(top)) << 23);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[m]);
-      ++npiece;
+      ++mine_so_far;
 
-      const int sees = live ? min(p.w.len, p.w.first + i + 1) : 0;  // positions
+      const int sees = live ? min(p.len, p.first + i + 1) : 0;  // positions
       float ref = -INFINITY, run_max = -INFINITY, sum = 0.f;
       float R = 0x1p-100f, inv_R = 0x1p100f;
       float mean_ref = -INFINITY, mean_sum = 0.f;  // of the mean taken over
-      const bool partial = p.k1 - p.k0 < p.tiles;
-      const int slot = 2 * (int)blockIdx.x + (p.k0 == 0);
+      const int k0 = p.k0, k1 = p.k1;
+      const bool partial = k1 - k0 < p.tiles;
+      const int slot = 2 * (int)blockIdx.x + (k0 == 0);
       // ---- O, with the mean taken over so far, to the mean, a piece's outputs or the rows
       auto flush = [&](bool last) {
         const float top_ref = fmaxf(ref, mean_ref);
@@ -430,29 +503,70 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
         const float co = R * 0x1p-7f * (wn * inv), cm = wm * mean_sum * inv;
         float4* mean = a.mean + (size_t)blockIdx.x * (D / 4) * S::PAIRS + 128 * m + r;
         float4* part = a.part_o + (size_t)slot * (D / 4) * S::PAIRS + 128 * m + r;
-        T* to = out + (long long)(p.w.r0 + i) * a.ldo + head * D;
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld_32x32b_x32(o_col + 32 * c, o);
-          tmem_ld_wait_regs(o);
+        const long long out_at = (long long)(p.r0 + i) * a.ldo + (long long)(head * D);
+        float4 x[2][8];  // the mean so far, 32 dims ahead
+        const bool more = S::TWO && mean_sum != 0.f;
+        if (more) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            float4 y = make_float4(__uint_as_float(o[4 * k]) * co, __uint_as_float(o[4 * k + 1]) * co,
-                                   __uint_as_float(o[4 * k + 2]) * co, __uint_as_float(o[4 * k + 3]) * co);
-            const size_t at = (size_t)(8 * c + k) * S::PAIRS;
-            if constexpr (S::TWO)
-              if (mean_sum != 0.f) {
-                const float4 x = mean[at];
-                y.x = fmaf(x.x, cm, y.x), y.y = fmaf(x.y, cm, y.y), y.z = fmaf(x.z, cm, y.z), y.w = fmaf(x.w, cm, y.w);
+          for (int k = 0; k < 8; ++k) x[0][k] = mean[(size_t)k * S::PAIRS];
+        }
+        // (rows of T leave through the warp's own rows of q's place, which no product reads any more: 128 bytes of
+        // a row together instead of 16)
+        constexpr int DIMS = 128 / sizeof(T);
+#pragma unroll 1
+        for (int c0 = 0; c0 < D / 32; c0 += 2) {
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            const int c = c0 + cc;
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(o_col + 32 * c, o);
+            if (more && c + 1 < D / 32) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) x[1 - cc][k] = mean[(size_t)(8 * c + 8 + k) * S::PAIRS];
+            }
+            tmem_ld_wait_regs(o);
+            uint8_t* row = sQ + m * S::PIECES * 128 * D * 2 + 32 * c / DIMS * (128 * 128) + r * 128;
+            uint2 half_chunk = make_uint2(0, 0);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              float4 y = make_float4(__uint_as_float(o[4 * k]) * co, __uint_as_float(o[4 * k + 1]) * co,
+                                     __uint_as_float(o[4 * k + 2]) * co, __uint_as_float(o[4 * k + 3]) * co);
+              if (more) {
+                const float4 z = x[cc][k];
+                y.x = fmaf(z.x, cm, y.x), y.y = fmaf(z.y, cm, y.y), y.z = fmaf(z.z, cm, y.z), y.w = fmaf(z.w, cm, y.w);
               }
-            if (all == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);  // (whatever O held)
-            if (!last)
-              mean[at] = y;
-            else if (partial)
-              part[at] = y;
-            else if (live)
-              store4<T>(to + 32 * c + 4 * k, y);
+              if (all == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);  // (whatever O held)
+              if (!last) {
+                mean[(size_t)(8 * c + k) * S::PAIRS] = y;
+              } else if (partial) {
+                part[(size_t)(8 * c + k) * S::PAIRS] = y;
+              } else if constexpr (sizeof(T) == 4) {
+                *reinterpret_cast<float4*>(row + ((k ^ (r & 7)) << 4)) = y;
+              } else {
+                const uint2 h = make_uint2(pack2<T>(y.x, y.y), pack2<T>(y.z, y.w));
+                if (k & 1)
+                  *reinterpret_cast<uint4*>(row + (((32 * c % DIMS / 8 + k / 2) ^ (r & 7)) << 4)) =
+                      make_uint4(half_chunk.x, half_chunk.y, h.x, h.y);
+                else
+                  half_chunk = h;
+              }
+            }
+          }
+          if (last && !partial) {
+            __syncwarp();
+#pragma unroll
+            for (int b = 0; b < 64 / DIMS; ++b) {  // 128-byte blocks of the 64 dims
+              const int block = 32 * c0 / DIMS + b;
+#pragma unroll
+              for (int it = 0; it < 8; ++it) {
+                const int rr = it * 4 + lane / 8, R = warp % 4 * 32 + rr;
+                const uint4 y = *reinterpret_cast<const uint4*>(sQ + m * S::PIECES * 128 * D * 2 + block * (128 * 128) + R * 128 +
+                                                                (((lane & 7) ^ (R & 7)) << 4));
+                const long long to = __shfl_sync(0xffffffffu, out_at, rr);
+                if (__shfl_sync(0xffffffffu, (int)live, rr))
+                  *reinterpret_cast<uint4*>(out + to + block * DIMS + (lane & 7) * (16 / (int)sizeof(T))) = y;
+              }
+            }
           }
         }
         mean_ref = top_ref;
@@ -461,46 +575,50 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
       };
       bool fresh = true;  // O holds nothing yet
 #pragma unroll 1
-      for (int j = p.k0; j < p.k1; ++j, ++cnt) {
+      for (int j = k0; j < k1; ++j, ++cnt) {
         const int buf = S::MT == 2 ? m : cnt & 1, phase = S::MT == 2 ? cnt : cnt >> 1;
         scales.reach(j * S::GROUPS, scales_of);
         float ks[S::GROUPS], vs[S::GROUPS];
-        float vmax = 0.f;
+        float vmax = 0.f, vmin = FLT_MAX;
 #pragma unroll
         for (int c = 0; c < S::GROUPS; ++c) {
-          ks[c] = __shfl_sync(0xffffffffu, scales.now.x, j * S::GROUPS + c - scales.base) * factor;
-          vs[c] = __shfl_sync(0xffffffffu, scales.now.y, j * S::GROUPS + c - scales.base);
-          vmax = fmaxf(vmax, vs[c]);
+          ks[c] = __shfl_sync(0xffffffffu, scales.now.k, j * S::GROUPS + c - scales.base) * factor;
+          ks[c] = ks[c] == 0.f ? FLT_MIN : ks[c];  // (as good as 0 for a score, but minus infinity stays that)
+          vs[c] = __shfl_sync(0xffffffffu, scales.now.v, j * S::GROUPS + c - scales.base);
+          vmax = fmaxf(vmax, vs[c]), vmin = fminf(vmin, vs[c]);
         }
         // (these scores' completion covers every product before them, O's of two tiles ago among them: so a wait for the
         // last tile's O, by parity, cannot be a phase behind)
         if (!wait(&s_full[buf], phase)) break;
         tc_fence_after();
-        if (S::TWO && j > p.k0 && (j - p.k0) % S::FOLD_TILES == 0) {
+        if (S::TWO && j > k0 && (j - k0) % S::FOLD_TILES == 0) {
           if (!wait(&o_done[m], cnt - 1)) break;
           tc_fence_after();
           flush(false);
           fresh = true;
         }
         const uint32_t s_col = lanes + S::COL_S + buf * S::KT, p_col = lanes + S::COL_P + buf * S::P_STEP;
+        uint32_t s[S::KT];
+#pragma unroll
+        for (int c = 0; c < S::GROUPS; ++c) tmem_ld_32x32b_x32(s_col + 32 * c, s + 32 * c);
+        tmem_ld_wait_regs(s);
+#pragma unroll
+        for (int c = 1; c < S::GROUPS; ++c) regs_after_wait(s + 32 * c);
         const int left = sees - j * S::KT;  // positions of the tile that the row sees
-        const bool whole = __all_sync(0xffffffffu, left >= S::KT);
+        if (!__all_sync(0xffffffffu, left >= S::KT)) {
+#pragma unroll
+          for (int k = 0; k < S::KT; ++k) s[k] = k < left ? s[k] : 0xff800000u;
+        }
         float tile_max = -INFINITY;
 #pragma unroll
         for (int c = 0; c < S::GROUPS; ++c) {
-          uint32_t s[32];
-          tmem_ld_32x32b_x32(s_col + 32 * c, s);
-          tmem_ld_wait_regs(s);
           float x[2] = {-INFINITY, -INFINITY};
-          if (whole) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k & 1] = fmaxf(x[k & 1], __uint_as_float(s[k]));
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) x[k & 1] = 32 * c + k < left ? fmaxf(x[k & 1], __uint_as_float(s[k])) : x[k & 1];
+          for (int k = 0; k < 32; k += 4) {
+            x[0] = fmaxf(fmaxf(x[0], __uint_as_float(s[32 * c + k])), __uint_as_float(s[32 * c + k + 1]));
+            x[1] = fmaxf(fmaxf(x[1], __uint_as_float(s[32 * c + k + 2])), __uint_as_float(s[32 * c + k + 3]));
           }
-          const float y = fmaxf(x[0], x[1]);
-          tile_max = fmaxf(tile_max, y == -INFINITY ? y : y * ks[c]);
+          tile_max = fmaxf(tile_max, fmaxf(x[0], x[1]) * ks[c]);
         }
         run_max = fmaxf(run_max, tile_max);
         // ---- the reference, and R: O moves with them
@@ -536,133 +654,117 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
           }
         }
         // ---- the weights
-        float l[2] = {0.f, 0.f};
+        if (!S::TWO && vmin > R * 0x1p-60f) {
+          // 2^(score - ref + log2 of the page's factor) at once, the sum divided by the factor again
+          const float shift = 134.f - (float)(__float_as_uint(R) >> 23);  // log2(2^7 / R)
 #pragma unroll
-        for (int c = 0; c < S::GROUPS; ++c) {
-          uint32_t s[32];
-          tmem_ld_32x32b_x32(s_col + 32 * c, s);
-          tmem_ld_wait_regs(s);
-          const float w = vs[c] * inv_R * 0x1p7f;
-          uint32_t hi[16], lo[16];
+          for (int c = 0; c < S::GROUPS; ++c) {
+            const float e = __shfl_sync(0xffffffffu, scales.now.log2_v, j * S::GROUPS + c - scales.base) + shift;
+            const float2 k2 = make_float2(ks[c], ks[c]), r2 = make_float2(e - ref, e - ref);
+            float2 l = make_float2(0.f, 0.f);
+            uint32_t hi[16];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float x0 = exp2_fast(fmaf(__uint_as_float(s[2 * k]), ks[c], -ref));
-            float x1 = exp2_fast(fmaf(__uint_as_float(s[2 * k + 1]), ks[c], -ref));
-            if (!whole) {
-              x0 = 32 * c + 2 * k < left ? x0 : 0.f;
-              x1 = 32 * c + 2 * k + 1 < left ? x1 : 0.f;
+            for (int k = 0; k < 16; ++k) {
+              const float2 y = make_float2(__uint_as_float(s[32 * c + 2 * k]), __uint_as_float(s[32 * c + 2 * k + 1]));
+              float2 x = __ffma2_rn(y, k2, r2);
+              x.x = exp2_fast(x.x), x.y = exp2_fast(x.y);
+              l = __fadd2_rn(l, x);
+              hi[k] = half2_bits(x.x, x.y);
             }
-            l[0] += x0, l[1] += x1;
-            x0 *= w, x1 *= w;
-            hi[k] = half2_bits(x0, x1);
-            if constexpr (S::TWO) {
-              const float2 f = half2_values(hi[k]);
-              lo[k] = half2_bits(x0 - f.x, x1 - f.y);
-            }
+            sum = fmaf(l.x + l.y, exp2f(-e), sum);
+            tmem_st_32x32b_x16(p_col + 16 * c, hi);
           }
-          tmem_st_32x32b_x16(p_col + 16 * c, hi);
-          if constexpr (S::TWO) tmem_st_32x32b_x16(p_col + S::KT / 2 + 16 * c, lo);
-          tmem_st_wait();
+        } else {
+#pragma unroll
+          for (int c = 0; c < S::GROUPS; ++c) {
+            const float w = vs[c] * inv_R * 0x1p7f;
+            const float2 k2 = make_float2(ks[c], ks[c]), r2 = make_float2(-ref, -ref), w2 = make_float2(w, w);
+            float2 l = make_float2(0.f, 0.f);
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float2 y = make_float2(__uint_as_float(s[32 * c + 2 * k]), __uint_as_float(s[32 * c + 2 * k + 1]));
+              float2 x = __ffma2_rn(y, k2, r2);
+              x.x = exp2_fast(x.x), x.y = exp2_fast(x.y);
+              l = __fadd2_rn(l, x);
+              x = __fmul2_rn(x, w2);
+              hi[k] = half2_bits(x.x, x.y);
+              if constexpr (S::TWO) {
+                const float2 f = half2_values(hi[k]);
+                lo[k] = half2_bits(x.x - f.x, x.y - f.y);
+              }
+            }
+            sum += l.x + l.y;
+            tmem_st_32x32b_x16(p_col + 16 * c, hi);
+            if constexpr (S::TWO) tmem_st_32x32b_x16(p_col + S::KT / 2 + 16 * c, lo);
+          }
         }
-        sum += l[0] + l[1];
+        tmem_st_wait();
         fresh = false;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[buf]);
       }
-      if (!ok || !wait(&o_last[m], npiece - 1)) break;
+      if (!ok || !wait(&o_last[m], mine_so_far - 1)) break;
       tc_fence_after();
       flush(true);
       tc_fence_before();
-      if (partial) {
-        a.part_ml[(size_t)slot * S::PAIRS + 128 * m + r] = make_float2(mean_ref, mean_sum);
-        if (p.k0 == 0 && threadIdx.x == 0) {
-          a.record[blockIdx.x] = make_int4(p.b, p.t, p.g, pieces.count(a, p, blockIdx.x));
-          begun = true;
-        }
-      }
+      if (partial) a.part_ml[(size_t)slot * S::PAIRS + 128 * m + r] = make_float2(mean_ref, mean_sum);
     }
-    if (threadIdx.x == 0 && !begun) a.record[blockIdx.x] = make_int4(0, 0, 0, 0);
   } else if (warp < MMA_WARP) {
     // ------------------------------------------------ converters: chunks of K and V in the order in which they are used
+    fewer_registers<S::CONV_REGS>();
     const int tid = (int)threadIdx.x - 32 * S::SOFT;
     constexpr int ROW = D / 16;                       // 16-byte pieces of a position's codes
     constexpr int STEP = 32 * S::CONV / ROW;          // positions from one of a thread's pieces to the next
     const int key0 = tid / ROW, piece = tid % ROW, panel = piece / 4;
-    int done = 0;  // chunks so far
-    bool ok = true;
-    auto at_of = [&](int group) { return group_at(a, p, group); };
-    Window<uint32_t, decltype(at_of)> at[2];
-    while (ok && pieces.next(a, p)) {
-      const int n = p.k1 - p.k0;
-      at[0].begin(p.k0 * S::GROUPS, at_of);
-      at[1] = at[0];
-      uint4 w[2][S::EACH];
-      // chunk c: K of tile 0, V of tile 0, K of tile 1, ..., or with one M tile K of tiles 0 and 1, V of tile 0, K of tile 2, ...
-      auto load = [&](int c, uint4 (&x)[S::EACH]) {
-        int j = c / 2, is_v = c & 1;
-        if (S::MT == 1 && c > 0 && c < 2 * n - 1) is_v = !(c & 1), j = is_v ? (c - 2) / 2 : (c + 1) / 2;
-        const int tile = p.k0 + j;
-        at[is_v].reach(tile * S::GROUPS, at_of);
-        const int8_t* codes = (is_v ? v.V : v.K) + piece * 16;
-#pragma unroll
-        for (int i = 0; i < S::EACH; ++i) {
-          const int key = key0 + i * STEP;
-          const uint32_t g = __shfl_sync(0xffffffffu, at[is_v].now, tile * S::GROUPS + key / 32 - at[is_v].base);
-          x[i] = make_uint4(0, 0, 0, 0);
-          if (tile * S::KT + key < p.w.len)
-            x[i] = *reinterpret_cast<const uint4*>(codes + ((size_t)g * 32 + key % 32) * D);
-        }
-      };
-      auto put = [&](const uint4 (&x)[S::EACH]) {
-        const int s = done % S::SLOTS;
-        ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], (uint32_t)((done / S::SLOTS + 1) & 1), abort_flag, v.status));
-        if (!ok) return;
+    uint32_t done = 0;  // chunks so far
+    for (int ip = 0; piece_is(ip); piece_done(ip), ++ip) {
+      const int chunks = 2 * (s_piece[ip & 1].k1 - s_piece[ip & 1].k0);
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c, ++done) {
+        const int rs = done % S::RAWS, s = done % S::SLOTS;
+        if (!wait(&raw_full[rs], done / S::RAWS) || !wait(&empty[s], done / S::SLOTS + 1)) break;
+        const uint8_t* from = raw + rs * S::RAW + tid * 16;
         uint8_t* slot = ring + s * S::SLOT + panel * S::PANEL;
+        uint4 x[S::EACH];
+#pragma unroll
+        for (int i = 0; i < S::EACH; ++i) x[i] = *reinterpret_cast<const uint4*>(from + i * (32 * S::CONV * 16));
 #pragma unroll
         for (int i = 0; i < S::EACH; ++i) {
           const int key = key0 + i * STEP;
           const uint32_t b[4] = {x[i].x ^ 0x80808080u, x[i].y ^ 0x80808080u, x[i].z ^ 0x80808080u, x[i].w ^ 0x80808080u};
-          uint4 y[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            y[h] = make_uint4(half2_of_codes(b[2 * h], 0x4140), half2_of_codes(b[2 * h], 0x4342),
-                              half2_of_codes(b[2 * h + 1], 0x4140), half2_of_codes(b[2 * h + 1], 0x4342));
+          const uint4 y0 = make_uint4(half2_of_codes(b[0], 0x4140), half2_of_codes(b[0], 0x4342),
+                                      half2_of_codes(b[1], 0x4140), half2_of_codes(b[1], 0x4342));
+          const uint4 y1 = make_uint4(half2_of_codes(b[2], 0x4140), half2_of_codes(b[2], 0x4342),
+                                      half2_of_codes(b[3], 0x4140), half2_of_codes(b[3], 0x4342));
           uint8_t* row = slot + key * 128;
-          const int c = 2 * (piece & 3), odd = panel & 1;  // (neighbouring panels' stores go to different banks)
-          *reinterpret_cast<uint4*>(row + (((c + odd) ^ (key & 7)) << 4)) = y[odd];
-          *reinterpret_cast<uint4*>(row + (((c + 1 - odd) ^ (key & 7)) << 4)) = y[1 - odd];
+          const int c8 = 2 * (piece & 3), odd = panel & 1;  // (neighbouring panels' stores go to different banks)
+          *reinterpret_cast<uint4*>(row + (((c8 + odd) ^ (key & 7)) << 4)) = odd ? y1 : y0;
+          *reinterpret_cast<uint4*>(row + (((c8 + 1 - odd) ^ (key & 7)) << 4)) = odd ? y0 : y1;
         }
-        fence_proxy_async_smem();
+        fence_proxy_async_smem();  // (no load from global memory is on its way, which it would wait for)
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[s]);
-        ++done;
-      };
-      load(0, w[0]);
-#pragma unroll 1
-      for (int c = 0; c < 2 * n && ok; c += 2) {
-        load(c + 1, w[1]);
-        put(w[0]);
-        if (!ok) break;
-        if (c + 2 < 2 * n) load(c + 2, w[0]);
-        put(w[1]);
+        if (lane == 0) {
+          mbar_arrive(&raw_empty[rs]);
+          mbar_arrive(&full[s]);
+        }
       }
+      if (!ok) break;
     }
   } else {
+    fewer_registers<S::MMA_REGS>();
+  }
+  if (warp == MMA_WARP) {
     // ------------------------------------------------ the products
     constexpr uint32_t IDESC_S = idesc_f16_f32(128, S::KT), IDESC_O = idesc_f16_f32(128, D) | N_MAJOR_B;
-    int chunks = 0, cnt[2] = {0, 0}, npiece[2] = {0, 0};
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, int phase) {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)(phase & 1), abort_flag, v.status));
-      return ok;
-    };
-    while (ok && pieces.next(a, p)) {
-      const int n = p.k1 - p.k0, nm = S::MT == 2 && p.np > 128 ? 2 : 1;
+    int chunks = 0, cnt0 = 0, cnt1 = 0, mine0 = 0, mine1 = 0;  // chunks; key tiles and pieces of each M tile, so far
+    for (int ip = 0; piece_is(ip); piece_done(ip), ++ip) {
+      const int n = s_piece[ip & 1].k1 - s_piece[ip & 1].k0, nm = S::MT == 2 && s_piece[ip & 1].np > 128 ? 2 : 1;
       auto k_chunk = [&](int j) { return chunks + (S::MT == 2 || j == 0 ? 2 * j : 2 * j - 1); };
       auto v_chunk = [&](int j) { return chunks + (S::MT == 2 || j == n - 1 ? 2 * j + 1 : 2 * j + 2); };
       auto issue_s = [&](int j, int m) {
-        const int c = k_chunk(j), x = cnt[m] + j, buf = S::MT == 2 ? m : x & 1;
+        const int c = k_chunk(j), x = (m ? cnt1 : cnt0) + j, buf = S::MT == 2 ? m : x & 1;
         if (!wait(&full[c % S::SLOTS], c / S::SLOTS)) return;
         tc_fence_after();
         const uint8_t* kt = ring + c % S::SLOTS * S::SLOT;
@@ -678,7 +780,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
         if (m == nm - 1) mma_commit_elect(&empty[c % S::SLOTS]);
       };
       auto issue_o = [&](int j, int m) {
-        const int c = v_chunk(j), x = cnt[m] + j, buf = S::MT == 2 ? m : x & 1;
+        const int c = v_chunk(j), x = (m ? cnt1 : cnt0) + j, buf = S::MT == 2 ? m : x & 1;
         if (!wait(&full[c % S::SLOTS], c / S::SLOTS)) return;
         if (!wait(&p_full[buf], S::MT == 2 ? x : x >> 1)) return;
         tc_fence_after();
@@ -697,7 +799,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
         if (m == nm - 1) mma_commit_elect(&empty[c % S::SLOTS]);
       };
       for (int m = 0; m < nm && ok; ++m) {
-        wait(&q_full[m], npiece[m]);
+        wait(&q_full[m], m ? mine1 : mine0);
         if (ok) issue_s(0, m);
       }
 #pragma unroll 1
@@ -712,12 +814,73 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
           if (ok) issue_o(j, 0);
         }
       }
-      for (int m = 0; m < nm; ++m) cnt[m] += n, ++npiece[m];
+      cnt0 += n, ++mine0;
+      if (nm == 2) cnt1 += n, ++mine1;
       chunks += 2 * n;
+      if (!ok) break;
     }
     // the products in flight have finished before tensor memory goes
     mma_commit_elect(&drain);
     __all_sync(0xffffffffu, mbar_wait(&drain, 0, abort_flag + 1, v.status));
+  } else if (warp == PIECE_WARP) {
+    // ------------------------------------------------ the pieces of the share, two ahead
+    Pieces<S> pieces{s_found_b, ctas, u, idle ? 0 : share_begin(blockIdx.x + 1, ctas, total), s_found[0], total};
+    int4 record = make_int4(0, 0, 0, 0);
+    bool more = true;
+    for (int ip = 0; more && wait(&piece_empty[ip & 1], (ip >> 1) + 1); ++ip) {
+      Piece p;
+      int t, made_of;
+      more = pieces.next(a, blockIdx.x, p, t, made_of);
+      if (!more) p.k1 = 0;
+      if (more && made_of > 1) record = make_int4(p.b, t, p.g, made_of);
+      if (lane == 0) {
+        s_piece[ip & 1] = p;
+        mbar_arrive(&piece_full[ip & 1]);
+      }
+      __syncwarp();
+    }
+    if (lane == 0) a.record[blockIdx.x] = record;
+  } else if (warp == COPY_WARP) {
+    // ------------------------------------------------ chunks of codes, page by page, in the order in which they are used
+    const int run = min(1 << v.page_shift, S::KT);  // positions of a tile that lie together
+    uint32_t sent = 0;
+    for (int ip = 0; piece_is(ip); piece_done(ip), ++ip) {
+      const Piece& p = s_piece[ip & 1];
+      const int n = p.k1 - p.k0, k0 = p.k0, len = p.len;
+      auto at_of = [&](int group) { return group_at(a, p, group); };
+      Window<uint32_t, decltype(at_of)> k_at, v_at;
+      k_at.begin(k0 * S::GROUPS, at_of);
+      v_at = k_at;
+      auto send = [&](int j, const int8_t* codes, Window<uint32_t, decltype(at_of)>& at) {
+        const int tile = k0 + j, rs = sent % S::RAWS;
+        at.reach(tile * S::GROUPS, at_of);
+        const int first = lane * run, pos = tile * S::KT + first;  // this lane's positions of the tile
+        const uint32_t g = __shfl_sync(0xffffffffu, at.now, min(tile * S::GROUPS + first / 32 - at.base, 31));
+        const bool some = first < S::KT && pos < len;  // (what lies past the sequence stays as it was: any codes are numbers)
+        const int runs = __popc(__ballot_sync(0xffffffffu, some));
+        if (!wait(&raw_empty[rs], sent / S::RAWS + 1)) return;
+        if (lane == 0) {
+          if (runs > 0)
+            mbar_arrive_expect_tx(&raw_full[rs], (uint32_t)(runs * run * D));
+          else
+            mbar_arrive(&raw_full[rs]);
+        }
+        __syncwarp();
+        if (some) bulk_load_1d(raw + rs * S::RAW + first * D, codes + (size_t)g * 32 * D, (uint32_t)(run * D), &raw_full[rs]);
+        ++sent;
+      };
+      // K of tile 0, V of tile 0, K of tile 1, ..., or with one M tile K of tiles 0 and 1, V of tile 0, K of tile 2, ...
+#pragma unroll 1
+      for (int j = 0; j < n && ok; ++j) {
+        if (S::MT == 2 || j == 0) send(j, v.K, k_at);
+        if (S::MT == 1 && j + 1 < n && ok) send(j + 1, v.K, k_at);
+        if (ok) send(j, v.V, v_at);
+      }
+      if (!ok) break;
+    }
+    if (!ok)  // the copies on their way land before the CTA ends
+      for (uint32_t i = sent > (uint32_t)S::RAWS ? sent - S::RAWS : 0; i < sent; ++i)
+        mbar_wait(&raw_full[i % S::RAWS], (i / S::RAWS) & 1, abort_flag + 1, v.status);
   }
   grid_launch_dependents();
   tc_fence_before();
