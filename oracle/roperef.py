@@ -13,9 +13,10 @@ def _f32(x):
 
 
 def rope_table(inv_freq, first, positions, scale=1.0):
-    """float64 [positions][pairs][2], not rounded. Position times float32 frequency is exact in float64."""
-    angle = np.arange(first, first + positions, dtype=np.float64)[:, None] * np.asarray(inv_freq, np.float32).astype(np.float64)
-    return np.stack((np.cos(angle), np.sin(angle)), -1) * scale
+    """float64 [positions][pairs][2]. Position times float32 frequency, up to 54 bits, is exact in a long double (64 bits
+    or more)."""
+    angle = np.arange(first, first + positions).astype(np.longdouble)[:, None] * np.asarray(inv_freq, np.float32).astype(np.longdouble)
+    return (np.stack((np.cos(angle), np.sin(angle)), -1) * np.longdouble(scale)).astype(np.float64)
 
 
 def rope_rows(table, pair_axis, interleaved, positions, x, heads, norm=None, eps=0.0):

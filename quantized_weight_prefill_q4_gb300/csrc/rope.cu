@@ -8,18 +8,84 @@ namespace apr {
 namespace {
 
 // ---------------------------------------------------------------- the table
+// Bound by memory, 8 bytes an entry written once, if an entry takes few instructions: this chip has
+// two FP64 lanes an SM for 128 of FP32, so a 64-bit cosine of each entry takes 50 times as long as its
+// store (400003 positions of 128 pairs: 2.9 ms). So a thread evaluates cosine and sine in 64 bits once in
+// RUN positions, and the others by turning that point on by one position's angle at a time, a complex
+// product of numbers of two float32 (rope.cuh) each, cosine and sine in the two halves of packed instructions: 20 an entry.
+// A product is off by some 2^-46, a run of 64 by 2^-40 at the most, far below half a step of the float32 result.
 constexpr int TB_THREADS = 256;
+constexpr int TB_RUN = 64;
+
+struct Point {
+  double c, s;
+};
+// Cosine and sine of n f (1 / 2 pi in two doubles takes the whole turns off; Taylor's series up to pi / 4, the
+// first term left out below 2^-53).
+__device__ __forceinline__ Point point_of(double n, double f) {
+  constexpr double C0 = 0.15915494309189535, C1 = -9.839338337591243e-18;  // 1 / (2 pi)
+  const double p = n * f, pe = fma(n, f, -p);
+  const double t = p * C0, te = fma(p, C0, -t) + (p * C1 + pe * C0);
+  const double whole = rint(t);
+  double r = (t - whole) + te;                      // turns, within a half
+  const double q = rint(4.0 * r);
+  const double x = (r - 0.25 * q) * 6.283185307179586, z = x * x;
+  double s = fma(z, -1.0 / 1307674368000.0, 1.0 / 6227020800.0);
+  s = fma(z, s, -1.0 / 39916800.0);
+  s = fma(z, s, 1.0 / 362880.0);
+  s = fma(z, s, -1.0 / 5040.0);
+  s = fma(z, s, 1.0 / 120.0);
+  s = fma(z, s, -1.0 / 6.0);
+  s = fma(z * x, s, x);
+  double c = fma(z, 1.0 / 20922789888000.0, -1.0 / 87178291200.0);
+  c = fma(z, c, 1.0 / 479001600.0);
+  c = fma(z, c, -1.0 / 3628800.0);
+  c = fma(z, c, 1.0 / 40320.0);
+  c = fma(z, c, -1.0 / 720.0);
+  c = fma(z, c, 1.0 / 24.0);
+  c = fma(z, c, -0.5);
+  c = fma(z, c, 1.0);
+  const int k = (int)q & 3;
+  return Point{k == 0 ? c : (k == 1 ? -s : (k == 2 ? -c : s)), k == 0 ? s : (k == 1 ? c : (k == 2 ? -s : -c))};
+}
+
+__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
 
 __global__ void __launch_bounds__(TB_THREADS) rope_table_kernel(const float* __restrict__ inv_freq, int pairs,
-                                                                long long first, long long entries, double scale,
-                                                                float2* __restrict__ table) {
+                                                                long long first, long long positions, double scale,
+                                                                int run, int groups, float2* __restrict__ table) {
   grid_dependency_wait();
   grid_launch_dependents();
-  for (long long i = (long long)blockIdx.x * TB_THREADS + threadIdx.x; i < entries; i += (long long)gridDim.x * TB_THREADS) {
-    const double angle = (double)(first + i / pairs) * (double)inv_freq[i % pairs];  // exact: 30 and 24 bits
-    double s, c;
-    sincos(angle, &s, &c);
-    table[i] = make_float2((float)(c * scale), (float)(s * scale));
+  // thread (group, pair): runs group, group + groups, ...
+  const long long id = (long long)blockIdx.x * TB_THREADS + threadIdx.x;
+  if (id >= (long long)groups * pairs) return;
+  const int pair = (int)(id % pairs);
+  const double f = (double)inv_freq[pair];
+  const Point w = point_of(1.0, f);
+  const float ah = (float)w.c, al = (float)(w.c - ah), bh = (float)w.s, bl = (float)(w.s - bh);
+  const float2 a_hi = make_float2(ah, ah), a_lo = make_float2(al, al), b_hi = make_float2(bh, bh), b_lo = make_float2(bl, bl);
+  for (long long p0 = id / pairs * run; p0 < positions; p0 += (long long)groups * run) {
+    const Point z = point_of((double)(first + p0), f);
+    const double c = z.c * scale, s = z.s * scale;
+    float2 hi = make_float2((float)c, (float)s), lo = make_float2((float)(c - (double)hi.x), (float)(s - (double)hi.y));
+    float2* to = table + p0 * pairs + pair;
+    const int n = (int)min((long long)run, positions - p0);
+    *to = hi;
+#pragma unroll 4
+    for (int k = 1; k < n; ++k) {
+      to += pairs;
+      // (c, s) a + (-s, c) b
+      const float2 xh = make_float2(-hi.y, hi.x), xl = make_float2(-lo.y, lo.x);
+      const float2 u = __fmul2_rn(hi, a_hi), v = __fmul2_rn(xh, b_hi);
+      const float2 ue = __ffma2_rn(lo, a_hi, __ffma2_rn(hi, a_lo, __ffma2_rn(hi, a_hi, neg2(u))));
+      const float2 ve = __ffma2_rn(xl, b_hi, __ffma2_rn(xh, b_lo, __ffma2_rn(xh, b_hi, neg2(v))));
+      const float2 t = __fadd2_rn(u, v), d = __fadd2_rn(t, neg2(u));
+      const float2 e = __fadd2_rn(__fadd2_rn(u, neg2(__fadd2_rn(t, neg2(d)))), __fadd2_rn(v, neg2(d)));
+      const float2 r = __fadd2_rn(e, __fadd2_rn(ue, ve));
+      hi = __fadd2_rn(t, r);
+      lo = __fadd2_rn(r, neg2(__fadd2_rn(hi, neg2(t))));
+      *to = hi;
+    }
   }
 }
 
@@ -65,15 +131,19 @@ cudaError_t rows_typed(const RopeView& r, const RopeRows& a, cudaStream_t s) {
 
 cudaError_t launch_rope_table(const float* inv_freq, int pairs, long long first, long long positions, double scale,
                               float* table, cudaStream_t s) {
-  const long long entries = positions * pairs, blocks = (entries + TB_THREADS - 1) / TB_THREADS;
+  // runs as long as they may be that give every SM two CTAs; no more threads than the chip holds at a time
+  int run = TB_RUN;
+  while (run > 8 && (positions + run - 1) / run * pairs < 2ll * TB_THREADS * num_sms()) run /= 2;
+  const long long runs = (positions + run - 1) / run, most = ((long long)num_sms() * 2048 + pairs - 1) / pairs;
+  const int groups = (int)(runs < most ? runs : most);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(blocks < 16ll * num_sms() ? blocks : 16ll * num_sms()));
+  cfg.gridDim = dim3((unsigned)(((long long)groups * pairs + TB_THREADS - 1) / TB_THREADS));
   cfg.blockDim = dim3(TB_THREADS);
   cfg.stream = s;
   cudaLaunchAttribute attr[1] = {pdl_attr()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rope_table_kernel, inv_freq, pairs, first, entries, scale, (float2*)table);
+  return cudaLaunchKernelEx(&cfg, rope_table_kernel, inv_freq, pairs, first, positions, scale, run, groups, (float2*)table);
 }
 
 cudaError_t launch_rope_rows(const RopeView& r, const RopeRows& a, int type, cudaStream_t s) {

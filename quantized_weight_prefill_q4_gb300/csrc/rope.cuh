@@ -80,7 +80,8 @@ __device__ __forceinline__ RopeTurn rope_turn(const RopeView& r, const RopeUnit&
   return w;
 }
 
-// Every product, sum and difference rounded by itself, whatever the compiler would join.
+// Every product, sum and difference rounded by itself. (Packed products and sums, two pairs an instruction, are made
+// into fmas by the compiler, whatever their rounding is said to be.)
 __device__ __forceinline__ void rope_pair(float& x, float& y, float2 t) {
   const float a = __fsub_rn(__fmul_rn(x, t.x), __fmul_rn(y, t.y));
   y = __fadd_rn(__fmul_rn(y, t.x), __fmul_rn(x, t.y));
@@ -111,15 +112,28 @@ __device__ __forceinline__ Two two_add(const Two& a, const Two& b) {
   const Two s = two_sum(a.hi, b.hi);
   return Two{s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo))};
 }
-__device__ __forceinline__ Two two_add_square(const Two& a, float x) {
-  const float p = __fmul_rn(x, x);
-  return two_add(a, Two{p, __fmaf_rn(x, x, -p)});
+// The sum of a unit's squares; two at a time, each half with its own sum and what rounding took: exactly, also where
+// the compiler makes a square and a sum one fma. (Squares of 16-bit numbers are exact.)
+template <bool EXACT>
+__device__ __forceinline__ Two squares_of(const float (&x)[8]) {
+  float2 sum = __fmul2_rn(make_float2(x[0], x[1]), make_float2(x[0], x[1])), low = make_float2(0.f, 0.f);
+  if (!EXACT) low = __ffma2_rn(make_float2(x[0], x[1]), make_float2(x[0], x[1]), make_float2(-sum.x, -sum.y));
+#pragma unroll
+  for (int i = 2; i < 8; i += 2) {
+    const float2 y = make_float2(x[i], x[i + 1]), p = __fmul2_rn(y, y);
+    const float2 s = __fadd2_rn(sum, p), t = __fadd2_rn(s, make_float2(-sum.x, -sum.y));
+    const float2 u = __fadd2_rn(s, make_float2(-t.x, -t.y));
+    low = __fadd2_rn(low, __fadd2_rn(__fadd2_rn(sum, make_float2(-u.x, -u.y)), __fadd2_rn(p, make_float2(-t.x, -t.y))));
+    if (!EXACT) low = __fadd2_rn(low, __ffma2_rn(y, y, make_float2(-p.x, -p.y)));
+    sum = s;
+  }
+  return two_add(Two{sum.x, low.x}, Two{sum.y, low.y});
 }
-// f32(1 / sqrt(sum / n + eps)): one step of Newton's from the approximation's 22
+// f32(1 / sqrt(sum / n + eps)), inv_n = f32(1 / n): the quotient's residual by fma; one step of Newton's from the approximation's 22
 // bits, its residual by fma.
-__device__ __forceinline__ float rope_inverse_rms(const Two& sum, float n, float eps) {
-  const float q = __fdiv_rn(sum.hi, n);
-  const Two m = two_add(Two{q, __fdiv_rn(__fadd_rn(__fmaf_rn(-q, n, sum.hi), sum.lo), n)}, Two{eps, 0.f});
+__device__ __forceinline__ float rope_inverse_rms(const Two& sum, float n, float inv_n, float eps) {
+  const float q = __fmul_rn(sum.hi, inv_n);
+  const Two m = two_add(two_sum(q, __fmul_rn(__fadd_rn(__fmaf_rn(-q, n, sum.hi), sum.lo), inv_n)), Two{eps, 0.f});
   const float s = __fadd_rn(m.hi, m.lo), low = __fadd_rn(__fsub_rn(m.hi, s), m.lo);
   const float y = rsqrtf(s), p = __fmul_rn(y, y), e = __fmaf_rn(y, y, -p);
   const float t = __fmaf_rn(-s, e, __fmaf_rn(-s, p, 1.f)) - low * p;
@@ -163,7 +177,10 @@ __device__ __forceinline__ Vec8<T> vec8_of(const float (&x)[8]) {
 // Norm and rotation of a unit's values, w its norm weights.
 __device__ __forceinline__ void rope_norm(float (&x)[8], float inv, const float (&w)[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], inv), w[i]);
+  for (int i = 0; i < 8; i += 2) {
+    const float2 y = __fmul2_rn(__fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(inv, inv)), make_float2(w[i], w[i + 1]));
+    x[i] = y.x, x[i + 1] = y.y;
+  }
 }
 
 // ---------------------------------------------------------------- rows into rows
@@ -181,6 +198,7 @@ __device__ __forceinline__ void rope_rows_group(const RopeView& r, const RopeRow
   live = live && group / per_row < a.num_rows;
   const long long row = live ? group / per_row : 0;
   const int h0 = (int)(group % per_row) * a.heads_a_group, h1 = live ? min(h0 + a.heads_a_group, a.heads) : h0;
+  const float inv_dim = 1.f / (float)a.dim;
   RopeUnit unit[EACH];
   RopeTurn turn[EACH];
   float w[EACH][8];
@@ -218,12 +236,9 @@ __device__ __forceinline__ void rope_rows_group(const RopeView& r, const RopeRow
         }
       }
       if (a.norm) {
-        Two s = {0.f, 0.f};
-#pragma unroll
-        for (int e = 0; e < EACH; ++e)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) s = two_add_square(s, y[e][k]);
-        const float inv = rope_inverse_rms(two_group_sum<LANES>(s), (float)a.dim, a.eps);
+        Two s = squares_of<sizeof(T) == 2>(y[0]);
+        if constexpr (EACH == 2) s = two_add(s, squares_of<sizeof(T) == 2>(y[1]));
+        const float inv = rope_inverse_rms(two_group_sum<LANES>(s), (float)a.dim, inv_dim, a.eps);
 #pragma unroll
         for (int e = 0; e < EACH; ++e) rope_norm(y[e], inv, w[e]);
       }

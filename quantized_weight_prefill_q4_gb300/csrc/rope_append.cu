@@ -110,10 +110,7 @@ __global__ void __launch_bounds__(A_THREADS, 4) kv8_append_rope_kernel(const __g
     float x[8];
     values8(e, x);
     if (normed) {
-      Two s = {0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s = two_add_square(s, x[i]);
-      rope_norm(x, rope_inverse_rms(two_group_sum<ROW>(s), (float)D, a.eps), w);
+      rope_norm(x, rope_inverse_rms(two_group_sum<ROW>(squares_of<sizeof(T) == 2>(x)), (float)D, 1.f / D, a.eps), w);
     }
     if (live && unit.pair >= 0) {
       const int pos = lo + row0 + j * STEP;
