@@ -103,12 +103,8 @@ __global__ void __launch_bounds__(RR_THREADS) rope_rows_kernel(const __grid_cons
 
 template <typename T, int LANES, int EACH>
 cudaError_t rows_shape(const RopeView& r, RopeRows a, cudaStream_t s) {
-  // heads of a group: as many as leave every SM some CTAs
-  a.heads_a_group = a.heads;
   constexpr int GROUPS = RR_THREADS / LANES;
-  while (a.heads_a_group > 1 &&
-         (long long)a.num_rows * ((a.heads + a.heads_a_group - 1) / a.heads_a_group) < (long long)GROUPS * 8 * num_sms())
-    a.heads_a_group = (a.heads_a_group + 1) / 2;
+  a.heads_a_group = rope_heads_a_group(a.num_rows, a.heads, GROUPS * 8ll * num_sms());
   const long long groups = (long long)a.num_rows * ((a.heads + a.heads_a_group - 1) / a.heads_a_group);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((groups + GROUPS - 1) / GROUPS));

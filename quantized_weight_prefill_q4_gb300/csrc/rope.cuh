@@ -56,17 +56,19 @@ __device__ __forceinline__ RopeUnit rope_unit(const RopeView& r, int u) {
 struct RopeTurn {
   float2 t[4];
 };
-__device__ __forceinline__ int rope_position(const RopeView& r, int axis, int row, int own) {
+// (`bad` where the table does not have the position: told at once, so that no load waits for a report.)
+__device__ __forceinline__ int rope_position(const RopeView& r, int axis, int row, int own, bool& bad) {
   const int p = r.positions ? r.positions[axis * r.positions_ld + row] : max(own, 0);
-  if ((unsigned)p < (unsigned)r.num_positions) return p;
-  atomicOr(r.status, kStatusBadIndex);
-  return 0;
+  const bool here = (unsigned)p < (unsigned)r.num_positions;
+  bad |= !here;
+  return here ? p : 0;
 }
 __device__ __forceinline__ RopeTurn rope_turn(const RopeView& r, const RopeUnit& u, int row, int own) {
   RopeTurn w;
   if (u.pair < 0) return w;
   const int a = (int)(u.axes & 255);
-  const float2* at = r.table + (size_t)rope_position(r, a, row, own) * r.pairs + u.pair;
+  bool bad = false;
+  const float2* at = r.table + (size_t)rope_position(r, a, row, own, bad) * r.pairs + u.pair;
   if (u.axes == a * 0x01010101u) {
     const float4 x = reinterpret_cast<const float4*>(at)[0], y = reinterpret_cast<const float4*>(at)[1];
     w.t[0] = make_float2(x.x, x.y), w.t[1] = make_float2(x.z, x.w);
@@ -75,8 +77,9 @@ __device__ __forceinline__ RopeTurn rope_turn(const RopeView& r, const RopeUnit&
     w.t[0] = at[0];
 #pragma unroll
     for (int i = 1; i < 4; ++i)
-      w.t[i] = r.table[(size_t)rope_position(r, (int)(u.axes >> 8 * i & 255), row, own) * r.pairs + u.pair + i];
+      w.t[i] = r.table[(size_t)rope_position(r, (int)(u.axes >> 8 * i & 255), row, own, bad) * r.pairs + u.pair + i];
   }
+  if (bad) atomicOr(r.status, kStatusBadIndex);
   return w;
 }
 
@@ -139,13 +142,23 @@ __device__ __forceinline__ float rope_inverse_rms(const Two& sum, float n, float
   const float t = __fmaf_rn(-s, e, __fmaf_rn(-s, p, 1.f)) - low * p;
   return __fmaf_rn(__fmul_rn(y, 0.5f), t, y);
 }
-// The sum over a group of LANES neighbouring lanes, for all of them.
+// rope_inverse_rms of four heads, each lane of a group of LANES with a part of each one's sum of squares: two
+// steps hand half of the heads to the neighbour, so that each lane goes on with one head and takes one root
+// (5 sums of two numbers instead of 16 for 16 lanes).
 template <int LANES>
-__device__ __forceinline__ Two two_group_sum(Two s) {
+__device__ __forceinline__ void rope_inverse_rms4(const Two (&s)[4], float n, float inv_n, float eps, float (&inv)[4]) {
+  const int lane = threadIdx.x & 31;
+  const bool b0 = lane & 1, b1 = lane & 2;
+  auto take = [](const Two& mine, const Two& other, int o) {
+    return two_add(mine, Two{__shfl_xor_sync(0xffffffffu, other.hi, o), __shfl_xor_sync(0xffffffffu, other.lo, o)});
+  };
+  const Two x = take(b0 ? s[2] : s[0], b0 ? s[0] : s[2], 1), y = take(b0 ? s[3] : s[1], b0 ? s[1] : s[3], 1);
+  Two z = take(b1 ? y : x, b1 ? x : y, 2);
 #pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1)
-    s = two_add(s, Two{__shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o)});
-  return s;
+  for (int o = 4; o < LANES; o *= 2) z = take(z, z, o);
+  const float r = rope_inverse_rms(z, n, inv_n, eps);
+#pragma unroll
+  for (int h = 0; h < 4; ++h) inv[h] = __shfl_sync(0xffffffffu, r, (lane & ~3) | h >> 1 | (h & 1) << 1);
 }
 
 // ---------------------------------------------------------------- elements
@@ -184,6 +197,13 @@ __device__ __forceinline__ void rope_norm(float (&x)[8], float inv, const float 
 }
 
 // ---------------------------------------------------------------- rows into rows
+// Heads that a group of lanes does of one row: all, or as few as it takes to have `want` groups.
+inline int rope_heads_a_group(long long rows, int heads, long long want) {
+  int each = heads;
+  while (each > 1 && rows * ((heads + each - 1) / each) < want) each = (each + 1) / 2;
+  return each;
+}
+
 // The row of group `group`, which may be past the last one.
 __device__ __forceinline__ long long rope_row_of(const RopeRows& a, long long group) {
   return group / ((a.heads + a.heads_a_group - 1) / a.heads_a_group);
@@ -193,7 +213,7 @@ __device__ __forceinline__ long long rope_row_of(const RopeRows& a, long long gr
 template <typename T, int LANES, int EACH>
 __device__ __forceinline__ void rope_rows_group(const RopeView& r, const RopeRows& a, long long group, int lane,
                                                 int own, bool live) {
-  constexpr int BATCH = EACH == 1 ? 4 : 2;  // heads whose values are on their way together
+  constexpr int BATCH = 4;  // heads whose values are on their way together
   const int per_row = (a.heads + a.heads_a_group - 1) / a.heads_a_group;
   live = live && group / per_row < a.num_rows;
   const long long row = live ? group / per_row : 0;
@@ -222,33 +242,34 @@ __device__ __forceinline__ void rope_rows_group(const RopeView& r, const RopeRow
 #pragma unroll
       for (int e = 0; e < EACH; ++e)
         if (mine[e] && h0 + i + j < h1) v[j][e] = load44(x + (size_t)(h0 + i + j) * a.dim, unit[e].d0, unit[e].d1);
+    float inv[BATCH];
+    if (a.norm) {
+      Two sum[BATCH];
 #pragma unroll
-    for (int j = 0; j < BATCH; ++j) {
-      const int h = h0 + i + j;
-      float y[EACH][8];
+      for (int j = 0; j < BATCH; ++j) {
+        sum[j] = Two{0.f, 0.f};
 #pragma unroll
-      for (int e = 0; e < EACH; ++e) {
-        if (mine[e] && h < h1) {
-          values8(v[j][e], y[e]);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) y[e][k] = 0.f;
-        }
+        for (int e = 0; e < EACH; ++e)
+          if (mine[e] && h0 + i + j < h1) {
+            float y[8];
+            values8(v[j][e], y);
+            const Two x = squares_of<sizeof(T) == 2>(y);
+            sum[j] = e ? two_add(sum[j], x) : x;
+          }
       }
-      if (a.norm) {
-        Two s = squares_of<sizeof(T) == 2>(y[0]);
-        if constexpr (EACH == 2) s = two_add(s, squares_of<sizeof(T) == 2>(y[1]));
-        const float inv = rope_inverse_rms(two_group_sum<LANES>(s), (float)a.dim, inv_dim, a.eps);
+      rope_inverse_rms4<LANES>(sum, (float)a.dim, inv_dim, a.eps, inv);
+    }
 #pragma unroll
-        for (int e = 0; e < EACH; ++e) rope_norm(y[e], inv, w[e]);
-      }
+    for (int j = 0; j < BATCH; ++j)
 #pragma unroll
       for (int e = 0; e < EACH; ++e)
-        if (mine[e] && h < h1) {
-          rope_rotate(r, unit[e], turn[e], y[e]);
-          store44(out + (size_t)h * a.dim, unit[e].d0, unit[e].d1, vec8_of<T>(y[e]));
+        if (mine[e] && h0 + i + j < h1) {
+          float y[8];
+          values8(v[j][e], y);
+          if (a.norm) rope_norm(y, inv[j], w[e]);
+          rope_rotate(r, unit[e], turn[e], y);
+          store44(out + (size_t)(h0 + i + j) * a.dim, unit[e].d0, unit[e].d1, vec8_of<T>(y));
         }
-    }
   }
 }
 

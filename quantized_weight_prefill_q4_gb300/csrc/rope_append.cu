@@ -16,6 +16,9 @@
 namespace apr {
 namespace {
 
+// K's CTAs of an SM that the heads are divided for, where each looks its page's turns up first.
+constexpr int K_CTAS = 3;
+
 struct AppendArgs {
   Kv8View v;
   RopeView r;
@@ -24,19 +27,23 @@ struct AppendArgs {
   long long ld;
   const float* k_norm;
   float eps;
-  int heads_a_cta;
+  int k_heads, v_heads;  // that a CTA takes one after the other
   unsigned append_ctas;  // the CTAs behind them are q's
+  int staged;            // bytes of a page's cosines and sines, where they are looked up once for all heads
+  int kept;              // a head's rows fit shared memory
   RopeRows q;            // heads 0: none
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(A_THREADS, 4) kv8_append_rope_kernel(const __grid_constant__ AppendArgs a) {
+// TH threads: 128 where a page's rows have no more units.
+template <typename T, int D, int TH>
+__global__ void __launch_bounds__(TH, TH == 128 ? 4 : (sizeof(T) == 4 ? 2 : 3)) kv8_append_rope_kernel(const __grid_constant__ AppendArgs a) {
   grid_dependency_wait();
   grid_launch_dependents();
+  extern __shared__ __align__(16) uint8_t smem[];  // [rows][pairs] cosines, then sines; a head's rows
   const Kv8View& v = a.v;
   constexpr int ROW = D / 8;  // units of a head, and lanes of a group
   if (blockIdx.x >= a.append_ctas) {
-    const long long group = (long long)(blockIdx.x - a.append_ctas) * (A_THREADS / ROW) + threadIdx.x / ROW;
+    const long long group = (long long)(blockIdx.x - a.append_ctas) * (TH / ROW) + threadIdx.x / ROW;
     const int row = (int)min(rope_row_of(a.q, group), (long long)v.num_rows - 1);
     // rows ahead of the first sequence's and behind the last one's are nobody's
     const bool live = !v.row_start || (row >= v.row_start[0] && row < v.row_start[v.num_seqs]);
@@ -60,13 +67,13 @@ __global__ void __launch_bounds__(A_THREADS, 4) kv8_append_rope_kernel(const __g
     rope_rows_group<T, ROW, 1>(a.r, a.q, group, threadIdx.x % ROW, own, live);
     return;
   }
-  const int parts = 2 * ((v.kv_heads + a.heads_a_cta - 1) / a.heads_a_cta);
-  const int index_of_unit = (int)(blockIdx.x / parts), part = (int)(blockIdx.x % parts);
-  constexpr int HELD = 16 / sizeof(T);  // vectors of 8 values a thread keeps between the passes, 32 registers
-  constexpr int STEP = A_THREADS / ROW;  // rows from one of a thread's vectors to the next
-  __shared__ float s_max[3][A_WARPS];
-  const bool is_v = part & 1;
-  const int g0 = (part >> 1) * a.heads_a_cta, g1 = min(g0 + a.heads_a_cta, v.kv_heads);
+  const int k_parts = (v.kv_heads + a.k_heads - 1) / a.k_heads, v_parts = (v.kv_heads + a.v_heads - 1) / a.v_heads;
+  const int index_of_unit = (int)(blockIdx.x / (k_parts + v_parts)), part = (int)(blockIdx.x % (k_parts + v_parts));
+  constexpr int STEP = TH / ROW;  // rows from one of a thread's vectors to the next
+  __shared__ float s_max[3][TH / 32];
+  const bool is_v = part >= k_parts;
+  const int g0 = is_v ? (part - k_parts) * a.v_heads : part * a.k_heads;
+  const int g1 = min(g0 + (is_v ? a.v_heads : a.k_heads), v.kv_heads);
 
   // ---- which page: the slot-th that the sequence's rows go to, if it has so many
   int b = index_of_unit, slot = 0;
@@ -90,7 +97,6 @@ __global__ void __launch_bounds__(A_THREADS, 4) kv8_append_rope_kernel(const __g
   const int lo = max(max(first, 0), page0), hi = min(len, page0 + (1 << v.page_shift));
   const int held = lo - page0;
   const int nvec = (hi - lo) * ROW;
-  const int nvec_all = (nvec + 31) & ~31;  // whole warps go through a norm together
   // this thread's vectors: one unit, every STEP-th row
   const int u = (int)threadIdx.x % ROW, row0 = (int)threadIdx.x / ROW;
   const RopeUnit unit = is_v ? RopeUnit{8 * u, 8 * u + 4, -1, 0} : rope_unit(a.r, u);
@@ -101,49 +107,107 @@ __global__ void __launch_bounds__(A_THREADS, 4) kv8_append_rope_kernel(const __g
     values8(x, w);
   }
   const T* src = static_cast<const T*>(is_v ? a.vv : a.k) + (long long)(span.r0 + lo - first + row0) * a.ld + (size_t)g0 * D;
-  // vector j of head g as it goes into the cache
-  auto vector = [&](int j, const T* from) -> Vec8<T> {
-    Vec8<T> e = {};
-    const bool live = (int)threadIdx.x + j * A_THREADS < nvec;
-    if (live) e = load44(from + (long long)j * STEP * a.ld, unit.d0, unit.d1);
-    if (is_v) return e;
-    float x[8];
-    values8(e, x);
+  const int rows = hi - lo;
+  float* s_turn = reinterpret_cast<float*>(smem);
+  Vec8<T>* s_rows = reinterpret_cast<Vec8<T>*>(smem + a.staged);
+  const bool staged = !is_v && a.staged;
+  if (staged) {
+    // the page's cosines and sines, for all the heads
+    // (a thread a pair, every few rows)
+    const int pairs = a.r.pairs, i = (int)threadIdx.x % pairs, step = TH / pairs;
+    int axis = a.r.axis ? a.r.axis[i] : 0;
+    if (axis >= a.r.num_axes) axis = 0;  // (flagged by rope_unit)
+    const float2* column = a.r.table + i;
+    if ((int)threadIdx.x < step * pairs) {
+      bool bad = false;
+      for (int row0 = (int)threadIdx.x / pairs; row0 < rows; row0 += 8 * step) {
+        float2 t[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int row = min(row0 + k * step, rows - 1);
+          t[k] = column[(size_t)rope_position(a.r, axis, span.r0 + lo - first + row, lo + row, bad) * pairs];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int row = row0 + k * step;
+          if (row < rows) {
+            s_turn[row * pairs + i] = t[k].x;
+            s_turn[(rows + row) * pairs + i] = t[k].y;
+          }
+        }
+      }
+      if (bad) atomicOr(a.r.status, kStatusBadIndex);
+    }
+    __syncthreads();
+  }
+  // vector j's cosines and sines
+  auto turn_of = [&](int j) -> RopeTurn {
+    const int row = row0 + j * STEP;
+    if (!staged) return rope_turn(a.r, unit, span.r0 + lo - first + row, lo + row);
+    const float4 c = *reinterpret_cast<const float4*>(s_turn + row * a.r.pairs + unit.pair);
+    const float4 t = *reinterpret_cast<const float4*>(s_turn + (rows + row) * a.r.pairs + unit.pair);
+    return RopeTurn{{make_float2(c.x, t.x), make_float2(c.y, t.y), make_float2(c.z, t.z), make_float2(c.w, t.w)}};
+  };
+  auto is_live = [&](int j) { return (int)threadIdx.x + j * TH < nvec; };
+  // vectors j .. j + 3 of a head as they go into the cache
+  auto vectors = [&](int j, const T* from, Vec8<T> (&e)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      e[i] = Vec8<T>{};
+      if (is_live(j + i)) e[i] = load44(from + (long long)(j + i) * STEP * a.ld, unit.d0, unit.d1);
+    }
+    if (is_v) return;
+    float inv[4];
     if (normed) {
-      rope_norm(x, rope_inverse_rms(two_group_sum<ROW>(squares_of<sizeof(T) == 2>(x)), (float)D, 1.f / D, a.eps), w);
+      Two sum[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float x[8];
+        values8(e[i], x);
+        sum[i] = squares_of<sizeof(T) == 2>(x);
+      }
+      rope_inverse_rms4<ROW>(sum, (float)D, 1.f / D, a.eps, inv);
     }
-    if (live && unit.pair >= 0) {
-      const int pos = lo + row0 + j * STEP;
-      rope_rotate(a.r, unit, rope_turn(a.r, unit, span.r0 + pos - first, pos), x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!is_live(j + i)) continue;
+      float x[8];
+      values8(e[i], x);
+      if (normed) rope_norm(x, inv[i], w);
+      if (unit.pair >= 0) rope_rotate(a.r, unit, turn_of(j + i), x);
+      e[i] = vec8_of<T>(x);
     }
-    return vec8_of<T>(x);
   };
   int8_t* codes = (is_v ? v.V : v.K) + kv8_codes_at(v, page, g0);
   float* scale = (is_v ? v.v_scale : v.k_scale) + kv8_scale_at(v, page, g0);
   for (int g = g0; g < g1; ++g, src += D, codes += (size_t)D << v.page_shift, ++scale) {
     const float s_old = held > 0 ? *scale : 0.f;
     // ---- the largest magnitude
-    Vec8<T> keep[HELD];
     float m = 0.f;
+#pragma unroll 1
+    for (int j = 0; j * TH < nvec; j += 4) {
+      Vec8<T> e[4];
+      vectors(j, src, e);
 #pragma unroll
-    for (int j = 0; j < HELD; ++j)
-      if ((int)threadIdx.x + j * A_THREADS < nvec_all) {
-        keep[j] = vector(j, src);
-        if ((int)threadIdx.x + j * A_THREADS < nvec) m = amax_of(keep[j], m);
-      }
-    for (int j = HELD; (int)threadIdx.x + j * A_THREADS < nvec_all; ++j) {
-      const Vec8<T> e = vector(j, src);
-      if ((int)threadIdx.x + j * A_THREADS < nvec) m = amax_of(e, m);
+      for (int i = 0; i < 4; ++i)
+        if (is_live(j + i)) {
+          m = amax_of(e[i], m);
+          if (a.kept) s_rows[(j + i) * TH + threadIdx.x] = e[i];
+        }
     }
-    m = block_max<A_WARPS>(m, s_max[g & 1]);  // (the next head writes the other: one barrier a head)
+    m = block_max<TH / 32>(m, s_max[g & 1]);  // (the next head writes the other: one barrier a head)
     if (m > FLT_MAX) {                        // an infinity among them, for the whole CTA
       m = 0.f;
-      for (int j = 0; (int)threadIdx.x + j * A_THREADS < nvec_all; ++j) {
-        const Vec8<T> e = vector(j, src);
-        if ((int)threadIdx.x + j * A_THREADS < nvec) m = finite_amax_of<T>(e, m);
+#pragma unroll 1
+      for (int j = 0; j * TH < nvec; j += 4) {
+        Vec8<T> e[4];
+        vectors(j, src, e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (is_live(j + i)) m = finite_amax_of<T>(e[i], m);
       }
       __syncthreads();
-      m = block_max<A_WARPS>(m, s_max[2]);
+      m = block_max<TH / 32>(m, s_max[2]);
     }
 
     // ---- the scale, and what the page held under a raised one
@@ -151,7 +215,7 @@ __global__ void __launch_bounds__(A_THREADS, 4) kv8_append_rope_kernel(const __g
     if (threadIdx.x == 0 && (held == 0 || s.s > s_old)) *scale = s.s;
     if (held > 0 && s.s > s_old) {
       uint4* old = reinterpret_cast<uint4*>(codes);
-      for (int i = threadIdx.x; i < held * D / 16; i += A_THREADS) {
+      for (int i = threadIdx.x; i < held * D / 16; i += TH) {
         const uint4 x = old[i];
         uint4 y = kv8_requantise16(x, s_old, s);
         // (a code of -128 may have come from elsewhere)
@@ -169,48 +233,70 @@ __global__ void __launch_bounds__(A_THREADS, 4) kv8_append_rope_kernel(const __g
       *reinterpret_cast<uint32_t*>(p + unit.d0) = c.x;
       *reinterpret_cast<uint32_t*>(p + unit.d1) = c.y;
     };
+#pragma unroll 1
+    for (int j = 0; j * TH < nvec; j += 4) {
+      Vec8<T> e[4];
+      if (a.kept) {
 #pragma unroll
-    for (int j = 0; j < HELD; ++j)
-      if ((int)threadIdx.x + j * A_THREADS < nvec) store(j, keep[j]);
-    for (int j = HELD; (int)threadIdx.x + j * A_THREADS < nvec_all; ++j) {
-      const Vec8<T> e = vector(j, src);
-      if ((int)threadIdx.x + j * A_THREADS < nvec) store(j, e);
+        for (int i = 0; i < 4; ++i)
+          if (is_live(j + i)) e[i] = s_rows[(j + i) * TH + threadIdx.x];
+      } else {
+        vectors(j, src, e);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (is_live(j + i)) store(j + i, e[i]);
     }
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, int TH>
 cudaError_t append_shape(AppendArgs& a, cudaStream_t s) {
   const Kv8View& v = a.v;
   // the most pages that the rows can touch (first_append_unit)
   const long long pages = v.row_start ? (v.num_rows >> v.page_shift) + 2ll * v.num_seqs : v.num_seqs;
-  a.heads_a_cta = heads_a_cta(pages, v.kv_heads, 12);
-  a.append_ctas = (unsigned)(pages * 2 * ((v.kv_heads + a.heads_a_cta - 1) / a.heads_a_cta));
-  constexpr int GROUPS = A_THREADS / (D / 8);
+  // the turns of a page's rows, but no more rows than a sequence has
+  const size_t rows = v.max_rows < 1 << v.page_shift ? v.max_rows : 1 << v.page_shift;
+  const size_t turns = rows * a.r.pairs * 8, held = rows * D * sizeof(T);
+  a.staged = rows >= 16 && turns <= 64 * 1024 && v.kv_heads > 1 ? (int)turns : 0;
+  a.kept = held <= 64 * 1024;
+  a.v_heads = heads_a_cta(pages, v.kv_heads, 12);
+  a.k_heads = a.staged ? heads_a_cta(pages, v.kv_heads, K_CTAS) : a.v_heads;
+  a.append_ctas = (unsigned)(pages * ((v.kv_heads + a.k_heads - 1) / a.k_heads + (v.kv_heads + a.v_heads - 1) / a.v_heads));
+  constexpr int GROUPS = TH / (D / 8);
   long long q_ctas = 0;
   if (a.q.heads > 0) {
-    a.q.heads_a_group = a.q.heads < 4 ? a.q.heads : 4;
+    a.q.heads_a_group = rope_heads_a_group(v.num_rows, a.q.heads, GROUPS * 8ll * num_sms());
     q_ctas = ((long long)v.num_rows * ((a.q.heads + a.q.heads_a_group - 1) / a.q.heads_a_group) + GROUPS - 1) / GROUPS;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.append_ctas + q_ctas));
-  cfg.blockDim = dim3(A_THREADS);
+  cfg.blockDim = dim3(TH);
+  cfg.dynamicSmemBytes = (a.staged ? turns : 0) + (a.kept ? held : 0);
+  if (cfg.dynamicSmemBytes > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kv8_append_rope_kernel<T, D, TH>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
+    if (e != cudaSuccess) return e;
+  }
   cfg.stream = s;
   cudaLaunchAttribute attr[1] = {pdl_attr()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_append_rope_kernel<T, D>, a);
+  return cudaLaunchKernelEx(&cfg, kv8_append_rope_kernel<T, D, TH>, a);
+}
+template <typename T, int D>
+cudaError_t append_sized(AppendArgs& a, cudaStream_t s) {
+  return a.v.max_rows * (D / 8) <= 128 ? append_shape<T, D, 128>(a, s) : append_shape<T, D, 256>(a, s);
 }
 template <typename T>
 cudaError_t append_typed(AppendArgs& a, cudaStream_t s) {
-  return a.v.dim == 64 ? append_shape<T, 64>(a, s) : (a.v.dim == 128 ? append_shape<T, 128>(a, s) : append_shape<T, 256>(a, s));
+  return a.v.dim == 64 ? append_sized<T, 64>(a, s) : (a.v.dim == 128 ? append_sized<T, 128>(a, s) : append_sized<T, 256>(a, s));
 }
 
 }  // namespace
 
 cudaError_t launch_rope_kv8_append(const Kv8View& v, const RopeView& r, int type, const void* k, const void* vv,
                                    long long ld, const float* k_norm, float eps, const RopeRows& q, cudaStream_t s) {
-  AppendArgs a{v, r, k, vv, ld, k_norm, eps, 0, 0, q};
+  AppendArgs a{v, r, k, vv, ld, k_norm, eps, 0, 0, 0, 0, 0, q};
   if (type == APR_T_F32) return append_typed<float>(a, s);
   if (type == APR_T_F16) return append_typed<__half>(a, s);
   return append_typed<__nv_bfloat16>(a, s);
