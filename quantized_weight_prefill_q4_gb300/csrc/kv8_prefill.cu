@@ -66,7 +66,7 @@ struct Shape {
   static constexpr bool TWO = TWO_;                        // two fp16 pieces of q and of the weights
   static constexpr int MT = D <= 128 ? 2 : 1;              // M tiles
   static constexpr int PAIRS = 128 * MT;
-  static constexpr int KT = D <= 128 && !TWO ? 128 : 64;   // keys of a tile
+  static constexpr int KT = 64;                            // keys of a tile
   static constexpr int GROUPS = KT / 32;                   // of 32 positions, within one page each
   static constexpr int PIECES = TWO ? 2 : 1;
   static constexpr int PANEL = KT * 128;                   // bytes of 64 dims of a tile
@@ -81,22 +81,22 @@ struct Shape {
   static constexpr int SMEM = Q_BYTES + SLOTS * SLOT + RAWS * RAW + 1024;
   static constexpr int SOFT = 4 * MT, CONV = MMA_WARP - SOFT;  // warps
   // registers a thread of each role; as launched: 128
-  static constexpr int SOFT_REGS = MT == 2 ? 200 : 208, CONV_REGS = MT == 2 ? 56 : 88, MMA_REGS = MT == 2 ? 56 : 128;
+  static constexpr int SOFT_REGS = MT == 2 ? 160 : 208, CONV_REGS = MT == 2 ? 96 : 88, MMA_REGS = MT == 2 ? 96 : 128;
   static_assert(32 * (SOFT * SOFT_REGS + CONV * CONV_REGS + 4 * MMA_REGS) <= THREADS * 128, "registers");
   static constexpr int EACH = KT * D / 16 / (32 * CONV);   // 16-byte pieces of a chunk that a converter thread has
-  // tensor memory columns: O of each M tile, then two buffers of scores, then (where there is room) two of weights
+  // tensor memory columns: O of each M tile, then two buffers of scores for each, which the weights take over
   static constexpr int COL_S = MT * D;
-  static constexpr int P_COLS = PIECES * KT / 2;
-  static constexpr bool OWN_P = COL_S + 2 * KT + 2 * P_COLS <= 512;
-  static constexpr int COL_P = OWN_P ? COL_S + 2 * KT : COL_S;
-  static constexpr int P_STEP = OWN_P ? P_COLS : KT;
-  static_assert(COL_S + 2 * KT <= 512 && (OWN_P || !TWO), "tensor memory");
+  static_assert(COL_S + 2 * MT * KT <= 512 && PIECES * KT / 2 <= KT, "tensor memory");
   static_assert(SLOTS >= 2 && RAWS >= 2 && SMEM + 1024 <= 232448, "shared memory");
   static_assert(EACH >= 1 && KT * D / 16 % (32 * CONV) == 0, "converters");
   static constexpr int FOLD_TILES = FOLD / KT;
 };
 
 // ---------------------------------------------------------------- the work
+// a / b of numbers that are not negative, in 32 bits where they are that small (a division of 64 takes hundreds of cycles).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
 // A sequence's segments: of `rows` rows at positions first .. len - 1.
 struct Work {
   int len, first, r0, n;
@@ -132,20 +132,15 @@ __device__ __forceinline__ long long cost_all(const PrefillArgs& a, const Work& 
 template <class S>
 __device__ __forceinline__ int key_tiles(const PrefillArgs& a, const Work& w, int t) {
   const long long last = min(w.pairs, (long long)(t + 1) * S::PAIRS) - 1;
-  const int sees = w.first + (int)(last / a.group) + 1;
+  const int sees = w.first + (int)quotient(last, a.group) + 1;
   return max(1, (sees + S::KT - 1) / S::KT);
 }
 // The key tile of a segment that a share begins with which begins `at` into the segment's cost.
 template <class S>
 __device__ __forceinline__ int tile_at(const PrefillArgs& a, long long at, int tiles) {
   const long long in = at - (long long)START * a.group, step = (long long)S::KT * a.group;
-  return in <= 0 ? 0 : (int)min((long long)tiles, (in + step - 1) / step);
+  return in <= 0 ? 0 : (int)min((long long)tiles, quotient(in + step - 1, step));
 }
-// Where CTA c's share of `total` begins, of `ctas`.
-__device__ __forceinline__ long long share_begin(int c, int ctas, long long total) {
-  return (long long)((unsigned long long)total / ctas) * c + (long long)((unsigned long long)total % ctas) * c / ctas;
-}
-
 // A piece, as the roles see it: key tiles k0 .. k1 - 1 of the `tiles` of a segment (k1 == 0: no more pieces).
 struct Piece {
   int b, g;          // sequence and KV head
@@ -158,11 +153,11 @@ struct Piece {
 // The pieces of a CTA's share, one after the other; a whole warp calls it.
 template <class S>
 struct Pieces {
-  int b, ctas;
-  long long u, end, seq_u0, total;
+  int b;
+  long long u, end, seq_u0, share, total;  // CTA c's share: share * c .. share * (c + 1) - 1, within the total
 
-  // The next piece, and of how many pieces its segment is made where the piece begins it (by CTA c).
-  __device__ bool next(const PrefillArgs& a, int c, Piece& p, int& t, int& made_of) {
+  // The next piece, and of how many pieces its segment is made where the piece begins it.
+  __device__ bool next(const PrefillArgs& a, Piece& p, int& t, int& made_of) {
     const int lane = threadIdx.x & 31;
     while (u < end && b < a.v.num_seqs) {
       const Work w = work_of<S>(a, b);
@@ -195,7 +190,7 @@ struct Pieces {
       const long long before = a.v.kv_heads * cost_before<S>(w, lo), one = cost<S>(w, lo);
       t = lo;
       p.b = b;
-      p.g = (int)min((at - before) / one, (long long)a.v.kv_heads - 1);
+      p.g = (int)min(quotient(at - before, one), (long long)a.v.kv_heads - 1);
       const long long seg_u0 = seq_u0 + before + p.g * one, seg_end = seg_u0 + one;
       p.tiles = key_tiles<S>(a, w, lo);
       p.k0 = u == seg_u0 ? 0 : tile_at<S>(a, u - seg_u0, p.tiles);
@@ -207,10 +202,7 @@ struct Pieces {
       p.np = (int)min((long long)S::PAIRS, w.pairs - p.p0);
       made_of = 1;
       if (p.k0 == 0 && p.k1 < p.tiles)
-        for (++c; c < ctas; ++c, ++made_of) {
-          const long long x = share_begin(c, ctas, total);
-          if (x >= seg_end || tile_at<S>(a, x - seg_u0, p.tiles) >= p.tiles) break;
-        }
+        for (long long x = end; x < min(seg_end, total) && tile_at<S>(a, x - seg_u0, p.tiles) < p.tiles; x += share) ++made_of;
       return true;
     }
     return false;
@@ -244,18 +236,20 @@ __device__ __forceinline__ uint32_t group_at(const PrefillArgs& a, const Piece& 
   return (uint32_t)(kv8_scale_at(a.v, page, p.g) << (a.v.page_shift - 5)) +
          (uint32_t)((pos >> 5) & ((1 << (a.v.page_shift - 5)) - 1));
 }
-// The scales of a group of 32 positions, V's as a logarithm too.
+// The scales of a group of 32 positions.
 struct GroupScales {
-  float k, v, log2_v;
+  float k, v;
 };
 __device__ __forceinline__ GroupScales group_scales(const PrefillArgs& a, const Piece& p, int group) {
-  if (group * 32ll >= p.len) return GroupScales{0.f, 0.f, 0.f};
+  if (group * 32ll >= p.len) return GroupScales{0.f, 0.f};
   const size_t at = kv8_scale_at(a.v, max(kv8_page(a.v, p.b, group * 32 >> a.v.page_shift), 0), p.g);
-  const float x = a.v.v_scale[at];
-  return GroupScales{a.v.k_scale[at], x, log2f(x)};
+  return GroupScales{a.v.k_scale[at], a.v.v_scale[at]};
 }
 
 // ---------------------------------------------------------------- tensor core operands
+// D[tmem] (+)= A . B, both from shared memory. As for mma_f16_ts_elect, the warp stays together and what the
+// instruction takes is the same for all of it, known to be so from a shuffle: in uniform registers, where
+// a product takes them from (from others each took 100 cycles to issue).
 __device__ __forceinline__ void mma_f16_ss_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                  uint32_t accumulate) {
   asm volatile(
@@ -264,10 +258,12 @@ __device__ __forceinline__ void mma_f16_ss_elect(uint32_t d_tmem, uint64_t adesc
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// V as the second product's B: N (dims) contiguous, 64 of them a 128-byte row, panels of 64 dims `panel`
-// bytes apart (leading byte offset), groups of 8 positions 1024 (stride byte offset).
-__device__ __forceinline__ uint64_t smem_desc_n_major(const void* tile, uint32_t panel) {
-  return (smem_desc_sw128(tile) & ~((uint64_t)0x3fff << 16)) | (uint64_t)(panel >> 4) << 16;
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+// A shared memory descriptor but for its start address: rows of 128 bytes, swizzled, groups of 8 of them 1024
+// bytes apart (stride byte offset), the next 64 columns `panel` bytes on (leading byte offset: counts where N is contiguous, as
+// in V as the second product's B).
+constexpr uint64_t operand_desc(uint32_t panel) {
+  return (uint64_t)(panel >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 constexpr uint32_t N_MAJOR_B = 1u << 16;
 
@@ -321,7 +317,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
   uint8_t* sQ = smem;
   uint8_t* ring = smem + S::Q_BYTES;
   uint8_t* raw = ring + S::SLOTS * S::SLOT;
-  __shared__ uint64_t raw_full[S::RAWS], raw_empty[S::RAWS], full[S::SLOTS], empty[S::SLOTS], q_full[2], s_full[2], p_full[2], o_done[2], o_last[2], piece_full[2],
+  __shared__ uint64_t raw_full[S::RAWS], raw_empty[S::RAWS], full[S::SLOTS], empty[S::SLOTS], q_full[2], s_full[4], p_full[4], o_done[2], o_last[2], piece_full[2],
       piece_empty[2], drain;
   __shared__ Piece s_piece[2];
   __shared__ uint32_t tmem_holder;
@@ -330,7 +326,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
   __shared__ int s_found_b;
   volatile int* abort_flag = abort_words;
   const Kv8View& v = a.v;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
 
   // ---- what the sequences cost, and where this CTA's share begins: a thread counts `run` neighbouring sequences
   const int run = (v.num_seqs + THREADS - 1) / THREADS;
@@ -355,8 +351,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 4);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&s_full[2 * i], 1);
+      mbar_init(&s_full[2 * i + 1], 1);
+      mbar_init(&p_full[2 * i], 4);
+      mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&o_done[i], 1);
       mbar_init(&o_last[i], 1);
       mbar_init(&piece_full[i], 1);
@@ -379,9 +377,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
     if (w < warp) my_u0 += s_scan[w];
     total += s_scan[w];
   }
-  const int ctas = (int)max(1ll, min((long long)a.ctas, total / ((long long)MIN_TILES * S::KT * a.group)));
-  const bool idle = (int)blockIdx.x >= ctas || total <= 0;
-  const long long u = idle ? 0 : share_begin(blockIdx.x, ctas, total);
+  const long long share = max(quotient(max(total, 0ll) + a.ctas - 1, a.ctas), (long long)MIN_TILES * S::KT * a.group);
+  const long long u = share * blockIdx.x, u_end = min(u + share, total);
+  const bool idle = u >= total;
   if (!idle && my_u0 <= u && u < my_u0 + mine) {
     int b = my_b0;
     long long at = my_u0;
@@ -416,18 +414,26 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
       auto scales_of = [&](int group) { return group_scales(a, p, group); };
       Window<GroupScales, decltype(scales_of)> scales;
       scales.begin(p.k0 * S::GROUPS, scales_of);
-      const bool live = 128 * m + r < p.np;
-      const long long pair = p.p0 + 128 * m + (live ? r : 0);
-      const int i = (int)(pair / a.group);
-      const size_t head = (size_t)p.g * a.group + (size_t)(pair % a.group);
+      // (what of a row the key tiles do not need is found again where it is)
+      const auto row_of = [&](bool& live) {
+        live = 128 * m + r < p.np;
+        return (int)quotient(p.p0 + 128 * m + (live ? r : 0), a.group);
+      };
+      const auto at_of_row = [&](int i, long long ld) {
+        const long long pair = p.p0 + 128 * m + (128 * m + r < p.np ? r : 0);
+        return (long long)(p.r0 + i) * ld + ((long long)p.g * a.group + pair - (long long)i * a.group) * D;
+      };
+      bool live;
+      const int i = row_of(live);
       // ---- the warp's 32 rows, some lanes a row: fp16 pieces times a power of two that brings a row's largest
       // magnitude into [1, 2); a row with a NaN or an infinity as zeros, its scores' factor NaN
-      const long long q_at = (long long)(p.r0 + i) * a.ldq + (long long)(head * D);
+      const long long q_at = at_of_row(i, a.ldq);
       float top = 0.f;  // of this thread's row
       {
         constexpr int N = 16 / sizeof(T), VECS = D / N, LR = VECS < 32 ? VECS : 32, V = VECS / LR;  // elements of 16 bytes; a row's lanes, and what a lane has of it
-        constexpr int RS = 32 / LR, BATCH = V == 1 ? 16 : 8;
+        constexpr int RS = 32 / LR, BATCH = V == 1 ? 8 : 4;
         const int in_row = lane % LR;
+        const unsigned alive = __ballot_sync(0xffffffffu, live);
         uint8_t* rows = sQ + m * S::PIECES * 128 * D * 2;
 #pragma unroll 1
         for (int b0 = 0; b0 < 32 / RS; b0 += BATCH) {
@@ -440,31 +446,41 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
             for (int e = 0; e < V; ++e)
               if (owner < 32) x[k][e] = *reinterpret_cast<const uint4*>(from + (e * LR + in_row) * N);
           }
+          float most[BATCH];
 #pragma unroll
           for (int k = 0; k < BATCH; ++k) {
-            if ((b0 + k) * RS >= 32) break;
-            const int owner = (b0 + k) * RS + lane / LR, R = warp % 4 * 32 + owner;
-            float y[V][N];
-            float most = 0.f;
+            most[k] = 0.f;
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-              values_of<T>(x[k][e], y[e]);
+              float y[N];
+              values_of<T>(x[k][e], y);
 #pragma unroll
-              for (int h = 0; h < N; ++h) most = fmaxf(most, y[e][h] == y[e][h] ? fabsf(y[e][h]) : INFINITY);
+              for (int h = 0; h < N; ++h) most[k] = fmaxf(most[k], y[h] == y[h] ? fabsf(y[h]) : INFINITY);
             }
+          }
 #pragma unroll
-            for (int o = LR / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-            const float mine = __shfl_sync(0xffffffffu, most, (lane - (b0 + k) * RS) * LR & 31);
+          for (int o = LR / 2; o > 0; o >>= 1)  // (the rows' steps side by side: a shuffle takes 25 cycles)
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) most[k] = fmaxf(most[k], __shfl_xor_sync(0xffffffffu, most[k], o));
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) {
+            const float mine = __shfl_sync(0xffffffffu, most[k], (lane - (b0 + k) * RS) * LR & 31);
             if (lane / RS == b0 + k) top = mine;
-            const int counts = __shfl_sync(0xffffffffu, (int)live, owner);
-            const bool zero = !(most <= FLT_MAX) || !counts;
-            const float down = __uint_as_float((uint32_t)(127 - q_exponent(most)) << 23);
+          }
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) {
+            const int owner = (b0 + k) * RS + lane / LR, R = warp % 4 * 32 + owner;
+            if (owner >= 32) break;
+            const bool zero = !(most[k] <= FLT_MAX) || !(alive >> owner & 1);
+            const float down = zero ? 0.f : __uint_as_float((uint32_t)(127 - q_exponent(most[k])) << 23);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
+              float y[N];
+              values_of<T>(x[k][e], y);
               uint32_t hi[N / 2], lo[N / 2];
 #pragma unroll
               for (int h = 0; h < N / 2; ++h) {
-                const float y0 = zero ? 0.f : y[e][2 * h] * down, y1 = zero ? 0.f : y[e][2 * h + 1] * down;
+                const float y0 = zero ? 0.f : y[2 * h] * down, y1 = zero ? 0.f : y[2 * h + 1] * down;
                 hi[h] = half2_bits(y0, y1);
                 const float2 f = half2_values(hi[h]);
                 lo[h] = half2_bits(y0 - f.x, y1 - f.y);
@@ -490,20 +506,29 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
 
       const int sees = live ? min(p.len, p.first + i + 1) : 0;  // positions
       float ref = -INFINITY, run_max = -INFINITY, sum = 0.f;
-      float R = 0x1p-100f, inv_R = 0x1p100f;
+      float R = 0x1p-100f;  // a power of two
       float mean_ref = -INFINITY, mean_sum = 0.f;  // of the mean taken over
       const int k0 = p.k0, k1 = p.k1;
-      const bool partial = k1 - k0 < p.tiles;
-      const int slot = 2 * (int)blockIdx.x + (k0 == 0);
       // ---- O, with the mean taken over so far, to the mean, a piece's outputs or the rows
       auto flush = [&](bool last) {
+        const bool partial = p.k1 - p.k0 < p.tiles;
+        const int slot = 2 * (int)blockIdx.x + (p.k0 == 0);
         const float top_ref = fmaxf(ref, mean_ref);
         const float wn = sum == 0.f ? 0.f : exp2f(ref - top_ref), wm = mean_sum == 0.f ? 0.f : exp2f(mean_ref - top_ref);
         const float all = sum * wn + mean_sum * wm, inv = all == 0.f ? 0.f : 1.f / all;
         const float co = R * 0x1p-7f * (wn * inv), cm = wm * mean_sum * inv;
         float4* mean = a.mean + (size_t)blockIdx.x * (D / 4) * S::PAIRS + 128 * m + r;
         float4* part = a.part_o + (size_t)slot * (D / 4) * S::PAIRS + 128 * m + r;
-        const long long out_at = (long long)(p.r0 + i) * a.ldo + (long long)(head * D);
+        bool live;
+        const long long out_at = at_of_row(row_of(live), a.ldo);
+        // the rows that this lane's 16 bytes go to: 4 it + lane / 8
+        long long to[8];
+        const unsigned alive = __ballot_sync(0xffffffffu, live);
+        if (last && !partial) {
+#pragma unroll
+          for (int it = 0; it < 8; ++it)
+            to[it] = __shfl_sync(0xffffffffu, out_at, it * 4 + lane / 8) + (lane & 7) * (16 / (int)sizeof(T));
+        }
         float4 x[2][8];  // the mean so far, 32 dims ahead
         const bool more = S::TWO && mean_sum != 0.f;
         if (more) {
@@ -562,9 +587,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
                 const int rr = it * 4 + lane / 8, R = warp % 4 * 32 + rr;
                 const uint4 y = *reinterpret_cast<const uint4*>(sQ + m * S::PIECES * 128 * D * 2 + block * (128 * 128) + R * 128 +
                                                                 (((lane & 7) ^ (R & 7)) << 4));
-                const long long to = __shfl_sync(0xffffffffu, out_at, rr);
-                if (__shfl_sync(0xffffffffu, (int)live, rr))
-                  *reinterpret_cast<uint4*>(out + to + block * DIMS + (lane & 7) * (16 / (int)sizeof(T))) = y;
+                if (alive >> rr & 1) *reinterpret_cast<uint4*>(out + to[it] + block * DIMS) = y;
               }
             }
           }
@@ -576,16 +599,16 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
       bool fresh = true;  // O holds nothing yet
 #pragma unroll 1
       for (int j = k0; j < k1; ++j, ++cnt) {
-        const int buf = S::MT == 2 ? m : cnt & 1, phase = S::MT == 2 ? cnt : cnt >> 1;
+        const int buf = 2 * m + (cnt & 1), phase = cnt >> 1;
         scales.reach(j * S::GROUPS, scales_of);
         float ks[S::GROUPS], vs[S::GROUPS];
-        float vmax = 0.f, vmin = FLT_MAX;
+        float vmax = 0.f;
 #pragma unroll
         for (int c = 0; c < S::GROUPS; ++c) {
           ks[c] = __shfl_sync(0xffffffffu, scales.now.k, j * S::GROUPS + c - scales.base) * factor;
           ks[c] = ks[c] == 0.f ? FLT_MIN : ks[c];  // (as good as 0 for a score, but minus infinity stays that)
           vs[c] = __shfl_sync(0xffffffffu, scales.now.v, j * S::GROUPS + c - scales.base);
-          vmax = fmaxf(vmax, vs[c]), vmin = fminf(vmin, vs[c]);
+          vmax = fmaxf(vmax, vs[c]);
         }
         // (these scores' completion covers every product before them, O's of two tiles ago among them: so a wait for the
         // last tile's O, by parity, cannot be a phase behind)
@@ -597,7 +620,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
           flush(false);
           fresh = true;
         }
-        const uint32_t s_col = lanes + S::COL_S + buf * S::KT, p_col = lanes + S::COL_P + buf * S::P_STEP;
+        const uint32_t s_col = lanes + S::COL_S + buf * S::KT;
         uint32_t s[S::KT];
 #pragma unroll
         for (int c = 0; c < S::GROUPS; ++c) tmem_ld_32x32b_x32(s_col + 32 * c, s + 32 * c);
@@ -627,7 +650,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
           ref = run_max == -INFINITY ? 0.f : run_max;
           if (grow) {
             R = __uint_as_float(min((__float_as_uint(vmax) & 0x7f800000u) + (2u << 23), 0x7e800000u));
-            inv_R = 1.f / R;
           }
         } else if (grow || __any_sync(0xffffffffu, run_max > ref + MOVE)) {
           if (!wait(&o_done[m], cnt - 1)) break;
@@ -640,7 +662,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
             const float new_R = __uint_as_float(min((__float_as_uint(vmax) & 0x7f800000u) + (2u << 23), 0x7e800000u));
             f *= R * (1.f / new_R);
             R = new_R;
-            inv_R = 1.f / R;
           }
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -654,50 +675,28 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
           }
         }
         // ---- the weights
-        if (!S::TWO && vmin > R * 0x1p-60f) {
-          // 2^(score - ref + log2 of the page's factor) at once, the sum divided by the factor again
-          const float shift = 134.f - (float)(__float_as_uint(R) >> 23);  // log2(2^7 / R)
 #pragma unroll
-          for (int c = 0; c < S::GROUPS; ++c) {
-            const float e = __shfl_sync(0xffffffffu, scales.now.log2_v, j * S::GROUPS + c - scales.base) + shift;
-            const float2 k2 = make_float2(ks[c], ks[c]), r2 = make_float2(e - ref, e - ref);
-            float2 l = make_float2(0.f, 0.f);
-            uint32_t hi[16];
+        for (int c = 0; c < S::GROUPS; ++c) {
+          const float w = vs[c] * __uint_as_float((261u << 23) - __float_as_uint(R));  // * 2^7 / R
+          const float2 k2 = make_float2(ks[c], ks[c]), r2 = make_float2(-ref, -ref), w2 = make_float2(w, w);
+          float2 l = make_float2(0.f, 0.f);
+          uint32_t hi[16], lo[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float2 y = make_float2(__uint_as_float(s[32 * c + 2 * k]), __uint_as_float(s[32 * c + 2 * k + 1]));
-              float2 x = __ffma2_rn(y, k2, r2);
-              x.x = exp2_fast(x.x), x.y = exp2_fast(x.y);
-              l = __fadd2_rn(l, x);
-              hi[k] = half2_bits(x.x, x.y);
+          for (int k = 0; k < 16; ++k) {
+            const float2 y = make_float2(__uint_as_float(s[32 * c + 2 * k]), __uint_as_float(s[32 * c + 2 * k + 1]));
+            float2 x = __ffma2_rn(y, k2, r2);
+            x.x = exp2_fast(x.x), x.y = exp2_fast(x.y);
+            l = __fadd2_rn(l, x);
+            x = __fmul2_rn(x, w2);
+            hi[k] = half2_bits(x.x, x.y);
+            if constexpr (S::TWO) {
+              const float2 f = half2_values(hi[k]);
+              lo[k] = half2_bits(x.x - f.x, x.y - f.y);
             }
-            sum = fmaf(l.x + l.y, exp2f(-e), sum);
-            tmem_st_32x32b_x16(p_col + 16 * c, hi);
           }
-        } else {
-#pragma unroll
-          for (int c = 0; c < S::GROUPS; ++c) {
-            const float w = vs[c] * inv_R * 0x1p7f;
-            const float2 k2 = make_float2(ks[c], ks[c]), r2 = make_float2(-ref, -ref), w2 = make_float2(w, w);
-            float2 l = make_float2(0.f, 0.f);
-            uint32_t hi[16], lo[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float2 y = make_float2(__uint_as_float(s[32 * c + 2 * k]), __uint_as_float(s[32 * c + 2 * k + 1]));
-              float2 x = __ffma2_rn(y, k2, r2);
-              x.x = exp2_fast(x.x), x.y = exp2_fast(x.y);
-              l = __fadd2_rn(l, x);
-              x = __fmul2_rn(x, w2);
-              hi[k] = half2_bits(x.x, x.y);
-              if constexpr (S::TWO) {
-                const float2 f = half2_values(hi[k]);
-                lo[k] = half2_bits(x.x - f.x, x.y - f.y);
-              }
-            }
-            sum += l.x + l.y;
-            tmem_st_32x32b_x16(p_col + 16 * c, hi);
-            if constexpr (S::TWO) tmem_st_32x32b_x16(p_col + S::KT / 2 + 16 * c, lo);
-          }
+          sum += l.x + l.y;
+          tmem_st_32x32b_x16(s_col + 16 * c, hi);
+          if constexpr (S::TWO) tmem_st_32x32b_x16(s_col + S::KT / 2 + 16 * c, lo);
         }
         tmem_st_wait();
         fresh = false;
@@ -709,7 +708,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
       tc_fence_after();
       flush(true);
       tc_fence_before();
-      if (partial) a.part_ml[(size_t)slot * S::PAIRS + 128 * m + r] = make_float2(mean_ref, mean_sum);
+      if (p.k1 - p.k0 < p.tiles)
+        a.part_ml[(size_t)(2 * (int)blockIdx.x + (p.k0 == 0)) * S::PAIRS + 128 * m + r] = make_float2(mean_ref, mean_sum);
     }
   } else if (warp < MMA_WARP) {
     // ------------------------------------------------ converters: chunks of K and V in the order in which they are used
@@ -758,65 +758,68 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
   if (warp == MMA_WARP) {
     // ------------------------------------------------ the products
     constexpr uint32_t IDESC_S = idesc_f16_f32(128, S::KT), IDESC_O = idesc_f16_f32(128, D) | N_MAJOR_B;
-    int chunks = 0, cnt0 = 0, cnt1 = 0, mine0 = 0, mine1 = 0;  // chunks; key tiles and pieces of each M tile, so far
+    const uint32_t base = uniform(tmem), q_at = uniform(smem_u32(sQ)) >> 4, ring_at = uniform(smem_u32(ring)) >> 4;
+    constexpr uint64_t desc = operand_desc(16), v_desc = operand_desc(S::PANEL);
+    uint32_t cnt0 = 0, cnt1 = 0, mine0 = 0, mine1 = 0;  // key tiles and pieces of each M tile, so far
+    uint32_t k_slot = 0, k_phase = 0;                    // of the K chunk that is next
     for (int ip = 0; piece_is(ip); piece_done(ip), ++ip) {
-      const int n = s_piece[ip & 1].k1 - s_piece[ip & 1].k0, nm = S::MT == 2 && s_piece[ip & 1].np > 128 ? 2 : 1;
-      auto k_chunk = [&](int j) { return chunks + (S::MT == 2 || j == 0 ? 2 * j : 2 * j - 1); };
-      auto v_chunk = [&](int j) { return chunks + (S::MT == 2 || j == n - 1 ? 2 * j + 1 : 2 * j + 2); };
-      auto issue_s = [&](int j, int m) {
-        const int c = k_chunk(j), x = (m ? cnt1 : cnt0) + j, buf = S::MT == 2 ? m : x & 1;
-        if (!wait(&full[c % S::SLOTS], c / S::SLOTS)) return;
+      const uint32_t n = uniform(s_piece[ip & 1].k1 - s_piece[ip & 1].k0);
+      const uint32_t nm = S::MT == 2 ? uniform(s_piece[ip & 1].np > 128 ? 2 : 1) : 1;
+      uint32_t v_slot = 0, v_phase = 0;  // the slot, and its phase, of the V chunk that is next
+      // chunks in order: K of tiles 0 and 1, V of tile 0, K of tile 2, V of tile 1, ...
+      auto advance = [&](uint32_t& slot, uint32_t& phase) {
+        if (++slot == S::SLOTS) slot = 0, phase ^= 1;
+      };
+      auto issue_s = [&](uint32_t x, uint32_t m) {
+        const uint32_t buf = 2 * m + (x & 1);
+        if (!wait(&full[k_slot], k_phase)) return;
         tc_fence_after();
-        const uint8_t* kt = ring + c % S::SLOTS * S::SLOT;
+        const uint64_t kd = desc + (ring_at + k_slot * (S::SLOT >> 4));
 #pragma unroll
         for (int s = S::PIECES - 1; s >= 0; --s) {  // the small piece first
-          const uint64_t qd = smem_desc_sw128(sQ + (m * S::PIECES + s) * 128 * D * 2), kd = smem_desc_sw128(kt);
+          const uint64_t qd = desc + (q_at + (m * S::PIECES + s) * (128 * D * 2 >> 4));
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_f16_ss_elect(tmem + S::COL_S + buf * S::KT, qd + (uint64_t)((kk / 4 * 128 * 128) >> 4) + 2 * (kk % 4),
+            mma_f16_ss_elect(base + S::COL_S + buf * S::KT, qd + (uint64_t)((kk / 4 * 128 * 128) >> 4) + 2 * (kk % 4),
                              kd + (uint64_t)((kk / 4 * S::PANEL) >> 4) + 2 * (kk % 4), IDESC_S, s != S::PIECES - 1 || kk != 0);
         }
         mma_commit_elect(&s_full[buf]);
-        if (m == nm - 1) mma_commit_elect(&empty[c % S::SLOTS]);
+        if (m == nm - 1) mma_commit_elect(&empty[k_slot]);
       };
-      auto issue_o = [&](int j, int m) {
-        const int c = v_chunk(j), x = (m ? cnt1 : cnt0) + j, buf = S::MT == 2 ? m : x & 1;
-        if (!wait(&full[c % S::SLOTS], c / S::SLOTS)) return;
-        if (!wait(&p_full[buf], S::MT == 2 ? x : x >> 1)) return;
+      auto issue_o = [&](uint32_t x, uint32_t m, bool fresh, bool last) {
+        const uint32_t buf = 2 * m + (x & 1);
+        if (!wait(&full[v_slot], v_phase)) return;
+        if (!wait(&p_full[buf], x >> 1)) return;
         tc_fence_after();
-        const uint8_t* vt = ring + c % S::SLOTS * S::SLOT;
-        const bool fresh = S::TWO ? j % S::FOLD_TILES == 0 : j == 0;
+        const uint64_t vd = v_desc + (ring_at + v_slot * (S::SLOT >> 4));
 #pragma unroll
-        for (int s = S::PIECES - 1; s >= 0; --s) {
-          const uint64_t vd = smem_desc_n_major(vt, S::PANEL);
+        for (int s = S::PIECES - 1; s >= 0; --s)
 #pragma unroll
           for (int kk = 0; kk < S::KT / 16; ++kk)
-            mma_f16_ts_elect(tmem + m * D, tmem + S::COL_P + buf * S::P_STEP + s * (S::KT / 2) + 8 * kk, vd + (uint64_t)((kk * 2048) >> 4),
+            mma_f16_ts_elect(base + m * D, base + S::COL_S + buf * S::KT + s * (S::KT / 2) + 8 * kk, vd + (uint64_t)((kk * 2048) >> 4),
                              IDESC_O, !fresh || s != S::PIECES - 1 || kk != 0);
-        }
         mma_commit_elect(&o_done[m]);
-        if (j == n - 1) mma_commit_elect(&o_last[m]);
-        if (m == nm - 1) mma_commit_elect(&empty[c % S::SLOTS]);
+        if (last) mma_commit_elect(&o_last[m]);
+        if (m == nm - 1) mma_commit_elect(&empty[v_slot]);
       };
-      for (int m = 0; m < nm && ok; ++m) {
-        wait(&q_full[m], m ? mine1 : mine0);
-        if (ok) issue_s(0, m);
-      }
+      for (uint32_t m = 0; m < nm && ok; ++m)
+        if (wait(&q_full[m], m ? mine1 : mine0)) issue_s(m ? cnt1 : cnt0, m);
+      advance(k_slot, k_phase);
 #pragma unroll 1
-      for (int j = 0; j < n && ok; ++j) {
-        if (S::MT == 2) {
-          for (int m = 0; m < nm && ok; ++m) {
-            issue_o(j, m);
-            if (ok && j + 1 < n) issue_s(j + 1, m);
-          }
-        } else {
-          if (j + 1 < n) issue_s(j + 1, 0);
-          if (ok) issue_o(j, 0);
+      for (uint32_t j = 0; j < n && ok; ++j) {
+        // K of tile j + 1 at (k_slot, k_phase), V of tile j behind it (or, of the last tile, there)
+        v_slot = k_slot, v_phase = k_phase;
+        if (j + 1 < n) advance(v_slot, v_phase);
+        for (uint32_t m = 0; m < nm && ok; ++m) {
+          const uint32_t x = (m ? cnt1 : cnt0) + j;
+          if (j + 1 < n) issue_s(x + 1, m);
+          if (ok) issue_o(x, m, S::TWO ? j % S::FOLD_TILES == 0 : j == 0, j + 1 == n);
         }
+        k_slot = v_slot, k_phase = v_phase;
+        advance(k_slot, k_phase);
       }
       cnt0 += n, ++mine0;
       if (nm == 2) cnt1 += n, ++mine1;
-      chunks += 2 * n;
       if (!ok) break;
     }
     // the products in flight have finished before tensor memory goes
@@ -824,13 +827,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
     __all_sync(0xffffffffu, mbar_wait(&drain, 0, abort_flag + 1, v.status));
   } else if (warp == PIECE_WARP) {
     // ------------------------------------------------ the pieces of the share, two ahead
-    Pieces<S> pieces{s_found_b, ctas, u, idle ? 0 : share_begin(blockIdx.x + 1, ctas, total), s_found[0], total};
+    Pieces<S> pieces{s_found_b, idle ? 0 : u, idle ? 0 : u_end, s_found[0], share, total};
     int4 record = make_int4(0, 0, 0, 0);
     bool more = true;
     for (int ip = 0; more && wait(&piece_empty[ip & 1], (ip >> 1) + 1); ++ip) {
       Piece p;
       int t, made_of;
-      more = pieces.next(a, blockIdx.x, p, t, made_of);
+      more = pieces.next(a, p, t, made_of);
       if (!more) p.k1 = 0;
       if (more && made_of > 1) record = make_int4(p.b, t, p.g, made_of);
       if (lane == 0) {
@@ -869,11 +872,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
         if (some) bulk_load_1d(raw + rs * S::RAW + first * D, codes + (size_t)g * 32 * D, (uint32_t)(run * D), &raw_full[rs]);
         ++sent;
       };
-      // K of tile 0, V of tile 0, K of tile 1, ..., or with one M tile K of tiles 0 and 1, V of tile 0, K of tile 2, ...
+      // K of tiles 0 and 1, V of tile 0, K of tile 2, V of tile 1, ...
+      send(0, v.K, k_at);
 #pragma unroll 1
       for (int j = 0; j < n && ok; ++j) {
-        if (S::MT == 2 || j == 0) send(j, v.K, k_at);
-        if (S::MT == 1 && j + 1 < n && ok) send(j + 1, v.K, k_at);
+        if (j + 1 < n) send(j + 1, v.K, k_at);
         if (ok) send(j, v.V, v_at);
       }
       if (!ok) break;
