@@ -66,7 +66,8 @@ struct Shape {
   static constexpr bool TWO = TWO_;                        // two fp16 pieces of q and of the weights
   static constexpr int MT = D <= 128 ? 2 : 1;              // M tiles
   static constexpr int PAIRS = 128 * MT;
-  static constexpr int KT = 64;                            // keys of a tile
+  static constexpr int KT = MT == 2 ? 128 : 64;            // keys of a tile
+  static constexpr int NB = MT == 2 ? 1 : 2;               // buffers of scores of an M tile
   static constexpr int GROUPS = KT / 32;                   // of 32 positions, within one page each
   static constexpr int PIECES = TWO ? 2 : 1;
   static constexpr int PANEL = KT * 128;                   // bytes of 64 dims of a tile
@@ -81,12 +82,12 @@ struct Shape {
   static constexpr int SMEM = Q_BYTES + SLOTS * SLOT + RAWS * RAW + 1024;
   static constexpr int SOFT = 4 * MT, CONV = MMA_WARP - SOFT;  // warps
   // registers a thread of each role; as launched: 128
-  static constexpr int SOFT_REGS = MT == 2 ? 160 : 208, CONV_REGS = MT == 2 ? 96 : 88, MMA_REGS = MT == 2 ? 96 : 128;
+  static constexpr int SOFT_REGS = MT == 2 ? 192 : 208, CONV_REGS = MT == 2 ? 64 : 88, MMA_REGS = MT == 2 ? 64 : 128;
   static_assert(32 * (SOFT * SOFT_REGS + CONV * CONV_REGS + 4 * MMA_REGS) <= THREADS * 128, "registers");
   static constexpr int EACH = KT * D / 16 / (32 * CONV);   // 16-byte pieces of a chunk that a converter thread has
-  // tensor memory columns: O of each M tile, then two buffers of scores for each, which the weights take over
+  // tensor memory columns: O of each M tile, then its buffers of scores, which the weights take over
   static constexpr int COL_S = MT * D;
-  static_assert(COL_S + 2 * MT * KT <= 512 && PIECES * KT / 2 <= KT, "tensor memory");
+  static_assert(COL_S + NB * MT * KT <= 512 && PIECES * KT / 2 <= KT, "tensor memory");
   static_assert(SLOTS >= 2 && RAWS >= 2 && SMEM + 1024 <= 232448, "shared memory");
   static_assert(EACH >= 1 && KT * D / 16 % (32 * CONV) == 0, "converters");
   static constexpr int FOLD_TILES = FOLD / KT;
@@ -599,7 +600,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
       bool fresh = true;  // O holds nothing yet
 #pragma unroll 1
       for (int j = k0; j < k1; ++j, ++cnt) {
-        const int buf = 2 * m + (cnt & 1), phase = cnt >> 1;
+        const int buf = S::NB == 2 ? cnt & 1 : m, phase = S::NB == 2 ? cnt >> 1 : cnt;
         scales.reach(j * S::GROUPS, scales_of);
         float ks[S::GROUPS], vs[S::GROUPS];
         float vmax = 0.f;
@@ -610,12 +611,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
           vs[c] = __shfl_sync(0xffffffffu, scales.now.v, j * S::GROUPS + c - scales.base);
           vmax = fmaxf(vmax, vs[c]);
         }
-        // (these scores' completion covers every product before them, O's of two tiles ago among them: so a wait for the
-        // last tile's O, by parity, cannot be a phase behind)
+        // (these scores' completion covers every product issued before them: with one buffer the last tile's O, with two the
+        // one before that, so that a wait for the last one, by parity, cannot be a phase behind)
         if (!wait(&s_full[buf], phase)) break;
         tc_fence_after();
         if (S::TWO && j > k0 && (j - k0) % S::FOLD_TILES == 0) {
-          if (!wait(&o_done[m], cnt - 1)) break;
+          if (S::NB == 2 && !wait(&o_done[m], cnt - 1)) break;
           tc_fence_after();
           flush(false);
           fresh = true;
@@ -652,7 +653,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
             R = __uint_as_float(min((__float_as_uint(vmax) & 0x7f800000u) + (2u << 23), 0x7e800000u));
           }
         } else if (grow || __any_sync(0xffffffffu, run_max > ref + MOVE)) {
-          if (!wait(&o_done[m], cnt - 1)) break;
+          if (S::NB == 2 && !wait(&o_done[m], cnt - 1)) break;
           tc_fence_after();
           const float new_ref = run_max > ref ? run_max : ref;
           float f = exp2f(ref - new_ref);
@@ -766,13 +767,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
       const uint32_t n = uniform(s_piece[ip & 1].k1 - s_piece[ip & 1].k0);
       const uint32_t nm = S::MT == 2 ? uniform(s_piece[ip & 1].np > 128 ? 2 : 1) : 1;
       uint32_t v_slot = 0, v_phase = 0;  // the slot, and its phase, of the V chunk that is next
-      // chunks in order: K of tiles 0 and 1, V of tile 0, K of tile 2, V of tile 1, ...
       auto advance = [&](uint32_t& slot, uint32_t& phase) {
         if (++slot == S::SLOTS) slot = 0, phase ^= 1;
       };
       auto issue_s = [&](uint32_t x, uint32_t m) {
-        const uint32_t buf = 2 * m + (x & 1);
-        if (!wait(&full[k_slot], k_phase)) return;
+        const uint32_t buf = S::NB == 2 ? x & 1 : m;
+        if (m == 0 && !wait(&full[k_slot], k_phase)) return;
         tc_fence_after();
         const uint64_t kd = desc + (ring_at + k_slot * (S::SLOT >> 4));
 #pragma unroll
@@ -787,9 +787,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
         if (m == nm - 1) mma_commit_elect(&empty[k_slot]);
       };
       auto issue_o = [&](uint32_t x, uint32_t m, bool fresh, bool last) {
-        const uint32_t buf = 2 * m + (x & 1);
-        if (!wait(&full[v_slot], v_phase)) return;
-        if (!wait(&p_full[buf], x >> 1)) return;
+        const uint32_t buf = S::NB == 2 ? x & 1 : m;
+        if (m == 0 && !wait(&full[v_slot], v_phase)) return;
+        if (!wait(&p_full[buf], S::NB == 2 ? x >> 1 : x)) return;
         tc_fence_after();
         const uint64_t vd = v_desc + (ring_at + v_slot * (S::SLOT >> 4));
 #pragma unroll
@@ -798,7 +798,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
           for (int kk = 0; kk < S::KT / 16; ++kk)
             mma_f16_ts_elect(base + m * D, base + S::COL_S + buf * S::KT + s * (S::KT / 2) + 8 * kk, vd + (uint64_t)((kk * 2048) >> 4),
                              IDESC_O, !fresh || s != S::PIECES - 1 || kk != 0);
-        mma_commit_elect(&o_done[m]);
+        if (S::NB == 2) mma_commit_elect(&o_done[m]);  // (with one buffer the next scores' commit says as much)
         if (last) mma_commit_elect(&o_last[m]);
         if (m == nm - 1) mma_commit_elect(&empty[v_slot]);
       };
@@ -807,16 +807,27 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
       advance(k_slot, k_phase);
 #pragma unroll 1
       for (uint32_t j = 0; j < n && ok; ++j) {
-        // K of tile j + 1 at (k_slot, k_phase), V of tile j behind it (or, of the last tile, there)
-        v_slot = k_slot, v_phase = k_phase;
-        if (j + 1 < n) advance(v_slot, v_phase);
-        for (uint32_t m = 0; m < nm && ok; ++m) {
-          const uint32_t x = (m ? cnt1 : cnt0) + j;
-          if (j + 1 < n) issue_s(x + 1, m);
-          if (ok) issue_o(x, m, S::TWO ? j % S::FOLD_TILES == 0 : j == 0, j + 1 == n);
+        if constexpr (S::NB == 2) {
+          // chunks in order: K of tiles 0 and 1, V of tile 0, K of tile 2, V of tile 1, ...
+          v_slot = k_slot, v_phase = k_phase;
+          if (j + 1 < n) {
+            advance(v_slot, v_phase);
+            issue_s(cnt0 + j + 1, 0);
+          }
+          if (ok) issue_o(cnt0 + j, 0, S::TWO ? j % S::FOLD_TILES == 0 : j == 0, j + 1 == n);
+          k_slot = v_slot, k_phase = v_phase;
+          advance(k_slot, k_phase);
+        } else {
+          // K of tile 0, V of tile 0, K of tile 1, ...; one M tile's products while the other's softmax runs
+          v_slot = k_slot, v_phase = k_phase;
+          advance(k_slot, k_phase);
+          for (uint32_t m = 0; m < nm && ok; ++m) {
+            const uint32_t x = (m ? cnt1 : cnt0) + j;
+            issue_o(x, m, S::TWO ? j % S::FOLD_TILES == 0 : j == 0, j + 1 == n);
+            if (ok && j + 1 < n) issue_s(x + 1, m);
+          }
+          if (j + 1 < n) advance(k_slot, k_phase);
         }
-        k_slot = v_slot, k_phase = v_phase;
-        advance(k_slot, k_phase);
       }
       cnt0 += n, ++mine0;
       if (nm == 2) cnt1 += n, ++mine1;
@@ -872,11 +883,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
         if (some) bulk_load_1d(raw + rs * S::RAW + first * D, codes + (size_t)g * 32 * D, (uint32_t)(run * D), &raw_full[rs]);
         ++sent;
       };
-      // K of tiles 0 and 1, V of tile 0, K of tile 2, V of tile 1, ...
-      send(0, v.K, k_at);
+      // (in the order of the products)
+      if (S::NB == 2) send(0, v.K, k_at);
 #pragma unroll 1
       for (int j = 0; j < n && ok; ++j) {
-        if (j + 1 < n) send(j + 1, v.K, k_at);
+        if (S::NB == 1) send(j, v.K, k_at);
+        if (S::NB == 2 && j + 1 < n) send(j + 1, v.K, k_at);
         if (ok) send(j, v.V, v_at);
       }
       if (!ok) break;
