@@ -84,12 +84,15 @@ struct Shape {
   // registers a thread of each role; as launched: 128
   static constexpr int SOFT_REGS = MT == 2 ? 192 : 208, CONV_REGS = MT == 2 ? 64 : 88, MMA_REGS = MT == 2 ? 64 : 128;
   static_assert(32 * (SOFT * SOFT_REGS + CONV * CONV_REGS + 4 * MMA_REGS) <= THREADS * 128, "registers");
-  static constexpr int EACH = KT * D / 16 / (32 * CONV);   // 16-byte pieces of a chunk that a converter thread has
+  // converter warps of a chunk: with eight two teams, every other chunk each (256 dims 154 -> 127 us; two teams of two warps took
+  // longer than one of four, 956 us instead of 851)
+  static constexpr int TEAMS = CONV / 4, TEAM = 4;
+  static constexpr int EACH = KT * D / 16 / (32 * TEAM);   // 16-byte pieces of a chunk that a converter thread has
   // tensor memory columns: O of each M tile, then its buffers of scores, which the weights take over
   static constexpr int COL_S = MT * D;
   static_assert(COL_S + NB * MT * KT <= 512 && PIECES * KT / 2 <= KT, "tensor memory");
   static_assert(SLOTS >= 2 && RAWS >= 2 && SMEM + 1024 <= 232448, "shared memory");
-  static_assert(EACH >= 1 && KT * D / 16 % (32 * CONV) == 0, "converters");
+  static_assert(EACH >= 1 && KT * D / 16 % (32 * TEAM) == 0, "converters");
   static constexpr int FOLD_TILES = FOLD / KT;
 };
 
@@ -343,12 +346,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
   if (lane == 31) s_scan[warp] = inc;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::SLOTS; ++i) {
-      mbar_init(&full[i], S::CONV);
+      mbar_init(&full[i], S::TEAM);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < S::RAWS; ++i) {
       mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], S::CONV);
+      mbar_init(&raw_empty[i], S::TEAM);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 4);
@@ -432,7 +435,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
       float top = 0.f;  // of this thread's row
       {
         constexpr int N = 16 / sizeof(T), VECS = D / N, LR = VECS < 32 ? VECS : 32, V = VECS / LR;  // elements of 16 bytes; a row's lanes, and what a lane has of it
-        constexpr int RS = 32 / LR, BATCH = V == 1 ? 8 : 4;
+        constexpr int RS = 32 / LR, BATCH = 8;
         const int in_row = lane % LR;
         const unsigned alive = __ballot_sync(0xffffffffu, live);
         uint8_t* rows = sQ + m * S::PIECES * 128 * D * 2;
@@ -530,15 +533,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
           for (int it = 0; it < 8; ++it)
             to[it] = __shfl_sync(0xffffffffu, out_at, it * 4 + lane / 8) + (lane & 7) * (16 / (int)sizeof(T));
         }
-        float4 x[2][8];  // the mean so far, 32 dims ahead
         const bool more = S::TWO && mean_sum != 0.f;
+        // (rows of T leave through the warp's own rows of q's place, which no product reads any more: 128 bytes of
+        // a row together instead of 16)
+        constexpr int DIMS = 128 / sizeof(T);
+        float4 x[2][8];  // the mean so far, 32 dims ahead
         if (more) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) x[0][k] = mean[(size_t)k * S::PAIRS];
         }
-        // (rows of T leave through the warp's own rows of q's place, which no product reads any more: 128 bytes of
-        // a row together instead of 16)
-        constexpr int DIMS = 128 / sizeof(T);
 #pragma unroll 1
         for (int c0 = 0; c0 < D / 32; c0 += 2) {
 #pragma unroll
@@ -715,40 +718,47 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
   } else if (warp < MMA_WARP) {
     // ------------------------------------------------ converters: chunks of K and V in the order in which they are used
     fewer_registers<S::CONV_REGS>();
-    const int tid = (int)threadIdx.x - 32 * S::SOFT;
+    const int tid = ((int)threadIdx.x - 32 * S::SOFT) % (32 * S::TEAM), team = (warp - S::SOFT) / S::TEAM;
     constexpr int ROW = D / 16;                       // 16-byte pieces of a position's codes
-    constexpr int STEP = 32 * S::CONV / ROW;          // positions from one of a thread's pieces to the next
+    constexpr int STEP = 32 * S::TEAM / ROW;          // positions from one of a thread's pieces to the next
     const int key0 = tid / ROW, piece = tid % ROW, panel = piece / 4;
-    uint32_t done = 0;  // chunks so far
+    uint32_t rs = team, slot_of = team, raw_phase = 0, phase = 1;  // of this team's next chunk
     for (int ip = 0; piece_is(ip); piece_done(ip), ++ip) {
-      const int chunks = 2 * (s_piece[ip & 1].k1 - s_piece[ip & 1].k0);
+      const int mine = 2 / S::TEAMS * (s_piece[ip & 1].k1 - s_piece[ip & 1].k0);
 #pragma unroll 1
-      for (int c = 0; c < chunks; ++c, ++done) {
-        const int rs = done % S::RAWS, s = done % S::SLOTS;
-        if (!wait(&raw_full[rs], done / S::RAWS) || !wait(&empty[s], done / S::SLOTS + 1)) break;
+      for (int c = 0; c < mine; ++c) {
+        if (!wait(&raw_full[rs], raw_phase) || !wait(&empty[slot_of], phase)) break;
         const uint8_t* from = raw + rs * S::RAW + tid * 16;
-        uint8_t* slot = ring + s * S::SLOT + panel * S::PANEL;
-        uint4 x[S::EACH];
+        uint8_t* slot = ring + slot_of * S::SLOT + panel * S::PANEL;
+        constexpr int AHEAD = S::EACH < 8 ? S::EACH : 8;
 #pragma unroll
-        for (int i = 0; i < S::EACH; ++i) x[i] = *reinterpret_cast<const uint4*>(from + i * (32 * S::CONV * 16));
+        for (int i0 = 0; i0 < S::EACH; i0 += AHEAD) {
+          uint4 x[AHEAD];
 #pragma unroll
-        for (int i = 0; i < S::EACH; ++i) {
-          const int key = key0 + i * STEP;
-          const uint32_t b[4] = {x[i].x ^ 0x80808080u, x[i].y ^ 0x80808080u, x[i].z ^ 0x80808080u, x[i].w ^ 0x80808080u};
-          const uint4 y0 = make_uint4(half2_of_codes(b[0], 0x4140), half2_of_codes(b[0], 0x4342),
-                                      half2_of_codes(b[1], 0x4140), half2_of_codes(b[1], 0x4342));
-          const uint4 y1 = make_uint4(half2_of_codes(b[2], 0x4140), half2_of_codes(b[2], 0x4342),
-                                      half2_of_codes(b[3], 0x4140), half2_of_codes(b[3], 0x4342));
-          uint8_t* row = slot + key * 128;
-          const int c8 = 2 * (piece & 3), odd = panel & 1;  // (neighbouring panels' stores go to different banks)
-          *reinterpret_cast<uint4*>(row + (((c8 + odd) ^ (key & 7)) << 4)) = odd ? y1 : y0;
-          *reinterpret_cast<uint4*>(row + (((c8 + 1 - odd) ^ (key & 7)) << 4)) = odd ? y0 : y1;
+          for (int i = 0; i < AHEAD; ++i) x[i] = *reinterpret_cast<const uint4*>(from + (i0 + i) * (32 * S::TEAM * 16));
+#pragma unroll
+          for (int i = 0; i < AHEAD; ++i) {
+            const int key = key0 + (i0 + i) * STEP;
+            const uint32_t b[4] = {x[i].x ^ 0x80808080u, x[i].y ^ 0x80808080u, x[i].z ^ 0x80808080u, x[i].w ^ 0x80808080u};
+            const uint4 y0 = make_uint4(half2_of_codes(b[0], 0x4140), half2_of_codes(b[0], 0x4342),
+                                        half2_of_codes(b[1], 0x4140), half2_of_codes(b[1], 0x4342));
+            const uint4 y1 = make_uint4(half2_of_codes(b[2], 0x4140), half2_of_codes(b[2], 0x4342),
+                                        half2_of_codes(b[3], 0x4140), half2_of_codes(b[3], 0x4342));
+            uint8_t* row = slot + key * 128;
+            const int c8 = 2 * (piece & 3), odd = panel & 1;  // (neighbouring panels' stores go to different banks)
+            *reinterpret_cast<uint4*>(row + (((c8 + odd) ^ (key & 7)) << 4)) = odd ? y1 : y0;
+            *reinterpret_cast<uint4*>(row + (((c8 + 1 - odd) ^ (key & 7)) << 4)) = odd ? y0 : y1;
+          }
         }
         fence_proxy_async_smem();  // (no load from global memory is on its way, which it would wait for)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&raw_empty[rs]);
-          mbar_arrive(&full[s]);
+          mbar_arrive(&full[slot_of]);
+        }
+        for (int i = 0; i < S::TEAMS; ++i) {
+          if (++rs == S::RAWS) rs = 0, raw_phase ^= 1;
+          if (++slot_of == S::SLOTS) slot_of = 0, phase ^= 1;
         }
       }
       if (!ok) break;
