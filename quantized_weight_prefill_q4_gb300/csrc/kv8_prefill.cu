@@ -66,8 +66,8 @@ struct Shape {
   static constexpr bool TWO = TWO_;                        // two fp16 pieces of q and of the weights
   static constexpr int MT = D <= 128 ? 2 : 1;              // M tiles
   static constexpr int PAIRS = 128 * MT;
-  static constexpr int KT = MT == 2 ? 128 : 64;            // keys of a tile
-  static constexpr int NB = MT == 2 ? 1 : 2;               // buffers of scores of an M tile
+  static constexpr int KT = MT == 2 && !TWO ? 128 : 64;    // keys of a tile
+  static constexpr int NB = KT == 128 ? 1 : 2;             // buffers of scores of an M tile
   static constexpr int GROUPS = KT / 32;                   // of 32 positions, within one page each
   static constexpr int PIECES = TWO ? 2 : 1;
   static constexpr int PANEL = KT * 128;                   // bytes of 64 dims of a tile
@@ -161,7 +161,7 @@ struct Pieces {
   long long u, end, seq_u0, share, total;  // CTA c's share: share * c .. share * (c + 1) - 1, within the total
 
   // The next piece, and of how many pieces its segment is made where the piece begins it.
-  __device__ bool next(const PrefillArgs& a, Piece& p, int& t, int& made_of) {
+  __device__ __forceinline__ bool next(const PrefillArgs& a, Piece& p, int& t, int& made_of) {
     const int lane = threadIdx.x & 31;
     while (u < end && b < a.v.num_seqs) {
       const Work w = work_of<S>(a, b);
@@ -514,13 +514,55 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
       float mean_ref = -INFINITY, mean_sum = 0.f;  // of the mean taken over
       const int k0 = p.k0, k1 = p.k1;
       // ---- O, with the mean taken over so far, to the mean, a piece's outputs or the rows
-      auto flush = [&](bool last) {
-        const bool partial = p.k1 - p.k0 < p.tiles;
-        const int slot = 2 * (int)blockIdx.x + (p.k0 == 0);
+      // (co, cm: what O and the mean count for)
+      float co, cm;
+      auto join = [&] {
         const float top_ref = fmaxf(ref, mean_ref);
         const float wn = sum == 0.f ? 0.f : exp2f(ref - top_ref), wm = mean_sum == 0.f ? 0.f : exp2f(mean_ref - top_ref);
         const float all = sum * wn + mean_sum * wm, inv = all == 0.f ? 0.f : 1.f / all;
-        const float co = R * 0x1p-7f * (wn * inv), cm = wm * mean_sum * inv;
+        co = R * 0x1p-7f * (wn * inv), cm = wm * mean_sum * inv;
+        const bool more = S::TWO && mean_sum != 0.f;
+        mean_ref = top_ref;
+        mean_sum = all;
+        sum = 0.f;
+        return more;
+      };
+      // O into the mean, 64 dims of which are on their way together (128 no longer fit the registers)
+      auto fold = [&] {
+        constexpr int G = 2;
+        const bool more = join();
+        float4* mean = a.mean + (size_t)blockIdx.x * (D / 4) * S::PAIRS + 128 * m + r;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D / 32; c0 += G, mean += (size_t)8 * G * S::PAIRS) {
+          float4 x[G][8];
+          if (more) {
+#pragma unroll
+            for (int k = 0; k < 8 * G; ++k) x[k / 8][k % 8] = mean[(size_t)k * S::PAIRS];
+          }
+#pragma unroll
+          for (int cc = 0; cc < G; ++cc) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(o_col + 32 * (c0 + cc), o);
+            tmem_ld_wait_regs(o);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              float4 y = make_float4(__uint_as_float(o[4 * k]) * co, __uint_as_float(o[4 * k + 1]) * co,
+                                     __uint_as_float(o[4 * k + 2]) * co, __uint_as_float(o[4 * k + 3]) * co);
+              if (more) {
+                const float4 z = x[cc][k];
+                y.x = fmaf(z.x, cm, y.x), y.y = fmaf(z.y, cm, y.y), y.z = fmaf(z.z, cm, y.z), y.w = fmaf(z.w, cm, y.w);
+              }
+              if (mean_sum == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);  // (whatever O held)
+              mean[(size_t)(8 * cc + k) * S::PAIRS] = y;
+            }
+          }
+        }
+      };
+      // O and the mean to a piece's outputs or the rows
+      auto finish = [&] {
+        const bool partial = p.k1 - p.k0 < p.tiles;
+        const int slot = 2 * (int)blockIdx.x + (p.k0 == 0);
+        const bool more = join();
         float4* mean = a.mean + (size_t)blockIdx.x * (D / 4) * S::PAIRS + 128 * m + r;
         float4* part = a.part_o + (size_t)slot * (D / 4) * S::PAIRS + 128 * m + r;
         bool live;
@@ -528,12 +570,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
         // the rows that this lane's 16 bytes go to: 4 it + lane / 8
         long long to[8];
         const unsigned alive = __ballot_sync(0xffffffffu, live);
-        if (last && !partial) {
+        if (!partial) {
 #pragma unroll
           for (int it = 0; it < 8; ++it)
             to[it] = __shfl_sync(0xffffffffu, out_at, it * 4 + lane / 8) + (lane & 7) * (16 / (int)sizeof(T));
         }
-        const bool more = S::TWO && mean_sum != 0.f;
         // (rows of T leave through the warp's own rows of q's place, which no product reads any more: 128 bytes of
         // a row together instead of 16)
         constexpr int DIMS = 128 / sizeof(T);
@@ -564,10 +605,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
                 const float4 z = x[cc][k];
                 y.x = fmaf(z.x, cm, y.x), y.y = fmaf(z.y, cm, y.y), y.z = fmaf(z.z, cm, y.z), y.w = fmaf(z.w, cm, y.w);
               }
-              if (all == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);  // (whatever O held)
-              if (!last) {
-                mean[(size_t)(8 * c + k) * S::PAIRS] = y;
-              } else if (partial) {
+              if (mean_sum == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);  // (whatever O held)
+              if (partial) {
                 part[(size_t)(8 * c + k) * S::PAIRS] = y;
               } else if constexpr (sizeof(T) == 4) {
                 *reinterpret_cast<float4*>(row + ((k ^ (r & 7)) << 4)) = y;
@@ -581,7 +620,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
               }
             }
           }
-          if (last && !partial) {
+          if (!partial) {
             __syncwarp();
 #pragma unroll
             for (int b = 0; b < 64 / DIMS; ++b) {  // 128-byte blocks of the 64 dims
@@ -596,14 +635,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
             }
           }
         }
-        mean_ref = top_ref;
-        mean_sum = all;
-        sum = 0.f;
       };
       bool fresh = true;  // O holds nothing yet
 #pragma unroll 1
       for (int j = k0; j < k1; ++j, ++cnt) {
-        const int buf = S::NB == 2 ? cnt & 1 : m, phase = S::NB == 2 ? cnt >> 1 : cnt;
+        const int buf = S::NB == 2 ? 2 * m + (cnt & 1) : m, phase = S::NB == 2 ? cnt >> 1 : cnt;
         scales.reach(j * S::GROUPS, scales_of);
         float ks[S::GROUPS], vs[S::GROUPS];
         float vmax = 0.f;
@@ -621,7 +657,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
         if (S::TWO && j > k0 && (j - k0) % S::FOLD_TILES == 0) {
           if (S::NB == 2 && !wait(&o_done[m], cnt - 1)) break;
           tc_fence_after();
-          flush(false);
+          fold();
           fresh = true;
         }
         const uint32_t s_col = lanes + S::COL_S + buf * S::KT;
@@ -710,7 +746,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
       }
       if (!ok || !wait(&o_last[m], mine_so_far - 1)) break;
       tc_fence_after();
-      flush(true);
+      finish();
       tc_fence_before();
       if (p.k1 - p.k0 < p.tiles)
         a.part_ml[(size_t)(2 * (int)blockIdx.x + (p.k0 == 0)) * S::PAIRS + 128 * m + r] = make_float2(mean_ref, mean_sum);
@@ -781,7 +817,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
         if (++slot == S::SLOTS) slot = 0, phase ^= 1;
       };
       auto issue_s = [&](uint32_t x, uint32_t m) {
-        const uint32_t buf = S::NB == 2 ? x & 1 : m;
+        const uint32_t buf = S::NB == 2 ? 2 * m + (x & 1) : m;
         if (m == 0 && !wait(&full[k_slot], k_phase)) return;
         tc_fence_after();
         const uint64_t kd = desc + (ring_at + k_slot * (S::SLOT >> 4));
@@ -797,7 +833,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
         if (m == nm - 1) mma_commit_elect(&empty[k_slot]);
       };
       auto issue_o = [&](uint32_t x, uint32_t m, bool fresh, bool last) {
-        const uint32_t buf = S::NB == 2 ? x & 1 : m;
+        const uint32_t buf = S::NB == 2 ? 2 * m + (x & 1) : m;
         if (m == 0 && !wait(&full[v_slot], v_phase)) return;
         if (!wait(&p_full[buf], S::NB == 2 ? x >> 1 : x)) return;
         tc_fence_after();
@@ -820,11 +856,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
         if constexpr (S::NB == 2) {
           // chunks in order: K of tiles 0 and 1, V of tile 0, K of tile 2, V of tile 1, ...
           v_slot = k_slot, v_phase = k_phase;
-          if (j + 1 < n) {
-            advance(v_slot, v_phase);
-            issue_s(cnt0 + j + 1, 0);
+          if (j + 1 < n) advance(v_slot, v_phase);
+          for (uint32_t m = 0; m < nm && ok; ++m) {
+            const uint32_t x = (m ? cnt1 : cnt0) + j;
+            if (j + 1 < n) issue_s(x + 1, m);
+            if (ok) issue_o(x, m, S::TWO ? j % S::FOLD_TILES == 0 : j == 0, j + 1 == n);
           }
-          if (ok) issue_o(cnt0 + j, 0, S::TWO ? j % S::FOLD_TILES == 0 : j == 0, j + 1 == n);
           k_slot = v_slot, k_phase = v_phase;
           advance(k_slot, k_phase);
         } else {
