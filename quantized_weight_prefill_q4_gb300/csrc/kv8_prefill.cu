@@ -40,8 +40,13 @@
 namespace apr {
 namespace {
 
-constexpr int START = 256;       // positions that a segment's start and end are worth
+// Positions that a segment's start and end are worth (2048 rows over 2048, 32 heads over 8 of 128: 68 us, 82 with 256, 108 with
+// 128, 69 with 1024).
+constexpr int START = 512;
 constexpr int MIN_TILES = 2;     // of a CTA's share
+// Pieces that a segment is cut into at the most: more take longer to combine than they save (64 rows over 20000, 8 heads over 2
+// of 64: 39 us, 75 in the 76 pieces that every SM would have one of).
+constexpr int MOST_PIECES = 24;
 constexpr float MOVE = 8.f;
 constexpr int FOLD = 512;        // positions
 constexpr int MMA_WARP = 12, PIECE_WARP = 13, COPY_WARP = 14, THREADS = 512;  // (the last warp has nothing to do)
@@ -326,7 +331,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
   __shared__ Piece s_piece[2];
   __shared__ uint32_t tmem_holder;
   __shared__ int abort_words[2];  // the second is never set: the drain's wait ignores the abort
-  __shared__ long long s_scan[THREADS / 32], s_found[1];
+  __shared__ long long s_scan[THREADS / 32], s_largest[THREADS / 32], s_found[1];
   __shared__ int s_found_b;
   volatile int* abort_flag = abort_words;
   const Kv8View& v = a.v;
@@ -335,15 +340,20 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
   // ---- what the sequences cost, and where this CTA's share begins: a thread counts `run` neighbouring sequences
   const int run = (v.num_seqs + THREADS - 1) / THREADS;
   const int my_b0 = min((int)threadIdx.x * run, v.num_seqs), my_b1 = min(my_b0 + run, v.num_seqs);
-  long long mine = 0;
-  for (int b = my_b0; b < my_b1; ++b) mine += cost_all<S>(a, work_of<S>(a, b));
+  long long mine = 0, largest = 0;  // what they cost, and the most that a segment of theirs does
+  for (int b = my_b0; b < my_b1; ++b) {
+    const Work w = work_of<S>(a, b);
+    mine += cost_all<S>(a, w);
+    if (w.segments > 0) largest = max(largest, cost<S>(w, w.segments - 1));
+  }
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
+    largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, o));
   }
-  if (lane == 31) s_scan[warp] = inc;
+  if (lane == 31) s_scan[warp] = inc, s_largest[warp] = largest;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::SLOTS; ++i) {
       mbar_init(&full[i], S::TEAM);
@@ -380,8 +390,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
   for (int w = 0; w < THREADS / 32; ++w) {
     if (w < warp) my_u0 += s_scan[w];
     total += s_scan[w];
+    largest = max(largest, s_largest[w]);
   }
-  const long long share = max(quotient(max(total, 0ll) + a.ctas - 1, a.ctas), (long long)MIN_TILES * S::KT * a.group);
+  const long long share = max(quotient(max(total, 0ll) + a.ctas - 1, a.ctas), max((long long)MIN_TILES * S::KT * a.group, quotient(largest, MOST_PIECES)));
   const long long u = share * blockIdx.x, u_end = min(u + share, total);
   const bool idle = u >= total;
   if (!idle && my_u0 <= u && u < my_u0 + mine) {
@@ -953,9 +964,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
 
 // ---------------------------------------------------------------- the pieces
 // The segment that CTA blockIdx.x began and others ended: its pieces' outputs by their totals, in order. 32
-// dims of 128 pairs a CTA.
+// dims of 128 pairs a CTA (with 8, four times as many that mostly find nothing to do, 4 us more for 512 rows over 2048).
+constexpr int JOIN_THREADS = 256;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(256) kv8_prefill_combine_kernel(const __grid_constant__ PrefillArgs a) {
+__global__ void __launch_bounds__(JOIN_THREADS) kv8_prefill_combine_kernel(const __grid_constant__ PrefillArgs a) {
   using S = Shape<D, sizeof(T) == 4>;
   grid_dependency_wait();
   grid_launch_dependents();
@@ -966,30 +979,35 @@ __global__ void __launch_bounds__(256) kv8_prefill_combine_kernel(const __grid_c
   const long long pair = (long long)rec.y * S::PAIRS + r;
   if (pair >= w.pairs) return;
   auto slot = [&](int i) { return (size_t)(2 * ((int)blockIdx.x + i) + (i == 0)); };
+  // (several pieces' loads are on their way together)
   float top = -INFINITY;
+#pragma unroll 8
   for (int i = 0; i < rec.w; ++i) {
     const float2 ml = a.part_ml[slot(i) * S::PAIRS + r];
-    if (ml.y != 0.f) top = fmaxf(top, ml.x);
+    top = ml.y != 0.f ? fmaxf(top, ml.x) : top;
   }
   float all = 0.f;
+#pragma unroll 8
   for (int i = 0; i < rec.w; ++i) {
     const float2 ml = a.part_ml[slot(i) * S::PAIRS + r];
-    if (ml.y != 0.f) all += ml.y * exp2f(ml.x - top);
+    all += ml.y != 0.f ? ml.y * exp2f(ml.x - top) : 0.f;
   }
   const float inv = all == 0.f ? 0.f : 1.f / all;
   float4 y[4] = {};
+#pragma unroll 4
   for (int i = 0; i < rec.w; ++i) {
     const float2 ml = a.part_ml[slot(i) * S::PAIRS + r];
-    if (ml.y == 0.f) continue;
-    const float f = ml.y * exp2f(ml.x - top) * inv;  // (at most 1: no sum of large values leaves the range)
     const float4* o = a.part_o + (slot(i) * (D / 4) + c0) * S::PAIRS + r;
+    float4 x[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float4 x = o[(size_t)c * S::PAIRS];
-      y[c].x = fmaf(x.x, f, y[c].x), y[c].y = fmaf(x.y, f, y[c].y), y[c].z = fmaf(x.z, f, y[c].z), y[c].w = fmaf(x.w, f, y[c].w);
-    }
+    for (int c = 0; c < 4; ++c) x[c] = o[(size_t)c * S::PAIRS];
+    const float f = ml.y != 0.f ? ml.y * exp2f(ml.x - top) * inv : 0.f;  // (at most 1: no sum of large values leaves the range)
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      y[c].x = fmaf(x[c].x, f, y[c].x), y[c].y = fmaf(x[c].y, f, y[c].y), y[c].z = fmaf(x[c].z, f, y[c].z), y[c].w = fmaf(x[c].w, f, y[c].w);
   }
-  T* to = static_cast<T*>(a.out) + (long long)(w.r0 + pair / a.group) * a.ldo + ((size_t)rec.z * a.group + pair % a.group) * D + 4 * c0;
+  const int i = (int)quotient(pair, a.group);
+  T* to = static_cast<T*>(a.out) + (long long)(w.r0 + i) * a.ldo + ((size_t)rec.z * a.group + (size_t)(pair - (long long)i * a.group)) * D + 4 * c0;
 #pragma unroll
   for (int c = 0; c < 4; ++c) store4<T>(to + 4 * c, y[c]);
 }
@@ -1018,7 +1036,7 @@ cudaError_t launch_shape(const PrefillArgs& a, cudaStream_t s) {
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)a.ctas, S::MT * (D / 32));
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(JOIN_THREADS);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, kv8_prefill_combine_kernel<T, D>, a);
 }
