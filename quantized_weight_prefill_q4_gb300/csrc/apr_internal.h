@@ -218,7 +218,7 @@ struct Kv8Attention {
 size_t kv8_attention_scratch(const Kv8View& v, const Kv8Attention& a);
 cudaError_t launch_kv8_attention(const Kv8View& v, const Kv8Attention& a, void* scratch, cudaStream_t s);
 // Chunks of rows (kv8_prefill.cu); its scratch: kv8_prefill_scratch.
-size_t kv8_prefill_scratch(const Kv8View& v, int type, int heads);
+size_t kv8_prefill_scratch(const Kv8View& v);
 cudaError_t launch_kv8_prefill(const Kv8View& v, int type, const void* q, long long ldq, void* out, long long ldo,
                                int heads, float scale, void* scratch, cudaStream_t s);
 cudaError_t launch_kv8_evict(const Kv8View& v, const float* weights, long long weights_ld, int budget, int recent,

@@ -273,8 +273,11 @@ int run_prefill_attention(const apr_kv8_cache* cache, const apr_kv8_rows* rows, 
   if (rc != APR_OK) return rc == 1 ? APR_OK : rc;
   rc = check_heads(w, type, q, ldq, out, ldo, num_heads, scale);
   if (rc != APR_OK) return rc;
-  // what the tiles are worth is counted in 64 bits
-  if ((double)w.num_rows * num_heads * ((double)w.max_len + 4096.) > 0x1p60 || (long long)w.num_rows * num_heads > (1LL << 32))
+  // what the segments cost is counted in 64 bits, for ranges of rows of any kind: of 128 pairs or more, each at most
+  // (max_len + max_rows + a start) * group, and shares of six times the sum
+  if ((long long)w.num_rows * num_heads > (1LL << 32) ||
+      (double)w.num_seqs * ((double)w.max_rows * num_heads / 128. + num_heads) * ((double)w.max_len + w.max_rows + 4096.) *
+              (num_heads / w.kv_heads) > 0x1p59)
     return set_error(APR_E_INVAL, "sizes beyond the supported limits");
   const size_t size = type_size(type), width = (size_t)num_heads * w.dim, cb = code_bytes(w), sb = scale_bytes(w);
   const Range outs[] = {{out, span_of(w.num_rows, ldo, width) * size, "out"}};
@@ -292,7 +295,7 @@ int run_prefill_attention(const apr_kv8_cache* cache, const apr_kv8_rows* rows, 
   if (rc != APR_OK) return rc;
   const StreamOrder order(s);
   void* scratch = nullptr;
-  rc = kv8_scratch(s, kv8_prefill_scratch(w, type, num_heads), &scratch);
+  rc = kv8_scratch(s, kv8_prefill_scratch(w), &scratch);
   if (rc != APR_OK) return rc;
   return launched(launch_kv8_prefill(w, type, q, ldq, out, ldo, num_heads, scale > 0.f ? scale : 1.f / std::sqrt((float)w.dim),
                                      scratch, s),

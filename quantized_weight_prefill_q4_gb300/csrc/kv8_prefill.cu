@@ -27,8 +27,7 @@
 // one (256 dims) on the next key tile's scores.
 //
 // float32 rows: q and the weights enter as two fp16 pieces each (22 bits), twice the
-// products. The tensor cores' sums lose about 2e-8 of themselves at each step, so O is
-// taken over into a float32 mean every FOLD positions.
+// products.
 //
 // Weights. A pair's weights are 2^7 p v, p against a reference at most MOVE (base 2) below the
 // maximum, v the page's V scale over a power of two R that no scale so far exceeds: at most 2^15.
@@ -48,7 +47,9 @@ constexpr int MIN_TILES = 2;     // of a CTA's share
 // of 64: 39 us, 75 in the 76 pieces that every SM would have one of).
 constexpr int MOST_PIECES = 24;
 constexpr float MOVE = 8.f;
-constexpr int FOLD = 512;        // positions
+// A wait for the next piece, or for the last one to be over, lasts as long as a piece: 2^30 positions take
+// some 40 s. (Every wait within one is short, and one that runs out ends these, too.)
+constexpr unsigned long long PIECE_LIMIT_NS = 300000000000ull;
 constexpr int MMA_WARP = 12, PIECE_WARP = 13, COPY_WARP = 14, THREADS = 512;  // (the last warp has nothing to do)
 
 struct PrefillArgs {
@@ -62,7 +63,7 @@ struct PrefillArgs {
   int4* record;      // [ctas] (sequence, segment of it, KV head, pieces) of the segment that a CTA begins and others end
   float2* part_ml;   // [2 ctas][pairs] reference maximum and total of a piece
   float4* part_o;    // [2 ctas][D / 4][pairs] its outputs
-  float4* mean;      // [ctas][D / 4][pairs] the mean taken over (float32 rows)
+  float4* mean;      // [ctas][D / 4][pairs] the mean taken over
 };
 
 template <int D_, bool TWO_>
@@ -98,7 +99,9 @@ struct Shape {
   static_assert(COL_S + NB * MT * KT <= 512 && PIECES * KT / 2 <= KT, "tensor memory");
   static_assert(SLOTS >= 2 && RAWS >= 2 && SMEM + 1024 <= 232448, "shared memory");
   static_assert(EACH >= 1 && KT * D / 16 % (32 * TEAM) == 0, "converters");
-  static constexpr int FOLD_TILES = FOLD / KT;
+  // Positions after which O is taken over into a float32 mean: its sums lose some 2e-8 of themselves at each step of 16
+  // positions, always towards zero. 6e-7 in 512 for float32 rows; 4e-5 in 32768 for 16-bit ones, whose outputs are rounded by 2^-11 or more.
+  static constexpr int FOLD = TWO ? 512 : 32768, FOLD_TILES = FOLD / KT;
 };
 
 // ---------------------------------------------------------------- the work
@@ -408,8 +411,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
     ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)(phase & 1), abort_flag, v.status));
     return ok;
   };
+  auto wait_piece = [&](uint64_t* bar, int phase) {
+    ok = ok && __all_sync(0xffffffffu, mbar_wait_for(bar, (uint32_t)(phase & 1), abort_flag, v.status, PIECE_LIMIT_NS));
+    return ok;
+  };
   // the i-th piece, once it is known; and no longer looked at
-  auto piece_is = [&](int i) { return wait(&piece_full[i & 1], i >> 1) && s_piece[i & 1].k1 > 0; };
+  auto piece_is = [&](int i) { return wait_piece(&piece_full[i & 1], i >> 1) && s_piece[i & 1].k1 > 0; };
   auto piece_done = [&](int i) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&piece_empty[i & 1]);
@@ -532,7 +539,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
         const float wn = sum == 0.f ? 0.f : exp2f(ref - top_ref), wm = mean_sum == 0.f ? 0.f : exp2f(mean_ref - top_ref);
         const float all = sum * wn + mean_sum * wm, inv = all == 0.f ? 0.f : 1.f / all;
         co = R * 0x1p-7f * (wn * inv), cm = wm * mean_sum * inv;
-        const bool more = S::TWO && mean_sum != 0.f;
+        const bool more = mean_sum != 0.f;
         mean_ref = top_ref;
         mean_sum = all;
         sum = 0.f;
@@ -665,7 +672,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
         // one before that, so that a wait for the last one, by parity, cannot be a phase behind)
         if (!wait(&s_full[buf], phase)) break;
         tc_fence_after();
-        if (S::TWO && j > k0 && (j - k0) % S::FOLD_TILES == 0) {
+        if (j > k0 && (j - k0) % S::FOLD_TILES == 0) {
           if (S::NB == 2 && !wait(&o_done[m], cnt - 1)) break;
           tc_fence_after();
           fold();
@@ -871,7 +878,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
           for (uint32_t m = 0; m < nm && ok; ++m) {
             const uint32_t x = (m ? cnt1 : cnt0) + j;
             if (j + 1 < n) issue_s(x + 1, m);
-            if (ok) issue_o(x, m, S::TWO ? j % S::FOLD_TILES == 0 : j == 0, j + 1 == n);
+            if (ok) issue_o(x, m, j % S::FOLD_TILES == 0, j + 1 == n);
           }
           k_slot = v_slot, k_phase = v_phase;
           advance(k_slot, k_phase);
@@ -881,7 +888,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
           advance(k_slot, k_phase);
           for (uint32_t m = 0; m < nm && ok; ++m) {
             const uint32_t x = (m ? cnt1 : cnt0) + j;
-            issue_o(x, m, S::TWO ? j % S::FOLD_TILES == 0 : j == 0, j + 1 == n);
+            issue_o(x, m, j % S::FOLD_TILES == 0, j + 1 == n);
             if (ok && j + 1 < n) issue_s(x + 1, m);
           }
           if (j + 1 < n) advance(k_slot, k_phase);
@@ -899,7 +906,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
     Pieces<S> pieces{s_found_b, idle ? 0 : u, idle ? 0 : u_end, s_found[0], share, total};
     int4 record = make_int4(0, 0, 0, 0);
     bool more = true;
-    for (int ip = 0; more && wait(&piece_empty[ip & 1], (ip >> 1) + 1); ++ip) {
+    for (int ip = 0; more && wait_piece(&piece_empty[ip & 1], (ip >> 1) + 1); ++ip) {
       Piece p;
       int t, made_of;
       more = pieces.next(a, p, t, made_of);
@@ -1051,9 +1058,8 @@ size_t piece_bytes(int dim) { return (size_t)pairs_of(dim) * dim * 4; }
 
 }  // namespace
 
-size_t kv8_prefill_scratch(const Kv8View& v, int type, int) {
-  const size_t ctas = num_sms();
-  return ctas * (16 + 2 * (piece_bytes(v.dim) + pairs_of(v.dim) * 8)) + (type == APR_T_F32 ? ctas * piece_bytes(v.dim) : 0);
+size_t kv8_prefill_scratch(const Kv8View& v) {
+  return (size_t)num_sms() * (16 + 3 * piece_bytes(v.dim) + 2 * pairs_of(v.dim) * 8);
 }
 
 cudaError_t launch_kv8_prefill(const Kv8View& v, int type, const void* q, long long ldq, void* out, long long ldo,

@@ -104,6 +104,38 @@ def test_long_sequences_beside_short_ones(q, dim, type_, heads, group):
     both(q, c, heads * group, [5, 3, 200], type_)
 
 
+@pytest.mark.parametrize("dim,type_,length,n", [
+    (128, "f16", 2 ** 17 + 77, 3), (256, "f32", 2 ** 16 + 5, 3), (128, "f32", 2 ** 16 + 5, 2), (64, "f32", 2 ** 17, 1),
+    (256, "bf16", 2 ** 17 + 1, 2), (64, "bf16", 2 ** 29 + 77, 1)])
+def test_positions_without_end(q, dim, type_, length, n):
+    # A table that names one page over and over: the attention of a page whose positions count as often as they are named.
+    # Each of 152 heads is a piece of its own, whose sums are taken over every 512 positions (float32) or 32768: between,
+    # 2 * 512 / 16 or 32768 / 16 steps lose 2^-24 each, and a join rounds the mean, what is added, both factors and the sum,
+    # 2^-22 in all. The longest takes the SMs some seconds.
+    heads, tokens, width = 152, 256, -(-length // 256)
+    c = Case([tokens], heads, dim, tokens, seed=23).on_gpu(q)
+    page = int(c.table[0, 0])
+    x = rows_tensor(c.rng.normal(size=(n, heads * dim)), TYPES[type_])
+    out = torch.full_like(x, float("nan"))
+    table = torch.full((1, width), page, dtype=torch.int32, device="cuda")
+    lens, start = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([length], [0, n]))
+    q.apr_kv8_prefill_attention(c.cache, table, lens, x, out, heads, row_start=start)
+    q.apr_stream_status()
+    k, v = (c.host[w][page].astype(np.float64) * c.host[s][page][:, None, None] for w, s in (("K", "k_scale"), ("V", "v_scale")))
+    score = np.einsum("ngd,gjd->ngj", as_f32(x).astype(np.float64).reshape(n, heads, dim), k) / np.sqrt(dim)
+    reach = np.einsum("ngd,gjd->ngj", np.abs(as_f32(x).astype(np.float64).reshape(n, heads, dim)), np.abs(k)).max(-1) / np.sqrt(dim)
+    sees = length - n + 1 + np.arange(n)
+    count = (sees[:, None] - np.arange(tokens) + tokens - 1) // tokens
+    p = np.exp(score - score.max(-1, keepdims=True)) * count[:, None, :]
+    p /= p.sum(-1, keepdims=True)
+    want, size, vmax = np.einsum("ngj,gjd->ngd", p, v), np.einsum("ngj,gjd->ngd", p, np.abs(v)), np.abs(v).max()
+    half, fold = torch.finfo(TYPES[type_]).eps / 2, 512 if type_ == "f32" else 32768
+    tol = (2 * dim * 2.0 ** -24 * reach + 2.0 ** -17)[..., None] * 2 * vmax + half * np.abs(want)
+    tol += (length / fold * 2.0 ** -22 + (0 if type_ == "f32" else 2.0 ** -11 + 2.0 ** -13)) * size + tokens * 2.0 ** -30 * vmax
+    y = as_f32(out).astype(np.float64).reshape(want.shape)
+    assert (np.abs(y - want) <= tol).all(), float((np.abs(y - want) / tol).max())
+
+
 @pytest.mark.parametrize("type_", ["f32", "bf16"])
 def test_many_sequences(q, type_):
     rng = np.random.default_rng(9)
