@@ -64,6 +64,7 @@ struct PrefillArgs {
   float2* part_ml;   // [2 ctas][pairs] reference maximum and total of a piece
   float4* part_o;    // [2 ctas][D / 4][pairs] its outputs
   float4* mean;      // [ctas][D / 4][pairs] the mean taken over
+  float2* mean_ml;   // [ctas][pairs] its reference and total
 };
 
 template <int D_, bool TWO_>
@@ -100,8 +101,9 @@ struct Shape {
   static_assert(SLOTS >= 2 && RAWS >= 2 && SMEM + 1024 <= 232448, "shared memory");
   static_assert(EACH >= 1 && KT * D / 16 % (32 * TEAM) == 0, "converters");
   // Positions after which O is taken over into a float32 mean: its sums lose some 2e-8 of themselves at each step of 16
-  // positions, always towards zero. 6e-7 in 512 for float32 rows; 4e-5 in 32768 for 16-bit ones, whose outputs are rounded by 2^-11 or more.
-  static constexpr int FOLD = TWO ? 512 : 32768, FOLD_TILES = FOLD / KT;
+  // positions, always towards zero. 6e-7 in 512 for float32 rows, within a piece; 8e-5 in 65536 for 16-bit rows, whose weights and outputs
+  // are rounded by 2e-4 or more, where a piece is cut (code for it in the loop over key tiles took 20% longer for all).
+  static constexpr int FOLD_TILES = (TWO ? 512 : 65536) / KT;
 };
 
 // ---------------------------------------------------------------- the work
@@ -158,6 +160,7 @@ struct Piece {
   int b, g;          // sequence and KV head
   int len, first, r0;
   int k0, k1, tiles;
+  int from, to;      // the CTA's part of the segment, of which this may be one of several cuts
   int np;            // pairs of the segment, from p0 of the sequence's on
   long long p0;
 };
@@ -212,6 +215,7 @@ struct Pieces {
       p.len = w.len, p.first = w.first, p.r0 = w.r0;
       p.p0 = (long long)lo * S::PAIRS;
       p.np = (int)min((long long)S::PAIRS, w.pairs - p.p0);
+      p.from = p.k0, p.to = p.k1;
       made_of = 1;
       if (p.k0 == 0 && p.k1 < p.tiles)
         for (long long x = end; x < min(seg_end, total) && tile_at<S>(a, x - seg_u0, p.tiles) < p.tiles; x += share) ++made_of;
@@ -545,15 +549,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
         sum = 0.f;
         return more;
       };
-      // O into the mean, 64 dims of which are on their way together (128 no longer fit the registers)
+      // O into the mean, 64 dims of which are on their way together (128 no longer fit the registers; 32 for 16-bit rows)
       auto fold = [&] {
-        constexpr int G = 2;
+        constexpr int G = S::TWO ? 2 : 1;
         const bool more = join();
         float4* mean = a.mean + (size_t)blockIdx.x * (D / 4) * S::PAIRS + 128 * m + r;
 #pragma unroll 1
         for (int c0 = 0; c0 < D / 32; c0 += G, mean += (size_t)8 * G * S::PAIRS) {
           float4 x[G][8];
-          if (more) {
+          if (S::TWO && more) {
 #pragma unroll
             for (int k = 0; k < 8 * G; ++k) x[k / 8][k % 8] = mean[(size_t)k * S::PAIRS];
           }
@@ -567,7 +571,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
               float4 y = make_float4(__uint_as_float(o[4 * k]) * co, __uint_as_float(o[4 * k + 1]) * co,
                                      __uint_as_float(o[4 * k + 2]) * co, __uint_as_float(o[4 * k + 3]) * co);
               if (more) {
-                const float4 z = x[cc][k];
+                const float4 z = S::TWO ? x[cc][k] : mean[(size_t)(8 * cc + k) * S::PAIRS];
                 y.x = fmaf(z.x, cm, y.x), y.y = fmaf(z.y, cm, y.y), y.z = fmaf(z.z, cm, y.z), y.w = fmaf(z.w, cm, y.w);
               }
               if (mean_sum == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);  // (whatever O held)
@@ -578,8 +582,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
       };
       // O and the mean to a piece's outputs or the rows
       auto finish = [&] {
-        const bool partial = p.k1 - p.k0 < p.tiles;
-        const int slot = 2 * (int)blockIdx.x + (p.k0 == 0);
+        const bool partial = p.to - p.from < p.tiles;
+        const int slot = 2 * (int)blockIdx.x + (p.from == 0);
         const bool more = join();
         float4* mean = a.mean + (size_t)blockIdx.x * (D / 4) * S::PAIRS + 128 * m + r;
         float4* part = a.part_o + (size_t)slot * (D / 4) * S::PAIRS + 128 * m + r;
@@ -596,8 +600,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
         // (rows of T leave through the warp's own rows of q's place, which no product reads any more: 128 bytes of
         // a row together instead of 16)
         constexpr int DIMS = 128 / sizeof(T);
-        float4 x[2][8];  // the mean so far, 32 dims ahead
-        if (more) {
+        float4 x[2][8];  // the mean so far, 32 dims ahead (16-bit rows: when it is added, which seldom is)
+        if (S::TWO && more) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) x[0][k] = mean[(size_t)k * S::PAIRS];
         }
@@ -608,7 +612,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
             const int c = c0 + cc;
             uint32_t o[32];
             tmem_ld_32x32b_x32(o_col + 32 * c, o);
-            if (more && c + 1 < D / 32) {
+            if (S::TWO && more && c + 1 < D / 32) {
 #pragma unroll
               for (int k = 0; k < 8; ++k) x[1 - cc][k] = mean[(size_t)(8 * c + 8 + k) * S::PAIRS];
             }
@@ -620,7 +624,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
               float4 y = make_float4(__uint_as_float(o[4 * k]) * co, __uint_as_float(o[4 * k + 1]) * co,
                                      __uint_as_float(o[4 * k + 2]) * co, __uint_as_float(o[4 * k + 3]) * co);
               if (more) {
-                const float4 z = x[cc][k];
+                const float4 z = S::TWO ? x[cc][k] : mean[(size_t)(8 * c + k) * S::PAIRS];
                 y.x = fmaf(z.x, cm, y.x), y.y = fmaf(z.y, cm, y.y), y.z = fmaf(z.z, cm, y.z), y.w = fmaf(z.w, cm, y.w);
               }
               if (mean_sum == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);  // (whatever O held)
@@ -672,7 +676,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
         // one before that, so that a wait for the last one, by parity, cannot be a phase behind)
         if (!wait(&s_full[buf], phase)) break;
         tc_fence_after();
-        if (j > k0 && (j - k0) % S::FOLD_TILES == 0) {
+        if (S::TWO && j > k0 && (j - k0) % S::FOLD_TILES == 0) {
           if (S::NB == 2 && !wait(&o_done[m], cnt - 1)) break;
           tc_fence_after();
           fold();
@@ -764,10 +768,20 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
       }
       if (!ok || !wait(&o_last[m], mine_so_far - 1)) break;
       tc_fence_after();
-      finish();
+      float2* mean_ml = a.mean_ml + (size_t)blockIdx.x * S::PAIRS + 128 * m + r;
+      if (!S::TWO && p.k0 > p.from) {
+        const float2 ml = *mean_ml;
+        mean_ref = ml.x, mean_sum = ml.y;
+      }
+      if (!S::TWO && p.k1 < p.to) {
+        fold();
+        *mean_ml = make_float2(mean_ref, mean_sum);
+      } else {
+        finish();
+        if (p.to - p.from < p.tiles)
+          a.part_ml[(size_t)(2 * (int)blockIdx.x + (p.from == 0)) * S::PAIRS + 128 * m + r] = make_float2(mean_ref, mean_sum);
+      }
       tc_fence_before();
-      if (p.k1 - p.k0 < p.tiles)
-        a.part_ml[(size_t)(2 * (int)blockIdx.x + (p.k0 == 0)) * S::PAIRS + 128 * m + r] = make_float2(mean_ref, mean_sum);
     }
   } else if (warp < MMA_WARP) {
     // ------------------------------------------------ converters: chunks of K and V in the order in which they are used
@@ -878,7 +892,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
           for (uint32_t m = 0; m < nm && ok; ++m) {
             const uint32_t x = (m ? cnt1 : cnt0) + j;
             if (j + 1 < n) issue_s(x + 1, m);
-            if (ok) issue_o(x, m, j % S::FOLD_TILES == 0, j + 1 == n);
+            if (ok) issue_o(x, m, S::TWO ? j % S::FOLD_TILES == 0 : j == 0, j + 1 == n);
           }
           k_slot = v_slot, k_phase = v_phase;
           advance(k_slot, k_phase);
@@ -888,7 +902,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
           advance(k_slot, k_phase);
           for (uint32_t m = 0; m < nm && ok; ++m) {
             const uint32_t x = (m ? cnt1 : cnt0) + j;
-            issue_o(x, m, j % S::FOLD_TILES == 0, j + 1 == n);
+            issue_o(x, m, S::TWO ? j % S::FOLD_TILES == 0 : j == 0, j + 1 == n);
             if (ok && j + 1 < n) issue_s(x + 1, m);
           }
           if (j + 1 < n) advance(k_slot, k_phase);
@@ -902,16 +916,21 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
     mma_commit_elect(&drain);
     __all_sync(0xffffffffu, mbar_wait(&drain, 0, abort_flag + 1, v.status));
   } else if (warp == PIECE_WARP) {
-    // ------------------------------------------------ the pieces of the share, two ahead
+    // ------------------------------------------------ the pieces of the share, and their cuts, ahead of the others
     Pieces<S> pieces{s_found_b, idle ? 0 : u, idle ? 0 : u_end, s_found[0], share, total};
     int4 record = make_int4(0, 0, 0, 0);
+    Piece p;
+    p.k1 = p.to = 0;
     bool more = true;
     for (int ip = 0; more && wait_piece(&piece_empty[ip & 1], (ip >> 1) + 1); ++ip) {
-      Piece p;
-      int t, made_of;
-      more = pieces.next(a, p, t, made_of);
-      if (!more) p.k1 = 0;
-      if (more && made_of > 1) record = make_int4(p.b, t, p.g, made_of);
+      if (p.k1 < p.to) {
+        p.k0 = p.k1;
+      } else {
+        int t, made_of;
+        more = pieces.next(a, p, t, made_of);
+        if (more && made_of > 1) record = make_int4(p.b, t, p.g, made_of);
+      }
+      p.k1 = !more ? 0 : (S::TWO ? p.to : min(p.k0 + S::FOLD_TILES, p.to));
       if (lane == 0) {
         s_piece[ip & 1] = p;
         mbar_arrive(&piece_full[ip & 1]);
@@ -1059,7 +1078,7 @@ size_t piece_bytes(int dim) { return (size_t)pairs_of(dim) * dim * 4; }
 }  // namespace
 
 size_t kv8_prefill_scratch(const Kv8View& v) {
-  return (size_t)num_sms() * (16 + 3 * piece_bytes(v.dim) + 2 * pairs_of(v.dim) * 8);
+  return (size_t)num_sms() * (16 + 3 * (piece_bytes(v.dim) + pairs_of(v.dim) * 8));
 }
 
 cudaError_t launch_kv8_prefill(const Kv8View& v, int type, const void* q, long long ldq, void* out, long long ldo,
@@ -1072,7 +1091,9 @@ cudaError_t launch_kv8_prefill(const Kv8View& v, int type, const void* q, long l
   a.part_ml = reinterpret_cast<float2*>(at);
   at += 2 * ctas * pairs_of(v.dim) * 8;
   a.record = reinterpret_cast<int4*>(at);
-  a.mean = reinterpret_cast<float4*>(at + ctas * 16);
+  at += ctas * 16;
+  a.mean_ml = reinterpret_cast<float2*>(at);
+  a.mean = reinterpret_cast<float4*>(at + ctas * pairs_of(v.dim) * 8);
   if (type == APR_T_F32) return launch_typed<float>(a, s);
   if (type == APR_T_F16) return launch_typed<__half>(a, s);
   return launch_typed<__nv_bfloat16>(a, s);

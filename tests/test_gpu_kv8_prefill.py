@@ -105,12 +105,12 @@ def test_long_sequences_beside_short_ones(q, dim, type_, heads, group):
 
 
 @pytest.mark.parametrize("dim,type_,length,n", [
-    (128, "f16", 2 ** 17 + 77, 3), (256, "f32", 2 ** 16 + 5, 3), (128, "f32", 2 ** 16 + 5, 2), (64, "f32", 2 ** 17, 1),
-    (256, "bf16", 2 ** 17 + 1, 2), (64, "bf16", 2 ** 29 + 77, 1)])
+    (128, "f16", 2 ** 18 + 77, 3), (256, "f32", 2 ** 16 + 5, 3), (128, "f32", 2 ** 16 + 5, 2), (64, "f32", 2 ** 17, 1),
+    (256, "bf16", 2 ** 18 + 1, 2), (64, "bf16", 2 ** 29 + 77, 1)])
 def test_positions_without_end(q, dim, type_, length, n):
     # A table that names one page over and over: the attention of a page whose positions count as often as they are named.
-    # Each of 152 heads is a piece of its own, whose sums are taken over every 512 positions (float32) or 32768: between,
-    # 2 * 512 / 16 or 32768 / 16 steps lose 2^-24 each, and a join rounds the mean, what is added, both factors and the sum,
+    # Each of 152 heads is a piece of its own, whose sums are taken over every 512 positions (float32) or 65536: between,
+    # 2 * 512 / 16 or 65536 / 16 steps lose 2^-24 each, and a join rounds the mean, what is added, both factors and the sum,
     # 2^-22 in all. The longest takes the SMs some seconds.
     heads, tokens, width = 152, 256, -(-length // 256)
     c = Case([tokens], heads, dim, tokens, seed=23).on_gpu(q)
@@ -129,9 +129,9 @@ def test_positions_without_end(q, dim, type_, length, n):
     p = np.exp(score - score.max(-1, keepdims=True)) * count[:, None, :]
     p /= p.sum(-1, keepdims=True)
     want, size, vmax = np.einsum("ngj,gjd->ngd", p, v), np.einsum("ngj,gjd->ngd", p, np.abs(v)), np.abs(v).max()
-    half, fold = torch.finfo(TYPES[type_]).eps / 2, 512 if type_ == "f32" else 32768
+    half, fold = torch.finfo(TYPES[type_]).eps / 2, 512 if type_ == "f32" else 65536
     tol = (2 * dim * 2.0 ** -24 * reach + 2.0 ** -17)[..., None] * 2 * vmax + half * np.abs(want)
-    tol += (length / fold * 2.0 ** -22 + (0 if type_ == "f32" else 2.0 ** -11 + 2.0 ** -13)) * size + tokens * 2.0 ** -30 * vmax
+    tol += (length / fold * 2.0 ** -22 + (0 if type_ == "f32" else 2.0 ** -11 + 2.0 ** -12)) * size + tokens * 2.0 ** -30 * vmax
     y = as_f32(out).astype(np.float64).reshape(want.shape)
     assert (np.abs(y - want) <= tol).all(), float((np.abs(y - want) / tol).max())
 
