@@ -57,11 +57,11 @@ typedef struct apr_rope {
 
 /*
  * table[p][i] = f32(scale cos(a)), f32(scale sin(a)), a = (first + p) inv_freq[i]
- * exactly, for 0 <= p < positions, 0 <= i < pairs: within half a step of float32 and 2^-11 of one
- * (scale 1; else of scale). Angles of far positions lose nothing.
+ * exactly, for 0 <= p < positions, 0 <= i < pairs: within half a step of float32 and 2^-40 (times
+ * scale). Angles of far positions lose nothing.
  *   inv_freq  [pairs] float32, magnitudes up to 2^10; pairs 1 .. 256
  *   first     >= 0, first + positions <= 2^30; positions * pairs <= 2^32
- *   scale     finite (the factor that some stretched rotations have; 1 otherwise)
+ *   scale     magnitudes up to 2^100 (the factor that some stretched rotations have; 1 otherwise)
  * positions == 0 is a no-op.
  */
 int apr_rope_table(const float* inv_freq, int pairs, long long first, long long positions, double scale,

@@ -4,7 +4,7 @@
 //
 // Bound. 4 D operations a pair and position, and every code is read once for 128 or 256
 // pairs, so the tensor cores bound it: M = 128 pairs of one KV head a tile, keys in
-// tiles of KT. Both products take fp16: codes are exact in it, a page's
+// tiles of 128 or 64. Both products take fp16: codes are exact in it, a page's
 // scale is a factor of 32 or more neighbouring scores (K) or weights (V).
 //
 // Segments. A segment is MT * 128 (row, head) pairs of a sequence that read one KV head,
@@ -14,23 +14,36 @@
 // segment within one share is finished there; of the others each CTA that has a piece
 // writes its outputs, reference maximum and total, and a second kernel combines them in order.
 //
-// A CTA. The roles hand work to each other through mbarriers:
+// A CTA, one on each SM. The roles hand work to each other through mbarriers:
 //   softmax    four warps for each M tile, a thread a pair (tensor memory lane): they
 //              write q into shared memory, then per key tile read the scores, move the
-//              running maximum and sum, and write the weights
-//              into tensor memory; O is rescaled only when a maximum grows by more than 2^MOVE
-//   converters turn codes into fp16 tiles in a ring of slots, rows of 128 bytes
-//              swizzled for the tensor cores: as they lie in memory for K (dims contiguous, the
-//              product's k side) and for V (dims contiguous, the N side)
+//              running maximum and sum, and write the weights over the scores in tensor memory; O is
+//              rescaled only when a maximum grows by more than 2^MOVE
+//   one warp   looks up the pages and copies codes, a page's part of a tile at a time, into slots as they lie in memory
+//   converters turn those into fp16 tiles in a ring of slots, rows of 128 bytes
+//              swizzled for the tensor cores, dims contiguous: the product's k side for K, its N side for V
+//              (loads straight from global memory held up every tile's fence until they landed: 2044 us, 1063 from the slots)
 //   one warp   issues S = Q K^T (both from shared memory) and O += P V (P from tensor memory)
-// With two M tiles the tensor cores work on one while the other's softmax runs; with
-// one (256 dims) on the next key tile's scores.
+//   one warp   finds the next piece of the CTA's share
+// With two M tiles (up to 128 dims) the tensor cores work on one while the other's softmax runs; with
+// one on the next key tile's scores. A CTA's products run in the order of their issue, so scores may be issued into what the
+// weights of the product ahead of them are read from.
 //
 // float32 rows: q and the weights enter as two fp16 pieces each (22 bits), twice the
 // products.
 //
 // Weights. A pair's weights are 2^7 p v, p against a reference at most MOVE (base 2) below the
 // maximum, v the page's V scale over a power of two R that no scale so far exceeds: at most 2^15.
+//
+// Measured (calls in a graph; bf16 products of a library run at 1928 TFLOP/s in a burst, 1745 sustained):
+//   2048 rows over 40011 positions, 32 heads over 8 of 128, bf16   854 us, 1532 TFLOP/s
+//   8192 over 131072, 32 over 8 of 128, bf16                       11.6 ms, 1469
+//   1024 over 8192, 32 over 8 of 128, bf16                         115 us, 1119 (starts, ends and the combination: 25)
+//   1024 over 8192, 16 over 4 of 256, bf16                         131 us, 982 (one M tile: a tile's scores wait for its softmax's end)
+//   1024 over 8192, 32 over 8 of 64, fp16                          92 us, 700 (54 of it exponentials, 16 a cycle and SM)
+//   1024 over 8192, 32 over 8 of 128, float32                      258 us, 500, twice as many products done
+//   512 over 512, 32 over 8 of 128, bf16                           26 us
+//   37 over 731, 8 over 2 of 64, fp16                              17 us (two launches, each role's first instructions, a tile's way through the roles)
 
 #include "apr_internal.h"
 #include "host_common.h"
@@ -44,7 +57,7 @@ namespace {
 constexpr int START = 512;
 constexpr int MIN_TILES = 2;     // of a CTA's share
 // Pieces that a segment is cut into at the most: more take longer to combine than they save (64 rows over 20000, 8 heads over 2
-// of 64: 39 us, 75 in the 76 pieces that every SM would have one of).
+// of 64: 36 us, 39 with 32, 75 in the 76 pieces that every SM would have one of; 32 rows over 100000 89 us, 119 with 12).
 constexpr int MOST_PIECES = 24;
 constexpr float MOVE = 8.f;
 // A wait for the next piece, or for the last one to be over, lasts as long as a piece: 2^30 positions take

@@ -10,11 +10,14 @@ namespace {
 // ---------------------------------------------------------------- the table
 // Bound by memory, 8 bytes an entry written once, if an entry takes few instructions: this chip has
 // two FP64 lanes an SM for 128 of FP32, so a 64-bit cosine of each entry takes 50 times as long as its
-// store (400003 positions of 128 pairs: 2.9 ms). So a thread evaluates cosine and sine in 64 bits once in
-// RUN positions, and the others by turning that point on by one position's angle at a time, a complex
-// product of numbers of two float32 (rope.cuh) each, cosine and sine in the two halves of packed instructions: 20 an entry.
-// A product is off by some 2^-46, a run of 64 by 2^-40 at the most, far below half a step of the float32 result.
-constexpr int TB_THREADS = 256;
+// store (400003 positions of 128 pairs: 2.9 ms). So a CTA has 32 columns (a pair, and TB_ROWS runs of positions one after the
+// other, a run for each warp), takes cosine and sine in 64 bits for a column's first position, for one position and for
+// a run, and turns on from there: a warp by whole runs to its own, then by one position at a time, each a
+// complex product of numbers of two float32 (rope.cuh), cosine and sine in the two halves of packed instructions: 20 an entry.
+// A product and its factor are off by some 2^-46, a run of 64 by 2^-40 at the most, far below half a step of the float32 result.
+// 400003 positions of 128 pairs 76 us, 0.81 of the HBM rate (runs of 32 91, of 128 73; 64-bit evaluations for every run 108); 8192 of 32
+// pairs 3.6 us (8.1).
+constexpr int TB_ROWS = 8, TB_THREADS = 32 * TB_ROWS;
 constexpr int TB_RUN = 64;
 
 struct Point {
@@ -51,41 +54,56 @@ __device__ __forceinline__ Point point_of(double n, double f) {
 
 __device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
 
-__global__ void __launch_bounds__(TB_THREADS) rope_table_kernel(const float* __restrict__ inv_freq, int pairs,
+// (cosine, sine) of an angle, each in two float32.
+struct Turn {
+  float2 hi, lo;
+};
+// z turned by w: (c, s) w.c + (-s, c) w.s.
+__device__ __forceinline__ Turn turned(const Turn& z, const Turn& w) {
+  const float2 a_hi = make_float2(w.hi.x, w.hi.x), a_lo = make_float2(w.lo.x, w.lo.x);
+  const float2 b_hi = make_float2(w.hi.y, w.hi.y), b_lo = make_float2(w.lo.y, w.lo.y);
+  const float2 xh = make_float2(-z.hi.y, z.hi.x), xl = make_float2(-z.lo.y, z.lo.x);
+  const float2 u = __fmul2_rn(z.hi, a_hi), v = __fmul2_rn(xh, b_hi);
+  const float2 ue = __ffma2_rn(z.lo, a_hi, __ffma2_rn(z.hi, a_lo, __ffma2_rn(z.hi, a_hi, neg2(u))));
+  const float2 ve = __ffma2_rn(xl, b_hi, __ffma2_rn(xh, b_lo, __ffma2_rn(xh, b_hi, neg2(v))));
+  const float2 t = __fadd2_rn(u, v), d = __fadd2_rn(t, neg2(u));
+  const float2 e = __fadd2_rn(__fadd2_rn(u, neg2(__fadd2_rn(t, neg2(d)))), __fadd2_rn(v, neg2(d)));
+  const float2 r = __fadd2_rn(e, __fadd2_rn(ue, ve));
+  Turn y;
+  y.hi = __fadd2_rn(t, r);
+  y.lo = __fadd2_rn(r, neg2(__fadd2_rn(y.hi, neg2(t))));
+  return y;
+}
+
+__global__ void __launch_bounds__(TB_THREADS) rope_table_kernel(const float* __restrict__ inv_freq, unsigned pairs,
                                                                 long long first, long long positions, double scale,
-                                                                int run, int groups, float2* __restrict__ table) {
+                                                                int run, unsigned columns, float2* __restrict__ table) {
   grid_dependency_wait();
   grid_launch_dependents();
-  // thread (group, pair): runs group, group + groups, ...
-  const long long id = (long long)blockIdx.x * TB_THREADS + threadIdx.x;
-  if (id >= (long long)groups * pairs) return;
-  const int pair = (int)(id % pairs);
-  const double f = (double)inv_freq[pair];
-  const Point w = point_of(1.0, f);
-  const float ah = (float)w.c, al = (float)(w.c - ah), bh = (float)w.s, bl = (float)(w.s - bh);
-  const float2 a_hi = make_float2(ah, ah), a_lo = make_float2(al, al), b_hi = make_float2(bh, bh), b_lo = make_float2(bl, bl);
-  for (long long p0 = id / pairs * run; p0 < positions; p0 += (long long)groups * run) {
-    const Point z = point_of((double)(first + p0), f);
-    const double c = z.c * scale, s = z.s * scale;
-    float2 hi = make_float2((float)c, (float)s), lo = make_float2((float)(c - (double)hi.x), (float)(s - (double)hi.y));
-    float2* to = table + p0 * pairs + pair;
-    const int n = (int)min((long long)run, positions - p0);
-    *to = hi;
+  __shared__ Turn s_turn[3][32];  // the first position of a column, one position, a run
+  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+  const unsigned column = min(blockIdx.x * 32 + lane, columns - 1), pair = column % pairs;
+  const long long begin = (long long)(column / pairs) * (TB_ROWS * run);
+  if (row < 3) {
+    const Point z = point_of(row == 0 ? (double)(first + begin) : (row == 1 ? 1.0 : (double)run), (double)inv_freq[pair]);
+    const double by = row == 0 ? scale : 1.0, c = z.c * by, s = z.s * by;
+    const float2 hi = make_float2((float)c, (float)s);
+    s_turn[row][lane] = Turn{hi, make_float2((float)(c - (double)hi.x), (float)(s - (double)hi.y))};
+  }
+  __syncthreads();
+  const long long p0 = begin + row * run;
+  if (blockIdx.x * 32 + lane >= columns || p0 >= positions) return;
+  Turn z = s_turn[0][lane];
+  const Turn one = s_turn[1][lane], whole = s_turn[2][lane];
+  for (int i = 0; i < row; ++i) z = turned(z, whole);
+  float2* to = table + p0 * pairs + pair;
+  const int n = (int)min((long long)run, positions - p0);
+  *to = z.hi;
 #pragma unroll 4
-    for (int k = 1; k < n; ++k) {
-      to += pairs;
-      // (c, s) a + (-s, c) b
-      const float2 xh = make_float2(-hi.y, hi.x), xl = make_float2(-lo.y, lo.x);
-      const float2 u = __fmul2_rn(hi, a_hi), v = __fmul2_rn(xh, b_hi);
-      const float2 ue = __ffma2_rn(lo, a_hi, __ffma2_rn(hi, a_lo, __ffma2_rn(hi, a_hi, neg2(u))));
-      const float2 ve = __ffma2_rn(xl, b_hi, __ffma2_rn(xh, b_lo, __ffma2_rn(xh, b_hi, neg2(v))));
-      const float2 t = __fadd2_rn(u, v), d = __fadd2_rn(t, neg2(u));
-      const float2 e = __fadd2_rn(__fadd2_rn(u, neg2(__fadd2_rn(t, neg2(d)))), __fadd2_rn(v, neg2(d)));
-      const float2 r = __fadd2_rn(e, __fadd2_rn(ue, ve));
-      hi = __fadd2_rn(t, r);
-      lo = __fadd2_rn(r, neg2(__fadd2_rn(hi, neg2(t))));
-      *to = hi;
-    }
+  for (int k = 1; k < n; ++k) {
+    to += pairs;
+    z = turned(z, one);
+    *to = z.hi;
   }
 }
 
@@ -127,19 +145,19 @@ cudaError_t rows_typed(const RopeView& r, const RopeRows& a, cudaStream_t s) {
 
 cudaError_t launch_rope_table(const float* inv_freq, int pairs, long long first, long long positions, double scale,
                               float* table, cudaStream_t s) {
-  // runs as long as they may be that give every SM two CTAs; no more threads than the chip holds at a time
+  // runs as long as they may be that give every SM two CTAs
   int run = TB_RUN;
-  while (run > 8 && (positions + run - 1) / run * pairs < 2ll * TB_THREADS * num_sms()) run /= 2;
-  const long long runs = (positions + run - 1) / run, most = ((long long)num_sms() * 2048 + pairs - 1) / pairs;
-  const int groups = (int)(runs < most ? runs : most);
+  while (run > 8 && positions * pairs < 2ll * TB_THREADS * run * num_sms()) run /= 2;
+  const long long spans = (positions + TB_ROWS * run - 1) / (TB_ROWS * run), columns = spans * pairs;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(((long long)groups * pairs + TB_THREADS - 1) / TB_THREADS));
+  cfg.gridDim = dim3((unsigned)((columns + 31) / 32));
   cfg.blockDim = dim3(TB_THREADS);
   cfg.stream = s;
   cudaLaunchAttribute attr[1] = {pdl_attr()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rope_table_kernel, inv_freq, pairs, first, positions, scale, run, groups, (float2*)table);
+  return cudaLaunchKernelEx(&cfg, rope_table_kernel, inv_freq, (unsigned)pairs, first, positions, scale, run, (unsigned)columns,
+                            (float2*)table);
 }
 
 cudaError_t launch_rope_rows(const RopeView& r, const RopeRows& a, int type, cudaStream_t s) {

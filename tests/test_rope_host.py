@@ -150,6 +150,8 @@ def test_bad_rows_to_rotate_are_refused(q, code, needle, change):
     (INVAL, "beyond", {2: 1 << 30, 3: 1}),
     (INVAL, "beyond", {3: 1 << 28}),
     (INVAL, "scale", {4: math.inf}),
+    (INVAL, "scale", {4: 1e39}),
+    (INVAL, "scale", {4: math.nan}),
     (INVAL, "null", {0: None}),
     (INVAL, "null", {5: None}),
     (ALIGN, "aligned", {5: 9 * A + 8}),
