@@ -419,7 +419,7 @@ int apr_prefill_attention(const float* Q, const float* K_cache, const float* V_c
  *   X += down(silu(h2 . Wg^T) * (h2 . Wu^T)),  h2 = RMSNorm(X) * ffn_norm
  * RoPE and the per-head q/k norm, which the pages apply between the qkv
  * projection and the attention, are not part of this call (a caller that needs
- * them runs the steps one by one with apr_qgemm_rmsnorm, apr_qgemm_ex with
+ * them runs the steps one by one with apr_qgemm_rmsnorm, apr_rope.h's calls, apr_qgemm_ex with
  * ldy, apr_prefill_attention, apr_qgemm and apr_ffn_sublayer).
  *   qtype, leg  as for apr_qgemm_ex, for every projection (the attention takes
  *               fp16 inputs on both legs)

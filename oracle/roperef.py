@@ -25,7 +25,7 @@ def rope_rows(table, pair_axis, interleaved, positions, x, heads, norm=None, eps
     float32 numbers, rounded to float32.)"""
     x = np.asarray(x, np.float32)
     rows, pairs = x.shape[0], table.shape[1]
-    y = x.astype(np.float64).reshape(rows, heads, -1)
+    y = x.astype(np.float64).reshape(rows, heads, x.shape[1] // heads)
     if norm is not None:
         with np.errstate(divide="ignore", invalid="ignore"):
             r = _f32(1.0 / np.sqrt((y * y).mean(-1, keepdims=True) + np.float64(np.float32(eps))))

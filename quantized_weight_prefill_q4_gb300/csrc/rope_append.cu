@@ -7,6 +7,10 @@
 // head's mean of squares within D / 8 neighbouring lanes. What is quantised are the values
 // rounded to the rows' type, the bits that apr_rope_rows would have written. The CTAs behind them
 // rotate the q rows.
+//
+// Bound by instructions (61 % of the issue slots): the norm, the rotation and two passes over a head's rows, between which lie the
+// largest magnitude and a barrier. 13157 bf16 rows of 8 normed heads of 128 on three axes take 61 us, 87 with 32 heads of q (156 before a
+// page's turns were looked up once and a head's rows kept); 50001 fp16 rows of 8 heads of 64 75 us, 91 with 16 of q; 64 rows 4.8 and 5.7 us.
 
 #include "apr_internal.h"
 #include "host_common.h"

@@ -398,3 +398,63 @@ def test_append_step_followed_by_a_replayed_graph_on_another_stream(q):
         assert np.array_equal(as_f32(out), oracle.rope_rows(table, None, False, at, rows[2], 4))
     torch.cuda.synchronize()
     c.assert_cache(want)
+
+
+def test_append_of_a_padded_batch_followed_by_a_replayed_graph(q):
+    # one captured call with positions, replayed as rows and lengths change; what stands in the padding is not looked at
+    c = Case([200, 120, 90], 2, 64, 32, seed=24).on_gpu(q)
+    want, table = c.host, table_of(32, 500)
+    rope = q.Rope(torch.from_numpy(table).cuda(), pair_axis=torch.from_numpy((np.arange(16) % 2).astype(np.uint8)).cuda())
+    k, v, x = (torch.zeros((150, n * 64), device="cuda") for n in (2, 2, 4))
+    out, positions, start = torch.empty_like(x), ints(np.zeros((2, 150))), ints(np.zeros(4))
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=stream):
+        q.apr_rope_kv8_append(c.cache, c.gtable, c.glens, rope, k, v, positions=positions, q=x, q_out=out, num_heads=4, row_start=start)
+    for lens, rows in (([60, 3, 90], [60, 3, 80]), ([61, 0, 90], [1, 0, 0]), ([200, 120, 90], [139, 11, 0]), ([5, 5, 5], [0, 0, 0])):
+        n = sum(rows)
+        c.lens[:] = lens
+        c.glens.copy_(torch.from_numpy(c.lens))
+        start.copy_(torch.from_numpy(starts(rows)))
+        data = [c.rng.normal(size=t.shape).astype(np.float32) for t in (k, v, x)]
+        at = c.rng.integers(0, 500, (2, 150)).astype(np.int32)
+        for a in data:
+            a[n:] = np.nan
+        at[:, n:] = np.array([[-5], [1 << 20]])
+        for t, a in zip((k, v, x, positions), (*data, at)):
+            t.copy_(torch.from_numpy(a))
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        axis = np.arange(16) % 2
+        turned = [oracle.rope_rows(table, axis, False, at[:, :n], data[i][:n], h) for i, h in ((0, 2), (2, 4))]
+        if n:
+            want = oracle.kv8_append(want, c.table, c.lens, starts(rows), turned[0], data[1][:n])
+        c.assert_cache(want)
+        assert np.array_equal(as_f32(out)[:n], turned[1]) and bool((out[n:] == 7).all())
+    q.apr_stream_status()
+
+
+def test_two_streams_at_once(q):
+    cases = [Case([900, 33], 2, 128, 64, seed=s).on_gpu(q) for s in (25, 26)]
+    streams, table = [torch.cuda.Stream() for _ in cases], table_of(128, 1000)
+    rope, start = q.Rope(torch.from_numpy(table).cuda()), ints([0, 700, 733])
+    rows = [[torch.from_numpy(c.rng.normal(size=(733, w * 128)).astype(np.float32)).cuda() for w in (2, 2, 4)] for c in cases]
+    outs, turned = [torch.empty_like(r[2]) for r in rows], [torch.empty_like(r[2]) for r in rows]
+    at = places([900, 33], [700, 33], 733)
+    gat = ints(at)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for c, s, (k, v, x), out, alone in zip(cases, streams, rows, outs, turned):
+            q.apr_rope_kv8_append(c.cache, c.gtable, c.glens, rope, k, v, q=x, q_out=out, num_heads=4, row_start=start, stream=s)
+            q.apr_rope_rows(rope, gat, x, alone, 4, 128, stream=s)
+    for s in streams:
+        q.apr_stream_status(s)
+    for c, (k, v, x), out, alone in zip(cases, rows, outs, turned):
+        assert torch.equal(out, alone)
+        assert np.array_equal(as_f32(out), oracle.rope_rows(table, None, False, [at], as_f32(x), 4))
+        kr = oracle.rope_rows(table, None, False, [at], as_f32(k), 2)
+        host = c.host
+        for _ in range(10):
+            host = oracle.kv8_append(host, c.table, c.lens, [0, 700, 733], kr, as_f32(v))
+        c.assert_cache(host)
