@@ -9,8 +9,9 @@
 // rotate the q rows.
 //
 // Bound by instructions (61 % of the issue slots): the norm, the rotation and two passes over a head's rows, between which lie the
-// largest magnitude and a barrier. 13157 bf16 rows of 8 normed heads of 128 on three axes take 61 us, 87 with 32 heads of q (156 before a
-// page's turns were looked up once and a head's rows kept); 50001 fp16 rows of 8 heads of 64 75 us, 91 with 16 of q; 64 rows 4.8 and 5.7 us.
+// largest magnitude and a barrier. 13157 bf16 rows of 8 normed heads of 128 on three axes take 50 us (61 with K's
+// CTAs among V's, whose last ones ended late), 86 with 32 heads of q (156 before a page's turns were looked up once and a head's rows kept);
+// 50001 fp16 rows of 8 heads of 64 61 us, 90 with 16 of q; 64 rows 4.7 and 5.7 us.
 
 #include "apr_internal.h"
 #include "host_common.h"
@@ -20,8 +21,9 @@
 namespace apr {
 namespace {
 
-// K's CTAs of an SM that the heads are divided for, where each looks its page's turns up first.
-constexpr int K_CTAS = 3;
+// K's CTAs of an SM that the heads are divided for, where each looks its page's turns up first (13157 rows with q 86 us, 92 with 12;
+// without q 50, 41 with 8).
+constexpr int K_CTAS = 5;
 
 struct AppendArgs {
   Kv8View v;
@@ -32,7 +34,8 @@ struct AppendArgs {
   const float* k_norm;
   float eps;
   int k_heads, v_heads;  // that a CTA takes one after the other
-  unsigned append_ctas;  // the CTAs behind them are q's
+  unsigned k_ctas;       // the first ones: they take longest
+  unsigned append_ctas;  // with V's; the CTAs behind them are q's
   int staged;            // bytes of a page's cosines and sines, where they are looked up once for all heads
   int kept;              // a head's rows fit shared memory
   RopeRows q;            // heads 0: none
@@ -71,13 +74,12 @@ __global__ void __launch_bounds__(TH, TH == 128 ? 4 : (sizeof(T) == 4 ? 2 : 3)) 
     rope_rows_group<T, ROW, 1>(a.r, a.q, group, threadIdx.x % ROW, own, live);
     return;
   }
-  const int k_parts = (v.kv_heads + a.k_heads - 1) / a.k_heads, v_parts = (v.kv_heads + a.v_heads - 1) / a.v_heads;
-  const int index_of_unit = (int)(blockIdx.x / (k_parts + v_parts)), part = (int)(blockIdx.x % (k_parts + v_parts));
+  const bool is_v = blockIdx.x >= a.k_ctas;
+  const int each = is_v ? a.v_heads : a.k_heads, parts = (v.kv_heads + each - 1) / each, cta = (int)(blockIdx.x - (is_v ? a.k_ctas : 0));
+  const int index_of_unit = cta / parts, part = cta % parts;
   constexpr int STEP = TH / ROW;  // rows from one of a thread's vectors to the next
   __shared__ float s_max[3][TH / 32];
-  const bool is_v = part >= k_parts;
-  const int g0 = is_v ? (part - k_parts) * a.v_heads : part * a.k_heads;
-  const int g1 = min(g0 + (is_v ? a.v_heads : a.k_heads), v.kv_heads);
+  const int g0 = part * each, g1 = min(g0 + each, v.kv_heads);
 
   // ---- which page: the slot-th that the sequence's rows go to, if it has so many
   int b = index_of_unit, slot = 0;
@@ -85,7 +87,7 @@ __global__ void __launch_bounds__(TH, TH == 128 ? 4 : (sizeof(T) == 4 ? 2 : 3)) 
     b = kv8_last_sequence(v, [&](int i) { return first_append_unit(v, i) <= index_of_unit; });
     slot = index_of_unit - first_append_unit(v, b);
     // every length and range is looked at, also one that no unit is found by
-    if (part == 0 && index_of_unit < v.num_seqs && threadIdx.x == 0) kv8_len(v, index_of_unit), kv8_rows(v, index_of_unit);
+    if (!is_v && part == 0 && index_of_unit < v.num_seqs && threadIdx.x == 0) kv8_len(v, index_of_unit), kv8_rows(v, index_of_unit);
   }
   const int len = kv8_len(v, b);
   const Kv8Span span = kv8_rows(v, b);
@@ -266,7 +268,8 @@ cudaError_t append_shape(AppendArgs& a, cudaStream_t s) {
   a.kept = held <= 64 * 1024;
   a.v_heads = heads_a_cta(pages, v.kv_heads, 12);
   a.k_heads = a.staged ? heads_a_cta(pages, v.kv_heads, K_CTAS) : a.v_heads;
-  a.append_ctas = (unsigned)(pages * ((v.kv_heads + a.k_heads - 1) / a.k_heads + (v.kv_heads + a.v_heads - 1) / a.v_heads));
+  a.k_ctas = (unsigned)(pages * ((v.kv_heads + a.k_heads - 1) / a.k_heads));
+  a.append_ctas = a.k_ctas + (unsigned)(pages * ((v.kv_heads + a.v_heads - 1) / a.v_heads));
   constexpr int GROUPS = TH / (D / 8);
   long long q_ctas = 0;
   if (a.q.heads > 0) {
@@ -300,7 +303,7 @@ cudaError_t append_typed(AppendArgs& a, cudaStream_t s) {
 
 cudaError_t launch_rope_kv8_append(const Kv8View& v, const RopeView& r, int type, const void* k, const void* vv,
                                    long long ld, const float* k_norm, float eps, const RopeRows& q, cudaStream_t s) {
-  AppendArgs a{v, r, k, vv, ld, k_norm, eps, 0, 0, 0, 0, 0, q};
+  AppendArgs a{v, r, k, vv, ld, k_norm, eps, 0, 0, 0, 0, 0, 0, q};
   if (type == APR_T_F32) return append_typed<float>(a, s);
   if (type == APR_T_F16) return append_typed<__half>(a, s);
   return append_typed<__nv_bfloat16>(a, s);
