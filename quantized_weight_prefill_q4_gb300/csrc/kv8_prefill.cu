@@ -552,7 +552,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
       // (co, cm: what O and the mean count for)
       float co, cm;
       auto join = [&] {
-        const float top_ref = fmaxf(ref, mean_ref);
+        // (a side without weights has no say: a row that sees nothing of a cut has a reference of 0 there, however low its scores were)
+        const float top_ref = sum == 0.f ? mean_ref : (mean_sum == 0.f ? ref : fmaxf(ref, mean_ref));
         const float wn = sum == 0.f ? 0.f : exp2f(ref - top_ref), wm = mean_sum == 0.f ? 0.f : exp2f(mean_ref - top_ref);
         const float all = sum * wn + mean_sum * wm, inv = all == 0.f ? 0.f : 1.f / all;
         co = R * 0x1p-7f * (wn * inv), cm = wm * mean_sum * inv;

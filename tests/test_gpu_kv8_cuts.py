@@ -1,0 +1,64 @@
+"""GPU parity of the attention of chunks (include/apr_kv8.h) where a CTA's part of a segment is cut: 16-bit rows' sums are
+taken over every 65536 positions.
+
+A table names one page over and over, so the oracle is the attention of that page whose positions count as often as they
+are named. Tolerances are those of tests/test_gpu_kv8_prefill.py for such tables: a score off by at most d 2^-24 R, 2^-17 more for the
+exponentials and additions, both in a mean of values up to vmax; a weight rounded to fp16 (2^-11), what 65536 / 16 additions
+lose (2^-12), 2^-22 for each time that sums are taken over or pieces combined; half a step of the output's type.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_kv8 import TYPES, Case, as_f32, rows_tensor
+
+pytestmark = pytest.mark.gpu
+
+CUT = 65536
+
+
+def sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def check_named_page(q, c, x, length, type_):
+    """The chunk attention of rows x, the last ones of `length` positions that are all of c's first page, time after time."""
+    n, tokens, heads, dim = len(x), c.tokens, c.heads, c.dim
+    page = int(c.table[0, 0])
+    x = rows_tensor(x, TYPES[type_])
+    out = torch.full_like(x, float("nan"))
+    table = torch.full((1, -(-length // tokens)), page, dtype=torch.int32, device="cuda")
+    lens, start = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([length], [0, n]))
+    q.apr_kv8_prefill_attention(c.cache, table, lens, x, out, heads, row_start=start)
+    q.apr_stream_status()
+    k, v = (c.host[w][page].astype(np.float64) * c.host[s][page][:, None, None] for w, s in (("K", "k_scale"), ("V", "v_scale")))
+    rows = as_f32(x).astype(np.float64).reshape(n, heads, dim)
+    score = np.einsum("ngd,gjd->ngj", rows, k) / np.sqrt(dim)
+    reach = np.einsum("ngd,gjd->ngj", np.abs(rows), np.abs(k)).max(-1) / np.sqrt(dim)
+    sees = length - n + 1 + np.arange(n)
+    count = (sees[:, None] - np.arange(tokens) + tokens - 1) // tokens
+    p = np.exp(score - score.max(-1, keepdims=True)) * count[:, None, :]
+    p /= p.sum(-1, keepdims=True)
+    want, size, vmax = np.einsum("ngj,gjd->ngd", p, v), np.einsum("ngj,gjd->ngd", p, np.abs(v)), np.abs(v).max()
+    tol = (2 * dim * 2.0 ** -24 * reach + 2.0 ** -17)[..., None] * 2 * vmax + torch.finfo(TYPES[type_]).eps / 2 * np.abs(want)
+    tol += ((length / CUT + 4) * 2.0 ** -22 + 2.0 ** -11 + 2.0 ** -12) * size + tokens * 2.0 ** -30 * vmax
+    y = as_f32(out).astype(np.float64).reshape(want.shape)
+    worst = float((np.abs(y - want) / tol).max())  # (NaN where an output is)
+    assert worst <= 1, worst
+
+
+@pytest.mark.parametrize("score", [-100.0, -200.0, -90.0, 100.0])
+@pytest.mark.parametrize("dim,type_", [(64, "f16"), (128, "bf16"), (256, "bf16")])
+def test_rows_that_see_nothing_of_the_last_cut(q, dim, type_, score):
+    # a segment for each CTA, whose first rows end before a multiple of 65536 and whose last ones behind it: what the former
+    # summed up stays, however low their scores are
+    heads, n = sms(), 5
+    c = Case([256], heads, dim, 256, seed=41)
+    c.host["K"][..., 0], c.host["V"][:] = 100, np.abs(c.host["V"])
+    c.host["k_scale"][:] = 0.03
+    c.on_gpu(q)
+    x = c.rng.normal(size=(n, heads, dim))
+    x[..., 0] = score * np.sqrt(dim) / 3.0
+    for length in (CUT + 2, 2 * CUT + 1):
+        check_named_page(q, c, x.reshape(n, -1), length, type_)
