@@ -62,3 +62,13 @@ def test_rows_that_see_nothing_of_the_last_cut(q, dim, type_, score):
     x[..., 0] = score * np.sqrt(dim) / 3.0
     for length in (CUT + 2, 2 * CUT + 1):
         check_named_page(q, c, x.reshape(n, -1), length, type_)
+
+
+@pytest.mark.parametrize("part,length", [((5, 13), 2 ** 19 + 77), ((2, 3), 2 ** 18 + 1), ((1, 3), 2 ** 19 + 200)])
+@pytest.mark.parametrize("dim,type_,n", [(64, "bf16", 1), (128, "f16", 150), (256, "bf16", 140), (128, "bf16", 2)])
+def test_cut_parts_of_shared_segments(q, dim, type_, n, part, length):
+    # fewer heads than SMs, so that a CTA's share begins, ends or lies within a segment, and is longer than two cuts
+    heads = sms() * part[0] // part[1] + 1
+    assert heads * length // sms() > 2 * CUT
+    c = Case([256], heads, dim, 256, seed=42).on_gpu(q)
+    check_named_page(q, c, c.rng.normal(size=(n, heads * dim)), length, type_)
