@@ -22,9 +22,11 @@
  *
  * With a norm (a weight for each dim of a head) the values are first
  *   f32(f32(x r) * weight),   r = f32(1 / sqrt(mean of x^2 over the head + eps)),
- * the mean and root to more than 40 bits (magnitudes up to 2^60; a head with a
- * NaN or an infinity in it becomes NaN). So the result is the same on every path,
- * whatever order a sum is taken in, but for one r in some 10^5.
+ * the mean and root to more than 40 bits, whatever the values' magnitude and
+ * eps (r itself has float32's range: a head of a root mean square of 2^126 or less. A
+ * head with a NaN or an infinity in it, or of zeros without an eps, becomes NaN). So
+ * the result is the same on every path, whatever order a sum is taken in, but for
+ * one r in some 10^5. Heads of a mean and eps beyond 2^+-100 take longer.
  *
  * Positions and axes are device arrays, read when the kernels run: an axis not
  * below num_axes counts as axis 0, a position that the table does not have as

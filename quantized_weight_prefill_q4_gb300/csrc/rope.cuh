@@ -115,10 +115,12 @@ __device__ __forceinline__ Two two_add(const Two& a, const Two& b) {
   const Two s = two_sum(a.hi, b.hi);
   return Two{s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo))};
 }
-// The sum of a unit's squares; two at a time, each half with its own sum and what rounding took: exactly, also where
+// The sum of a unit's squares, of `by` times its values; two at a time, each half with its own sum and what rounding took: exactly, also where
 // the compiler makes a square and a sum one fma. (Squares of 16-bit numbers are exact.)
 template <bool EXACT>
-__device__ __forceinline__ Two squares_of(const float (&x)[8]) {
+__device__ __forceinline__ Two squares_of(float (&x)[8], float by) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] *= by;
   float2 sum = __fmul2_rn(make_float2(x[0], x[1]), make_float2(x[0], x[1])), low = make_float2(0.f, 0.f);
   if (!EXACT) low = __ffma2_rn(make_float2(x[0], x[1]), make_float2(x[0], x[1]), make_float2(-sum.x, -sum.y));
 #pragma unroll
@@ -132,33 +134,105 @@ __device__ __forceinline__ Two squares_of(const float (&x)[8]) {
   }
   return two_add(Two{sum.x, low.x}, Two{sum.y, low.y});
 }
-// f32(1 / sqrt(sum / n + eps)), inv_n = f32(1 / n): the quotient's residual by fma; one step of Newton's from the approximation's 22
-// bits, its residual by fma.
-__device__ __forceinline__ float rope_inverse_rms(const Two& sum, float n, float inv_n, float eps) {
+// f32(1 / sqrt(mean)), mean = sum / n + eps, inv_n = f32(1 / n): the quotient's residual by fma; one step of Newton's from the
+// approximation's 22 bits, its residual by fma. Where `mean` is within 2^+-100; elsewhere squares, sums or residuals leave float32.
+__device__ __forceinline__ float rope_inverse_rms(const Two& sum, float n, float inv_n, float eps, float& mean) {
   const float q = __fmul_rn(sum.hi, inv_n);
   const Two m = two_add(two_sum(q, __fmul_rn(__fadd_rn(__fmaf_rn(-q, n, sum.hi), sum.lo), inv_n)), Two{eps, 0.f});
   const float s = __fadd_rn(m.hi, m.lo), low = __fadd_rn(__fsub_rn(m.hi, s), m.lo);
   const float y = rsqrtf(s), p = __fmul_rn(y, y), e = __fmaf_rn(y, y, -p);
   const float t = __fmaf_rn(-s, e, __fmaf_rn(-s, p, 1.f)) - low * p;
+  mean = s;
   return __fmaf_rn(__fmul_rn(y, 0.5f), t, y);
 }
-// rope_inverse_rms of four heads, each lane of a group of LANES with a part of each one's sum of squares: two
+// What a lane has of a head: EACH units, zeros where it has none.
+template <typename T, int EACH>
+struct HeadPart {
+  Vec8<T> v[EACH];
+};
+// The sum of squares of `by` times a part's values.
+template <typename T, int EACH>
+__device__ __forceinline__ Two squares_of(const HeadPart<T, EACH>& x, float by) {
+  Two sum;
+#pragma unroll
+  for (int e = 0; e < EACH; ++e) {
+    float y[8];
+    values8(x.v[e], y);
+    const Two z = squares_of<sizeof(T) == 2>(y, by);
+    sum = e ? two_add(sum, z) : z;
+  }
+  return sum;
+}
+__device__ __forceinline__ Two shfl_xor(const Two& x, int o) {
+  return Two{__shfl_xor_sync(0xffffffffu, x.hi, o), __shfl_xor_sync(0xffffffffu, x.lo, o)};
+}
+// The inverse root of a head whose mean is out of rope_inverse_rms's range: of the head divided by a power of two, next
+// to its largest magnitude or to eps's root. (Not inlined: its registers would be the callers' everywhere.)
+template <int LANES, typename T, int EACH>
+static __device__ __noinline__ float rope_inverse_rms_scaled(HeadPart<T, EACH> x, float n, float inv_n, float eps) {
+  float top = 0.f;
+#pragma unroll
+  for (int e = 0; e < EACH; ++e) {
+    float y[8];
+    values8(x.v[e], y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(y[i]));
+  }
+#pragma unroll
+  for (int o = 1; o < LANES; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const int of_top = (int)(__float_as_uint(top) >> 23) - 127;
+  const int of_eps = eps > 0.f ? ((int)(__float_as_uint(eps) >> 23) - 126) >> 1 : -126;
+  const float down = __uint_as_float((uint32_t)(127 - min(max(max(of_top, of_eps), -126), 126)) << 23);
+  Two sum = squares_of(x, down);
+#pragma unroll
+  for (int o = 1; o < LANES; o *= 2) sum = two_add(sum, shfl_xor(sum, o));
+  float mean;
+  return rope_inverse_rms(sum, n, inv_n, eps * down * down, mean) * down;
+}
+__device__ __forceinline__ bool rope_out_of_range(float mean) { return !(mean >= 0x1p-100f && mean <= 0x1p100f); }
+// The inverse root of one head, of any magnitude, each lane of a group of LANES with a part of it.
+template <int LANES, typename T, int EACH>
+__device__ __forceinline__ float rope_inverse_rms_of(const HeadPart<T, EACH>& x, float n, float inv_n, float eps) {
+  Two sum = squares_of(x, 1.f);
+#pragma unroll
+  for (int o = 1; o < LANES; o *= 2) sum = two_add(sum, shfl_xor(sum, o));
+  float mean;
+  const float r = rope_inverse_rms(sum, n, inv_n, eps, mean), scaled = rope_inverse_rms_scaled<LANES>(x, n, inv_n, eps);
+  return rope_out_of_range(mean) ? scaled : r;
+}
+// rope_inverse_rms of four heads, each lane of a group of LANES with a part of each one: two
 // steps hand half of the heads to the neighbour, so that each lane goes on with one head and takes one root
-// (5 sums of two numbers instead of 16 for 16 lanes).
-template <int LANES>
-__device__ __forceinline__ void rope_inverse_rms4(const Two (&s)[4], float n, float inv_n, float eps, float (&inv)[4]) {
+// (5 sums of two numbers instead of 16 for 16 lanes). All lanes of the warp call it. Whether the lane's own head is out of range.
+template <int LANES, typename T, int EACH>
+__device__ __forceinline__ bool rope_inverse_rms4(const HeadPart<T, EACH> (&x)[4], float n, float inv_n, float eps,
+                                                  float (&inv)[4]) {
   const int lane = threadIdx.x & 31;
   const bool b0 = lane & 1, b1 = lane & 2;
-  auto take = [](const Two& mine, const Two& other, int o) {
-    return two_add(mine, Two{__shfl_xor_sync(0xffffffffu, other.hi, o), __shfl_xor_sync(0xffffffffu, other.lo, o)});
-  };
-  const Two x = take(b0 ? s[2] : s[0], b0 ? s[0] : s[2], 1), y = take(b0 ? s[3] : s[1], b0 ? s[1] : s[3], 1);
-  Two z = take(b1 ? y : x, b1 ? x : y, 2);
+  Two s[4];
 #pragma unroll
-  for (int o = 4; o < LANES; o *= 2) z = take(z, z, o);
-  const float r = rope_inverse_rms(z, n, inv_n, eps);
+  for (int h = 0; h < 4; ++h) s[h] = squares_of(x[h], 1.f);
+  const Two u = two_add(b0 ? s[2] : s[0], shfl_xor(b0 ? s[0] : s[2], 1)), w = two_add(b0 ? s[3] : s[1], shfl_xor(b0 ? s[1] : s[3], 1));
+  Two z = two_add(b1 ? w : u, shfl_xor(b1 ? u : w, 2));
+#pragma unroll
+  for (int o = 4; o < LANES; o *= 2) z = two_add(z, shfl_xor(z, o));
+  float mean;
+  const float r = rope_inverse_rms(z, n, inv_n, eps, mean);
+  const bool far = rope_out_of_range(mean);
 #pragma unroll
   for (int h = 0; h < 4; ++h) inv[h] = __shfl_sync(0xffffffffu, r, (lane & ~3) | h >> 1 | (h & 1) << 1);
+  return far;
+}
+// The same, and those heads that are out of its range again.
+template <int LANES, typename T, int EACH>
+__device__ __forceinline__ void rope_inverse_rms4_of_any(const HeadPart<T, EACH> (&x)[4], float n, float inv_n, float eps, float (&inv)[4]) {
+  const bool far = rope_inverse_rms4<LANES>(x, n, inv_n, eps, inv);
+  if (!__any_sync(0xffffffffu, far)) return;
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    const bool mine = __shfl_sync(0xffffffffu, far, (threadIdx.x & 28) | h >> 1 | (h & 1) << 1);
+    const float again = rope_inverse_rms_scaled<LANES>(x[h], n, inv_n, eps);
+    if (mine) inv[h] = again;
+  }
 }
 
 // ---------------------------------------------------------------- elements
@@ -187,6 +261,13 @@ __device__ __forceinline__ Vec8<T> vec8_of(const float (&x)[8]) {
     return Vec8<T>{make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]))};
 }
 
+// What stands for a head that is not there: one whose norm takes no second look.
+template <typename T>
+__device__ __forceinline__ Vec8<T> ones8() {
+  const float x[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+  return vec8_of<T>(x);
+}
+
 // Norm and rotation of a unit's values, w its norm weights.
 __device__ __forceinline__ void rope_norm(float (&x)[8], float inv, const float (&w)[8]) {
 #pragma unroll
@@ -207,6 +288,43 @@ inline int rope_heads_a_group(long long rows, int heads, long long want) {
 // The row of group `group`, which may be past the last one.
 __device__ __forceinline__ long long rope_row_of(const RopeRows& a, long long group) {
   return group / ((a.heads + a.heads_a_group - 1) / a.heads_a_group);
+}
+// The heads of rope_rows_group from its i-th on, one after the other and of any magnitude. (Not inlined: its registers
+// would be rope_rows_group's: 16390 rows of 32 heads of 128 64 us instead of 61, 59.9 without any of this.)
+template <typename T, int LANES, int EACH>
+static __device__ __noinline__ void rope_rows_rest(const RopeView& r, const RopeRows& a, int row, int own, int lane, int h0, int h1, int i) {
+  RopeUnit unit[EACH];
+  RopeTurn turn[EACH];
+  float w[EACH][8];
+  bool mine[EACH];
+#pragma unroll
+  for (int e = 0; e < EACH; ++e) {
+    mine[e] = (lane + e * LANES) * 8 < a.dim && h0 < h1;
+    unit[e] = rope_unit(r, mine[e] ? lane + e * LANES : 0);
+    if (mine[e]) turn[e] = rope_turn(r, unit[e], row, own);
+    const Vec8<float> v = load44(a.norm, unit[e].d0, unit[e].d1);
+    values8(v, w[e]);
+  }
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  T* out = static_cast<T*>(a.out) + row * a.ldo;
+#pragma unroll 1
+  for (; i < a.heads_a_group; ++i) {
+    const bool here = h0 + i < h1;
+    HeadPart<T, EACH> part = {};
+#pragma unroll
+    for (int e = 0; e < EACH; ++e)
+      if (mine[e] && here) part.v[e] = load44(x + (size_t)(h0 + i) * a.dim, unit[e].d0, unit[e].d1);
+    const float inv = rope_inverse_rms_of<LANES>(part, (float)a.dim, 1.f / (float)a.dim, a.eps);
+#pragma unroll
+    for (int e = 0; e < EACH; ++e)
+      if (mine[e] && here) {
+        float y[8];
+        values8(part.v[e], y);
+        rope_norm(y, inv, w[e]);
+        rope_rotate(r, unit[e], turn[e], y);
+        store44(out + (size_t)(h0 + i) * a.dim, unit[e].d0, unit[e].d1, vec8_of<T>(y));
+      }
+  }
 }
 // Group `group` of LANES lanes does heads_a_group heads of one row, EACH units a
 // lane; `lane` within the group; nothing of a row that is not `live`. All lanes of the warp call it.
@@ -244,20 +362,13 @@ __device__ __forceinline__ void rope_rows_group(const RopeView& r, const RopeRow
         if (mine[e] && h0 + i + j < h1) v[j][e] = load44(x + (size_t)(h0 + i + j) * a.dim, unit[e].d0, unit[e].d1);
     float inv[BATCH];
     if (a.norm) {
-      Two sum[BATCH];
+      HeadPart<T, EACH> part[BATCH];
 #pragma unroll
-      for (int j = 0; j < BATCH; ++j) {
-        sum[j] = Two{0.f, 0.f};
+      for (int j = 0; j < BATCH; ++j)
 #pragma unroll
-        for (int e = 0; e < EACH; ++e)
-          if (mine[e] && h0 + i + j < h1) {
-            float y[8];
-            values8(v[j][e], y);
-            const Two x = squares_of<sizeof(T) == 2>(y);
-            sum[j] = e ? two_add(sum[j], x) : x;
-          }
-      }
-      rope_inverse_rms4<LANES>(sum, (float)a.dim, inv_dim, a.eps, inv);
+        for (int e = 0; e < EACH; ++e) part[j].v[e] = h0 + i + j >= h1 ? ones8<T>() : (mine[e] ? v[j][e] : Vec8<T>{});
+      if (__any_sync(0xffffffffu, rope_inverse_rms4<LANES>(part, (float)a.dim, inv_dim, a.eps, inv)))
+        return rope_rows_rest<T, LANES, EACH>(r, a, (int)row, own, lane, h0, h1, i);
     }
 #pragma unroll
     for (int j = 0; j < BATCH; ++j)

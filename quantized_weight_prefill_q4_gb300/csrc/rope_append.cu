@@ -159,20 +159,16 @@ __global__ void __launch_bounds__(TH, TH == 128 ? 4 : (sizeof(T) == 4 ? 2 : 3)) 
   auto vectors = [&](int j, const T* from, Vec8<T> (&e)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      e[i] = Vec8<T>{};
+      e[i] = ones8<T>();
       if (is_live(j + i)) e[i] = load44(from + (long long)(j + i) * STEP * a.ld, unit.d0, unit.d1);
     }
     if (is_v) return;
     float inv[4];
     if (normed) {
-      Two sum[4];
+      HeadPart<T, 1> part[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float x[8];
-        values8(e[i], x);
-        sum[i] = squares_of<sizeof(T) == 2>(x);
-      }
-      rope_inverse_rms4<ROW>(sum, (float)D, 1.f / D, a.eps, inv);
+      for (int i = 0; i < 4; ++i) part[i].v[0] = e[i];
+      rope_inverse_rms4_of_any<ROW>(part, (float)D, 1.f / D, a.eps, inv);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
