@@ -32,8 +32,11 @@
 // float32 rows: q and the weights enter as two fp16 pieces each (22 bits), twice the
 // products.
 //
-// Weights. A pair's weights are 2^7 p v, p against a reference at most MOVE (base 2) below the
-// maximum, v the page's V scale over a power of two R that no scale so far exceeds: at most 2^15.
+// Weights. A pair's weights are 2^12 p v, p against a reference at most MOVE (base 2) below the
+// maximum, v the page's V scale over a power of two R, a quarter or more of it for the largest scale so far: 2^10 or more for the largest
+// weight, at most 2^15 for any. fp16's steps end at 2^-24, so that a weight is kept to 2^-35 of the largest (times the largest scale
+// over its own), where 2^7 and a MOVE of 8 kept 2^-30 in the same time (2048 rows over 40011 positions 859 and 861 us, 512 float32 rows over
+// 6007 121 and 123): O is seldom rescaled, with either.
 //
 // Measured (calls in a graph; bf16 products of a library run at 1928 TFLOP/s in a burst, 1745 sustained):
 //   2048 rows over 40011 positions, 32 heads over 8 of 128, bf16   854 us, 1532 TFLOP/s
@@ -59,7 +62,7 @@ constexpr int MIN_TILES = 2;     // of a CTA's share
 // Pieces that a segment is cut into at the most: more take longer to combine than they save (64 rows over 20000, 8 heads over 2
 // of 64: 36 us, 39 with 32, 75 in the 76 pieces that every SM would have one of; 32 rows over 100000 89 us, 119 with 12).
 constexpr int MOST_PIECES = 24;
-constexpr float MOVE = 8.f;
+constexpr float MOVE = 4.f;
 // A wait for the next piece, or for the last one to be over, lasts as long as a piece: 2^30 positions take
 // some 40 s. (Every wait within one is short, and one that runs out ends these, too.)
 constexpr unsigned long long PIECE_LIMIT_NS = 300000000000ull;
@@ -556,7 +559,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
         const float top_ref = sum == 0.f ? mean_ref : (mean_sum == 0.f ? ref : fmaxf(ref, mean_ref));
         const float wn = sum == 0.f ? 0.f : exp2f(ref - top_ref), wm = mean_sum == 0.f ? 0.f : exp2f(mean_ref - top_ref);
         const float all = sum * wn + mean_sum * wm, inv = all == 0.f ? 0.f : 1.f / all;
-        co = R * 0x1p-7f * (wn * inv), cm = wm * mean_sum * inv;
+        co = R * 0x1p-12f * (wn * inv), cm = wm * mean_sum * inv;
         const bool more = mean_sum != 0.f;
         mean_ref = top_ref;
         mean_sum = all;
@@ -753,7 +756,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
         // ---- the weights
 #pragma unroll
         for (int c = 0; c < S::GROUPS; ++c) {
-          const float w = vs[c] * __uint_as_float((261u << 23) - __float_as_uint(R));  // * 2^7 / R
+          const float w = vs[c] * __uint_as_float((266u << 23) - __float_as_uint(R));  // * 2^12 / R
           const float2 k2 = make_float2(ks[c], ks[c]), r2 = make_float2(-ref, -ref), w2 = make_float2(w, w);
           float2 l = make_float2(0.f, 0.f);
           uint32_t hi[16], lo[16];

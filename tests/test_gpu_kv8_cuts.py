@@ -72,3 +72,31 @@ def test_cut_parts_of_shared_segments(q, dim, type_, n, part, length):
     assert heads * length // sms() > 2 * CUT
     c = Case([256], heads, dim, 256, seed=42).on_gpu(q)
     check_named_page(q, c, c.rng.normal(size=(n, heads * dim)), length, type_)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("code", [96, 120])
+def test_small_weights_of_float32_rows(q, dim, code):
+    # the first position's weight of 1 beside 6000 of exp(-s), alike, a head a CTA: each is off by at most 2^-35 of the largest (fp16's last
+    # step for its second piece), which all have alike. What else may be off, relatively: the reference (two products of three
+    # roundings, of a score of s log2 e < 22: 2^-24 * 3 * 22 * ln 2 < 2.8e-6), exponentials 2^-22, 512 / 16 steps of the tensor cores' sums
+    # 2^-24 each (1.9e-6), 12 times that the sums are taken over 2^-22 (2.9e-6), and their total's additions (16 in the first part, 3 at each
+    # joining: 3.1e-6), 1.1e-5 in all; scores are exact (a code times a power of two, q a small number)
+    heads, length = sms(), 6000
+    c = Case([128], heads, dim, 64, seed=43)
+    first, other = (int(p) for p in c.table[0, :2])
+    c.host["K"][:], c.host["V"][:] = 0, 100
+    c.host["k_scale"][:], c.host["v_scale"][:] = 1.0, 1.0
+    c.host["K"][first, :, 0, 0], c.host["V"][first, :, 0] = code, 0
+    c.on_gpu(q)
+    x = torch.zeros((3, heads, dim), device="cuda")
+    x[..., 0] = 1.0
+    x, out = x.view(3, -1), torch.empty((3, heads * dim), device="cuda")
+    table = torch.full((1, 94), other, dtype=torch.int32, device="cuda")
+    table[0, 0] = first
+    lens, start = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([length], [0, 3]))
+    q.apr_kv8_prefill_attention(c.cache, table, lens, x, out, heads, row_start=start, scale=0.125)
+    q.apr_stream_status()
+    small = np.exp(-code / 8.0) * (length - 3 + np.arange(3))
+    worst = float(np.abs(as_f32(out) / (100 * small / (1 + small))[:, None] - 1).max())
+    assert worst <= 2.0 ** -35 * np.exp(code / 8.0) + 1.5e-5, worst
