@@ -539,14 +539,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
           }
         }
       }
-      const float factor = !(top <= FLT_MAX) ? __int_as_float(0x7fffffff)
-                                             : a.scale_log2 * __uint_as_float((uint32_t)(127 + q_exponent(top)) << 23);
+      const int sees = live ? min(p.len, p.first + i + 1) : 0;  // positions
+      // (of a row that sees none, as in a slot without a sequence, whatever it holds: its outputs are zeros)
+      const float factor = !(top <= FLT_MAX) && sees > 0 ? __int_as_float(0x7fffffff)
+                                                         : a.scale_log2 * __uint_as_float((uint32_t)(127 + q_exponent(top)) << 23);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[m]);
       ++mine_so_far;
 
-      const int sees = live ? min(p.len, p.first + i + 1) : 0;  // positions
       float ref = -INFINITY, run_max = -INFINITY, sum = 0.f;
       float R = 0x1p-100f;  // a power of two
       float mean_ref = -INFINITY, mean_sum = 0.f;  // of the mean taken over

@@ -1,5 +1,5 @@
 """GPU parity of the attention of chunks (include/apr_kv8.h) where a CTA's part of a segment is cut: 16-bit rows' sums are
-taken over every 65536 positions.
+taken over every 65536 positions; its small weights, and rows that see nothing.
 
 A table names one page over and over, so the oracle is the attention of that page whose positions count as often as they
 are named. Tolerances are those of tests/test_gpu_kv8_prefill.py for such tables: a score off by at most d 2^-24 R, 2^-17 more for the
@@ -100,3 +100,22 @@ def test_small_weights_of_float32_rows(q, dim, code):
     small = np.exp(-code / 8.0) * (length - 3 + np.arange(3))
     worst = float(np.abs(as_f32(out) / (100 * small / (1 + small))[:, None] - 1).max())
     assert worst <= 2.0 ** -35 * np.exp(code / 8.0) + 1.5e-5, worst
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("type_", ["f32", "f16", "bf16"])
+def test_rows_that_see_nothing_give_zeros_whatever_they_hold(q, dim, type_):
+    # a slot without a sequence, and rows before a sequence's start: zeros, as from the attention of few rows, where a row that
+    # sees a position becomes NaN
+    c = Case([0, 3, 40], 2, dim, 32, seed=44).on_gpu(q)
+    x = torch.from_numpy(c.rng.normal(size=(11, 4 * dim))).cuda().to(TYPES[type_])
+    x[:6, 7], x[:6, dim + 9], x[:6, 3 * dim] = float("nan"), float("inf"), -float("inf")
+    out, few = torch.full_like(x, 7.0), torch.full_like(x, 7.0)
+    start = torch.tensor([0, 1, 8, 11], dtype=torch.int32, device="cuda")  # seven rows of a sequence of three tokens
+    for call, y in ((q.apr_kv8_prefill_attention, out), (q.apr_kv8_attention, few)):
+        call(c.cache, c.gtable, c.glens, x, y, 4, row_start=start)
+    q.apr_stream_status()
+    nan = torch.zeros((11, 4), dtype=torch.bool, device="cuda")
+    nan[5, [0, 1, 3]] = True
+    for y in (out, few):
+        assert not y[:5].any() and torch.equal(torch.isnan(y.view(11, 4, dim)).all(-1), nan) and torch.equal(torch.isnan(y.view(11, 4, dim)).any(-1), nan)
