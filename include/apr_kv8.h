@@ -165,7 +165,7 @@ int apr_kv8_attention(const apr_kv8_cache* cache, const apr_kv8_rows* rows, int 
  *   fp16, bf16    q enters as one fp16 row (scaled by a power of two: all bits
  *                 of values within 2^-14 of the row's largest), the softmax weights rounded
  *                 to fp16
- * Beside that a weight is off by at most 2^-35 of the row's largest, times the
+ * Beside that a weight is off by at most 2^-34 of the row's largest, times the
  * largest V scale of the sequence so far over its own position's.
  * out must not overlap q or the cache. Scratch per stream: partial results of
  * what several CTAs share, and means (64 MB).

@@ -32,11 +32,11 @@
 // float32 rows: q and the weights enter as two fp16 pieces each (22 bits), twice the
 // products.
 //
-// Weights. A pair's weights are 2^12 p v, p against a reference at most MOVE (base 2) below the
-// maximum, v the page's V scale over a power of two R, a quarter or more of it for the largest scale so far: 2^10 or more for the largest
-// weight, at most 2^15 for any. fp16's steps end at 2^-24, so that a weight is kept to 2^-35 of the largest (times the largest scale
-// over its own), where 2^7 and a MOVE of 8 kept 2^-30 in the same time (2048 rows over 40011 positions 859 and 861 us, 512 float32 rows over
-// 6007 121 and 123): O is seldom rescaled, with either.
+// Weights. A pair's weights are 2^11 p v, p against a reference at most MOVE (base 2) below the
+// maximum, v the page's V scale over a power of two R that no scale so far exceeds, a quarter or more for the largest: at most 2^15, and
+// 2^9 or more for the largest one. fp16's steps end at 2^-24, so that a weight is kept to 2^-34 of the largest (times the largest
+// scale over its own); 2^7 and a MOVE of 8 kept 2^-30. O is rescaled a little more often (2048 rows over 40011 positions 856 us, 853 with
+// 8; seven sequences of 900 to 9000 242 and 238).
 //
 // Measured (calls in a graph; bf16 products of a library run at 1928 TFLOP/s in a burst, 1745 sustained):
 //   2048 rows over 40011 positions, 32 heads over 8 of 128, bf16   854 us, 1532 TFLOP/s
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
         const float top_ref = sum == 0.f ? mean_ref : (mean_sum == 0.f ? ref : fmaxf(ref, mean_ref));
         const float wn = sum == 0.f ? 0.f : exp2f(ref - top_ref), wm = mean_sum == 0.f ? 0.f : exp2f(mean_ref - top_ref);
         const float all = sum * wn + mean_sum * wm, inv = all == 0.f ? 0.f : 1.f / all;
-        co = R * 0x1p-12f * (wn * inv), cm = wm * mean_sum * inv;
+        co = R * 0x1p-11f * (wn * inv), cm = wm * mean_sum * inv;
         const bool more = mean_sum != 0.f;
         mean_ref = top_ref;
         mean_sum = all;
@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_prefill_kernel(const __grid_co
         // ---- the weights
 #pragma unroll
         for (int c = 0; c < S::GROUPS; ++c) {
-          const float w = vs[c] * __uint_as_float((266u << 23) - __float_as_uint(R));  // * 2^12 / R
+          const float w = vs[c] * __uint_as_float((265u << 23) - __float_as_uint(R));  // * 2^11 / R
           const float2 k2 = make_float2(ks[c], ks[c]), r2 = make_float2(-ref, -ref), w2 = make_float2(w, w);
           float2 l = make_float2(0.f, 0.f);
           uint32_t hi[16], lo[16];
