@@ -63,7 +63,7 @@ typedef struct apr_rope {
  * scale). Angles of far positions lose nothing.
  *   inv_freq  [pairs] float32, magnitudes up to 2^10; pairs 1 .. 256
  *   first     >= 0, first + positions <= 2^30; positions * pairs <= 2^32
- *   scale     magnitudes up to 2^100 (the factor that some stretched rotations have; 1 otherwise)
+ *   scale     0, or magnitudes of 2^-100 to 2^100 (the factor that some stretched rotations have; 1 otherwise)
  * positions == 0 is a no-op.
  */
 int apr_rope_table(const float* inv_freq, int pairs, long long first, long long positions, double scale,

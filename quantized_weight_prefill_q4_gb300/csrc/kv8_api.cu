@@ -352,7 +352,9 @@ int run_rope_table(const float* inv_freq, int pairs, long long first, long long 
   if (pairs < 1 || pairs > 256) return failf(APR_E_INVAL, "pairs=%lld must be within 1 and 256", pairs);
   if (first < 0 || positions < 0 || first > (1LL << 30) || positions > (1LL << 30) - first || positions * pairs > (1LL << 32))
     return failf(APR_E_INVAL, "positions %lld and %lld more are beyond 2^30, or 2^32 values", first, positions);
-  if (!(std::fabs(scale) <= 0x1p100)) return set_error(APR_E_INVAL, "scale must be finite, and at most 2^100");
+  // (what rounding took, 2^-48 of a value, is turned on with it: below 2^-100 it leaves float32's range)
+  if (!(std::fabs(scale) <= 0x1p100) || (scale != 0. && std::fabs(scale) < 0x1p-100))
+    return set_error(APR_E_INVAL, "scale must be 0 or of a magnitude within 2^-100 and 2^100");
   if (positions == 0) return APR_OK;
   if (!inv_freq || !table) return set_error(APR_E_INVAL, "null inv_freq or table");
   if (!on16(table) || !on4(inv_freq)) return set_error(APR_E_ALIGN, "the table is not 16-byte, or inv_freq not 4-byte aligned");

@@ -1,4 +1,5 @@
-"""GPU parity of the norm of heads (include/apr_rope.h) over the whole range of magnitudes and of eps, against its oracle.
+"""GPU parity of the norm of heads (include/apr_rope.h) over the whole range of magnitudes and of eps, and of the table over that of
+its scale, against their oracle.
 
 r = f32(1 / sqrt(mean of x^2 + eps)) is taken to more than 40 bits before its rounding at every magnitude, so a result is the oracle's
 but for one head in 2^16 or so: assert_rows of tests/test_gpu_rope.py, with the 3 heads that it allows.
@@ -76,3 +77,14 @@ def test_zeros_and_not_numbers_beside_heads_of_any_magnitude(q):
     y, keep = out.view(9, dim), [0, 1, 3, 5, 6, 8]
     assert bool(torch.isnan(y[[2, 4, 7]]).all())
     assert_rows(y[keep].reshape(1, -1), oracle.rope_rows(table, None, False, [[4]], x.reshape(9, dim)[keep].reshape(1, -1), 6, w, 0.0), "f32", 6, True)
+
+
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -100, -(2.0 ** -99), 2.0 ** 100])
+def test_tables_at_the_ends_of_the_scales_range(q, scale):
+    # half a step of float32, 2^-24 of a normal value and 2^-150 of a smaller one, and 2^-40 times the scale
+    inv = (1.0 / 10000.0 ** (np.arange(36) / 36)).astype(np.float32)
+    table = torch.full((1500, 36, 2), float("nan"), device="cuda")
+    q.apr_rope_table(torch.from_numpy(inv).cuda(), table, first=5000, scale=scale)
+    q.apr_stream_status()
+    want = oracle.rope_table(inv, 5000, 1500, scale)
+    assert (np.abs(table.cpu().numpy().astype(np.float64) - want) <= 2.0 ** -24 * np.abs(want) + 2.0 ** -150 + 2.0 ** -40 * abs(scale)).all()

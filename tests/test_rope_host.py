@@ -164,6 +164,12 @@ def test_bad_tables_are_refused(q, code, needle, change):
     assert needle in q.apr_last_error()
 
 
+@pytest.mark.parametrize("scale", [2.0 ** -101, -(2.0 ** -101), 1e-300, 5e-324])
+def test_tables_of_scales_whose_roundings_float32_does_not_hold_are_refused(q, scale):
+    assert q.library().apr_rope_table(8 * A, 64, 0, 100, scale, 9 * A, None) == INVAL
+    assert "scale" in q.apr_last_error()
+
+
 # rope, type, k, v, ld, k_norm, q, ldq, q_out, ldqo, heads, q_norm, eps, stream
 def append(**change):
     return (rope(**change), 0, 8 * A, 9 * A, 256, None, 10 * A, 1024, 11 * A, 1024, 8, None, 0.0, None)
