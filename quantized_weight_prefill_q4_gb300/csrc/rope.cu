@@ -108,9 +108,11 @@ __global__ void __launch_bounds__(TB_THREADS) rope_table_kernel(const float* __r
 }
 
 // ---------------------------------------------------------------- rows
-// A row read and written once, its turns read once for all its heads: bound by memory, and where there is a norm by
-// instructions, as every step is rounded by itself and a mean of squares has 45 bits (rope.cuh). 16390 normed bf16 rows of 32 heads
-// of 128 on three axes take 59 us, 0.70 of the HBM rate with 61 % of the issue slots taken; 5329 fp16 rows of 16 heads of 72 9 us; one row 2.5 us.
+// A row read and written once, its turns read once for all its heads: bound by memory. Where there is a norm, by its latency: a warp
+// loads its next heads when the last ones are stored, at 24 warps an SM (78 registers: every step is rounded by itself and a mean of squares has
+// 45 bits, rope.cuh). 16390 normed bf16 rows of 32 heads of 128 on three axes take 61 us, 0.68 of the HBM rate with 62 % of the issue
+// slots taken, loads the largest stall; 8192 float32 rows of 16 heads of 256 51 us, 0.79; 5329 fp16 rows of 16 heads of 72 9.4 us (9 of 16
+// lanes have a unit); one row 3 us.
 constexpr int RR_THREADS = 256;
 
 template <typename T, int LANES, int EACH>

@@ -8,10 +8,12 @@
 // rounded to the rows' type, the bits that apr_rope_rows would have written. The CTAs behind them
 // rotate the q rows.
 //
-// Bound by instructions (61 % of the issue slots): the norm, the rotation and two passes over a head's rows, between which lie the
-// largest magnitude and a barrier. 13157 bf16 rows of 8 normed heads of 128 on three axes take 50 us (61 with K's
-// CTAs among V's, whose last ones ended late), 86 with 32 heads of q (156 before a page's turns were looked up once and a head's rows kept);
-// 50001 fp16 rows of 8 heads of 64 61 us, 90 with 16 of q; 64 rows 4.7 and 5.7 us.
+// Bound by latency at 24 warps an SM: a head is loaded, normed and rotated, its largest magnitude found across a barrier, and quantised
+// before the next head's loads begin (63 % of the issue slots taken, HBM at 0.4 of its rate, loads the largest stall). 13157 bf16 rows of 8
+// normed heads of 128 on three axes take 49 us (61 with K's CTAs among V's, whose last ones ended late), 89 with 32 heads of q (156 before a page's
+// turns were looked up once and a head's rows kept); 50001 fp16 rows of 8 heads of 64 63 us, 92 with 16 of q; 64 rows 5.0 and 6.6 us; 8192
+// float32 rows of 4 normed heads of 256 28 us in pages of 64 (33 if they are not kept, below), 33 in pages of 128, 48 in pages of 256; with 16
+// heads of q 79, 83 and 83.
 
 #include "apr_internal.h"
 #include "host_common.h"
@@ -21,8 +23,8 @@
 namespace apr {
 namespace {
 
-// K's CTAs of an SM that the heads are divided for, where each looks its page's turns up first (13157 rows with q 86 us, 92 with 12;
-// without q 50, 41 with 8).
+// K's CTAs of an SM that the heads are divided for, where each looks its page's turns up first (13157 rows with q 89 us, 90 with 8, 92 with
+// 12; without q 49, 42 with 8; but 8192 float32 rows of 8 heads of 128 without q 48, 58 with 8, and with 32 heads of q 128 and 138).
 constexpr int K_CTAS = 5;
 
 struct AppendArgs {
@@ -37,7 +39,7 @@ struct AppendArgs {
   unsigned k_ctas;       // the first ones: they take longest
   unsigned append_ctas;  // with V's; the CTAs behind them are q's
   int staged;            // bytes of a page's cosines and sines, where they are looked up once for all heads
-  int kept;              // a head's rows fit shared memory
+  int kept;              // a head's rows fit shared memory, and are not loaded, normed and rotated twice
   RopeRows q;            // heads 0: none
 };
 
@@ -261,6 +263,9 @@ cudaError_t append_shape(AppendArgs& a, cudaStream_t s) {
   const size_t rows = v.max_rows < 1 << v.page_shift ? v.max_rows : 1 << v.page_shift;
   const size_t turns = rows * a.r.pairs * 8, held = rows * D * sizeof(T);
   a.staged = rows >= 16 && turns <= 64 * 1024 && v.kv_heads > 1 ? (int)turns : 0;
+  // (kept up to 64 KB, normed rows of 4 heads of 256 without q: 8192 float32 ones in pages of 64 28 us, 33 if not; bf16 ones in pages of 128
+  // 29 and 37. With q, whose CTAs have the same shared memory: 79 and 83, 70 and 63, but 128 and 86 for float32 rows of 8 + 32
+  // heads of 128 in pages of 128, whose turns take another 64 KB. Past 64 KB a CTA an SM is left: 82 us become 122, 71 become 111)
   a.kept = held <= 64 * 1024;
   a.v_heads = heads_a_cta(pages, v.kv_heads, 12);
   a.k_heads = a.staged ? heads_a_cta(pages, v.kv_heads, K_CTAS) : a.v_heads;
